@@ -21,6 +21,11 @@
  *     boolean mask indexing of the kept mask units replaced by gather and
  *     scatter.
  *
+ *   kv4_store / kv4_load / mha_fwd_kv4 / iha_premix_fwd_qkv_at
+ *     serving: a paged key-value cache held in 4 bits, the attention of new
+ *     tokens over it and the premix of tokens that continue a sequence (no
+ *     counterpart in the pages).
+ *
  * Conventions shared by every entry point:
  *   - Pointers named x, y, q, ... are DEVICE pointers owned by the caller.
  *     The library allocates nothing, keeps no pointer after return and never
@@ -102,6 +107,21 @@ iha_status iha_premix_fwd_qkv(const void* xq, const void* xk, const void* xv,
                               const float* wq, const float* wk, const float* wv,
                               void* yq, void* yk, void* yv, int B, int N, int H, int P,
                               int d, iha_dtype dt, int rope, float rope_base, void* stream);
+
+/*
+ * Premix forward of Q, K and V of tokens at given positions, for tokens that
+ * continue sequences (a decode step, a chunk of a prompt): exactly
+ * iha_premix_fwd_qkv with rope != 0, except that token (b, n) rotates at
+ * positions[b * N + n] instead of n.
+ *   positions  int32 [B, N] (device), any order; |position| < 2^24 (beyond it
+ *              the angles of the bf16 kernel lose accuracy)
+ * All other buffers, limits and kernels as iha_premix_fwd_qkv.
+ */
+iha_status iha_premix_fwd_qkv_at(const void* xq, const void* xk, const void* xv,
+                                 const float* wq, const float* wk, const float* wv,
+                                 const int32_t* positions, void* yq, void* yk, void* yv,
+                                 int B, int N, int H, int P, int d, iha_dtype dt,
+                                 float rope_base, void* stream);
 
 /*
  * Premix forward of Q, K and V with the interleaved pseudo-token layout of
@@ -278,6 +298,87 @@ iha_status mha_bwd_noalloc(const void* q, const void* k, const void* v,
                            iha_dtype dt, void* stream);
 
 /*
+ * The 4-bit key-value cache.  A cached row (one token and head of K or of V,
+ * d features) is d / 32 groups of 32 neighbouring features.  A value counts as
+ * its bf16 rounding; a group has a bf16 scale s = bf16(max |x| / 7) and codes
+ * c = round(x / s), ties to even, -7 <= c <= 7, and stands for s * c.  A group
+ * whose maximum is below 2^-100 is held as zeros; one that holds a NaN or an
+ * infinity reads back as NaN throughout.  36 bytes per 32 features of K and V
+ * together (4.5 bits a value).
+ *
+ * The cache is n_pages pages of kv4_page_bytes() bytes, dense, 16-byte
+ * aligned; a page holds `page` tokens (a multiple of 16) of all Hkv heads, K
+ * and V.  A slot is a token's place: page id * page + offset in the page.  The
+ * order of the bytes inside a page belongs to the library.  Pages need no
+ * initial value.  d is 32, 64, 96 or 128; n_pages * page < 2^31.
+ */
+size_t kv4_page_bytes(int page, int Hkv, int d);  /* 0 for sizes it cannot hold */
+
+/*
+ * Quantise rows into the cache as they are written:
+ *   cache[slots[b, n]] <- (k[b, n, :, :], v[b, n, :, :])
+ *   k, v   [B_outer, B_inner, N, Hkv, d] views, dtype dt (bf16 or f32), element
+ *          strides sk, sv (>= 0, multiples of 16 bytes; 0 repeats a row)
+ *   slots  int32 [B_outer, B_inner, N] dense; -1 is padding, its row is not
+ *          stored; any other value outside the cache is skipped and flagged
+ *          (iha_device_error)
+ * Slots that occur twice in one call race: the slot is left with a mixture.
+ * Every byte of the cache outside the named slots keeps its value.
+ */
+iha_status kv4_store(const void* k, const void* v, const int32_t* slots, void* cache,
+                     int B_outer, int B_inner, int N, int n_pages, int page, int Hkv, int d,
+                     iha_strides sk, iha_strides sv, iha_dtype dt, void* stream);
+
+/*
+ * Read rows back: (k, v)[b, n, :, :] <- cache[slots[b, n]], s * c exactly in
+ * f32 or rounded to bf16 (nearest even).  Slot -1, and a slot outside the
+ * cache (also flagged), gives a row of zeros.  A slot may occur any number of
+ * times.  Arguments as kv4_store; the strides of k and v must not repeat rows.
+ */
+iha_status kv4_load(const void* cache, const int32_t* slots, void* k, void* v, int B_outer,
+                    int B_inner, int N, int n_pages, int page, int Hkv, int d, iha_strides sk,
+                    iha_strides sv, iha_dtype dt, void* stream);
+
+/*
+ * Softmax attention of Nq new tokens of each of B sequences over the 4-bit
+ * cache: single-token decode (Nq = 1), several tokens at once (speculative
+ * tokens, the P pseudo-tokens of the interleaved layout, short chunks).
+ *   o[b, t, h] = sum_j softmax_j(scale <q[b, t, h], k_j>) v_j   over visible j,
+ * k_j, v_j the values the cache stands for at key j of sequence b, head
+ * h / (Hq / Hkv).  Sequence b has seq_lens[b] keys, the new tokens' own among
+ * them; key j is in page block_table[b, j / page].  New token t sits at position
+ * i = seq_lens[b] - Nq + t:
+ *   IHA_MASK_NONE           every key of the sequence is visible
+ *   IHA_MASK_CAUSAL         j <= i
+ *   IHA_MASK_CAUSAL_WINDOW  j <= i and i - j < window
+ * A row without visible keys (an empty sequence, i < 0) gives o = 0 and
+ * lse = -inf.  What hidden keys hold, NaN too, has no influence.
+ *   q, o         bf16 [B, Nq, Hq, d] views, element strides sq, so (b_outer,
+ *                seq, head; b_inner unused), >= 0, multiples of 8
+ *   cache        as kv4_store; block_table int32 [B, table_width] dense, only
+ *                entries of pages with visible keys are read; seq_lens int32
+ *                [B].  A page id outside the cache counts as hidden keys, a
+ *                length outside [0, table_width * page] is clamped; both are
+ *                flagged (iha_device_error).
+ *   lse_out      nullable; float32 [B, Hq, Nq] dense, natural log, with scale
+ *   workspace    device scratch of mha_fwd_kv4_workspace_bytes() bytes, 256-byte
+ *                aligned, ZERO-FILLED once before its first use; every call
+ *                leaves it ready for the next.  Calls that may run at the same
+ *                time (other streams, graphs replayed together) need a
+ *                workspace each.
+ *   scale <= 0 selects 1/sqrt(d)
+ * Hq a multiple of Hkv, d in {32, 64, 96, 128}, bf16.  No length is read on
+ * the host, so a captured call replays with new seq_lens and block_table.  The
+ * result does not depend on timing (no atomics on values).
+ */
+size_t mha_fwd_kv4_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d);
+iha_status mha_fwd_kv4(const void* q, const void* cache, const int32_t* block_table,
+                       const int32_t* seq_lens, void* o, float* lse_out, void* workspace,
+                       size_t workspace_bytes, int B, int Nq, int Hq, int Hkv, int d,
+                       int n_pages, int page, int table_width, iha_strides sq, iha_strides so,
+                       float scale, iha_mask mask_mode, int window, iha_dtype dt, void* stream);
+
+/*
  * Mask-unit gather (README item 2, x[mask] -> gather):
  *   out[b,k,t,:] = x[b, tok(keep[b,k], t), :]
  * where the grid is row-major [grid_h, grid_w], mask units are mu_h x mu_w
@@ -347,7 +448,8 @@ const char* iha_last_error(void);
  * Device error word of the current device: 0 if no kernel has flagged an
  * error, else a bitwise OR of codes (1 = out-of-range keep index, 2 = a
  * bounded internal wait gave up, 4 = a kernel found its dynamic shared memory
- * not 1024-byte aligned and did nothing).  Synchronises the device; clears the word if clear != 0.
+ * not 1024-byte aligned and did nothing, 8 = a slot, page id or length outside
+ * the 4-bit cache).  Synchronises the device; clears the word if clear != 0.
  * Returns -1 if the word cannot be read.
  */
 int iha_device_error(int clear);

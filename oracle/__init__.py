@@ -305,3 +305,69 @@ def attention_qpool(q: np.ndarray, k: np.ndarray, v: np.ndarray, q_stride: int,
     Returns O [Bo,Bi,Tq,Hh,d] float64 and lse [Bo,Bi,Hh,Tq] float64.
     """
     return attention(q_pool(q, q_stride), k, v, MASK_NONE, 0, scale)
+
+
+# ---------------------------------------------------------------- 4-bit key-value cache
+def kv4_values(x: np.ndarray) -> np.ndarray:
+    """The values (float64) that rows x[..., d] (float32 or bf16 bits) stand for
+    once held in 4 bits: x rounded to bf16, groups of 32 neighbours, scale
+    s = bf16(max |x| / 7), codes round(x / s) with ties to even; a group whose
+    maximum is below 2^-100 is zeros, one with a NaN or an infinity is NaN."""
+    xf = _as_f32(x)
+    with np.errstate(invalid="ignore", over="ignore"):
+        b = round_bf16(xf) if x.dtype != np.uint16 else xf.astype(np.float64)
+    g = b.reshape(*b.shape[:-1], b.shape[-1] // 32, 32)
+    with np.errstate(invalid="ignore"):
+        top = np.abs(g).max(axis=-1, keepdims=True)
+    good = np.isfinite(top)
+    use = good & (top >= 2.0 ** -100)
+    s = round_bf16(np.where(use, top, 7.0) / 7.0).reshape(top.shape)
+    c = np.rint(np.where(use, g, 0.0) / s)  # rint: ties to even
+    out = np.where(good, c * s, np.nan)
+    return out.reshape(b.shape)
+
+
+def kv4_attention(q: np.ndarray, k: np.ndarray, v: np.ndarray, mask: int = MASK_CAUSAL,
+                  window: int = 0, scale: float | None = None):
+    """Attention of the last Nq positions of one sequence: q [Nq, Hq, d] (float32
+    or bf16 bits), k, v [n, Hkv, d] values, query head h on key head
+    h // (Hq // Hkv); two-pass softmax in float64.  Returns O [Nq, Hq, d],
+    lse [Hq, Nq] and sum_j p_j |v_j| [Nq, Hq, d] (the scale of rounding errors)."""
+    qf = _as_f32(q).astype(np.float64)
+    Nq, Hq, d = qf.shape
+    n, Hkv, _ = k.shape
+    G = Hq // Hkv
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    o = np.zeros((Nq, Hq, d))
+    oa = np.zeros((Nq, Hq, d))
+    lse = np.full((Hq, Nq), -np.inf)
+    for t in range(Nq):
+        i = n - Nq + t
+        hi = n if mask == MASK_NONE else min(n, i + 1)
+        lo = max(0, i - window + 1) if mask == MASK_CAUSAL_WINDOW else 0
+        if hi <= lo:
+            continue
+        for h in range(Hq):
+            kk, vv = k[lo:hi, h // G], v[lo:hi, h // G]
+            x = scale * (kk @ qf[t, h])
+            m = x.max()
+            p = np.exp(x - m)
+            l = p.sum()
+            o[t, h] = (p / l) @ vv
+            oa[t, h] = (p / l) @ np.abs(vv)
+            lse[h, t] = m + math.log(l)
+    return o, lse, oa
+
+
+def premix_at(x: np.ndarray, w: np.ndarray, P: int, positions: np.ndarray,
+              rope_base: float = 10000.0) -> np.ndarray:
+    """Y[B,N,H*P,d] (float64): the premix with RoPE, token (b, n) rotated at
+    positions[b, n]."""
+    B, N, H, d = x.shape
+    y = np.empty((B, N, H * P, d), dtype=np.float64)
+    for b in range(B):
+        for n in range(N):
+            y[b, n] = premix_fwd(np.ascontiguousarray(x[b:b + 1, n:n + 1]), w, P, rope=True,
+                                 rope_base=rope_base, pos0=int(positions[b, n]))[0, 0]
+    return y

@@ -12,10 +12,15 @@ Entry points (same names as the C ABI in include/iha.h):
       Design" and "FLOP Matching"; hiera-optim MaskUnitAttentionFast.forward
   mu_gather, mu_scatter                     -- "hiera-optim 0.1.0", README,
       item 2 of what optimize(model) does
+  premix_fwd_qkv_at, kv4_store, kv4_load, mha_fwd_kv4
+                                            -- serving: the premix of tokens at
+      given positions, a paged key-value cache held in 4 bits, the attention
+      of new tokens over it
 PyTorch supplies device memory and the current stream only.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 
@@ -24,7 +29,9 @@ from . import _build
 __all__ = ["build", "lib", "premix_fwd", "premix_bwd_dx", "premix_bwd_dw", "premix_bwd", "mha_fwd",
            "mha_bwd", "mha_bwd_workspace_bytes",
            "mu_gather", "mu_scatter", "device_error", "IHAError", "Strides", "MASK_NONE",
-           "MASK_CAUSAL", "MASK_CAUSAL_WINDOW", "F32", "BF16"]
+           "MASK_CAUSAL", "MASK_CAUSAL_WINDOW", "F32", "BF16",
+           "premix_fwd_qkv_at", "kv4_page_bytes", "kv4_store", "kv4_load",
+           "mha_fwd_kv4", "mha_fwd_kv4_workspace_bytes"]
 
 IHA_OK, IHA_ERR_INVALID_ARG, IHA_ERR_UNSUPPORTED, IHA_ERR_ALIGNMENT, IHA_ERR_CUDA = range(5)
 F32, BF16 = 0, 1
@@ -34,7 +41,9 @@ SYMBOLS = ("iha_premix_fwd", "iha_premix_bwd_dx", "iha_premix_bwd_dw", "iha_prem
            "mha_fwd", "mu_gather", "mu_scatter", "iha_status_string", "iha_last_error",
            "iha_device_error", "iha_test_fail_next_wait", "mha_bwd", "mha_bwd_workspace_bytes",
            "mha_bwd_noalloc", "iha_premix_fwd_qkv", "mu_attention_fused",
-           "iha_premix_fwd_qkv_interleaved", "iha_premix_bwd_qkv", "mha_fwd_qpool")
+           "iha_premix_fwd_qkv_interleaved", "iha_premix_bwd_qkv", "mha_fwd_qpool",
+           "iha_premix_fwd_qkv_at", "kv4_page_bytes", "kv4_store", "kv4_load",
+           "mha_fwd_kv4_workspace_bytes", "mha_fwd_kv4")
 
 
 class IHAError(RuntimeError):
@@ -86,7 +95,16 @@ def lib() -> C.CDLL:
     L.iha_premix_bwd_qkv.argtypes = [vp] * 15 + [i, i, i, i, i, i, i, f, vp]
     L.mha_fwd_qpool.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, Strides, Strides, Strides,
                                 Strides, f, i, vp]
-    for name in ("iha_premix_fwd", "iha_premix_fwd_qkv", "iha_premix_fwd_qkv_interleaved",
+    L.iha_premix_fwd_qkv_at.argtypes = [vp] * 10 + [i, i, i, i, i, i, f, vp]
+    L.kv4_page_bytes.argtypes = [i, i, i]
+    L.kv4_page_bytes.restype = C.c_size_t
+    for name in ("kv4_store", "kv4_load"):
+        getattr(L, name).argtypes = [vp] * 4 + [i] * 7 + [Strides, Strides, i, vp]
+    L.mha_fwd_kv4_workspace_bytes.argtypes = [i, i, i, i, i]
+    L.mha_fwd_kv4_workspace_bytes.restype = C.c_size_t
+    L.mha_fwd_kv4.argtypes = [vp] * 7 + [C.c_size_t] + [i] * 8 + [Strides, Strides, f, i, i, i, vp]
+    for name in ("iha_premix_fwd_qkv_at", "kv4_store", "kv4_load", "mha_fwd_kv4",
+                 "iha_premix_fwd", "iha_premix_fwd_qkv", "iha_premix_fwd_qkv_interleaved",
                  "iha_premix_bwd_dx",
                  "iha_premix_bwd_dw", "iha_premix_bwd", "mha_fwd", "mha_bwd", "mu_gather",
                  "mu_scatter", "mu_attention_fused", "iha_premix_bwd_qkv", "mha_fwd_qpool"):
@@ -126,6 +144,22 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return C.c_void_p(stream.cuda_stream)
+
+
+def _stream_on(device, stream):
+    """(stream pointer, context for tensors made here) for a call on `device`,
+    which must be the current one.  Tensors that a call makes itself come from
+    the memory of the stream it runs on, so that nothing pending on another
+    stream still uses them."""
+    torch = _torch()
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return C.c_void_p(torch.cuda.current_stream(device).cuda_stream), contextlib.nullcontext
+    if stream.device != device:
+        raise ValueError(f"stream on {stream.device}, tensors on {device}")
+    return C.c_void_p(stream.cuda_stream), lambda: torch.cuda.stream(stream)
 
 
 def _dt(t) -> int:
@@ -204,6 +238,38 @@ def premix_fwd_qkv(xs, ws, P: int, rope: bool = False, rope_base: float = 10000.
     check(lib().iha_premix_fwd_qkv(*(_ptr(x) for x in xs), *(_ptr(w) for w in ws),
                                    *(_ptr(y) for y in out), B, N, H, P, d, _dt(x0), int(rope),
                                    float(rope_base), _stream(stream)), "iha_premix_fwd_qkv")
+    return tuple(out)
+
+
+def premix_fwd_qkv_at(xs, ws, P: int, positions, rope_base: float = 10000.0, out=None,
+                      stream=None):
+    """(Y_q, Y_k, Y_v) as premix_fwd_qkv with RoPE, for tokens that continue
+    sequences: token (b, n) of Q and K rotates at positions[b, n] (int32 [B, N])
+    instead of n."""
+    torch = _torch()
+    if len(xs) != 3 or len(ws) != 3:
+        raise ValueError("xs and ws must hold three tensors (q, k, v)")
+    x0 = xs[0]
+    _expect(x0, "xq")
+    if x0.dim() != 4:
+        raise ValueError("x must be [B, N, H, d]")
+    B, N, H, d = x0.shape
+    for t, (x, w) in enumerate(zip(xs, ws)):
+        _expect(x, f"x[{t}]", (B, N, H, d), x0.dtype, x0.device)
+        _expect(w, f"w[{t}]", (H, P, H), torch.float32, x0.device)
+    _expect(positions, "positions", (B, N), torch.int32, x0.device)
+    sp, ctx = _stream_on(x0.device, stream)
+    if out is None:
+        with ctx():
+            out = tuple(torch.empty((B, N, H * P, d), dtype=x0.dtype, device=x0.device)
+                        for _ in range(3))
+    if len(out) != 3:
+        raise ValueError("out must hold three tensors")
+    for t, y in enumerate(out):
+        _expect(y, f"out[{t}]", (B, N, H * P, d), x0.dtype, x0.device)
+    check(lib().iha_premix_fwd_qkv_at(*(_ptr(x) for x in xs), *(_ptr(w) for w in ws),
+                                      _ptr(positions), *(_ptr(y) for y in out), B, N, H, P, d,
+                                      _dt(x0), float(rope_base), sp), "iha_premix_fwd_qkv_at")
     return tuple(out)
 
 
@@ -456,6 +522,127 @@ def mha_bwd(q, k, v, o, dout, lse, mask: int = MASK_NONE, window: int = 0, scale
                         float(scale), int(mask), int(window), _dt(q), _stream(stream)),
           "mha_bwd")
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------- 4-bit key-value cache
+def kv4_page_bytes(page: int, Hkv: int, d: int) -> int:
+    """Bytes of one page of `page` tokens (K and V of Hkv heads of d features).
+    A cache is a uint8 CUDA tensor [n_pages, kv4_page_bytes(page, Hkv, d)]; it
+    needs no initial value."""
+    n = int(lib().kv4_page_bytes(page, Hkv, d))
+    if n == 0:
+        raise ValueError(f"no 4-bit cache of page {page}, {Hkv} heads of {d} features: page must "
+                         "be a multiple of 16, d one of 32, 64, 96, 128")
+    return n
+
+
+def _kv4_cache(cache, page: int, Hkv: int, d: int, device) -> int:
+    """Checks a cache tensor; its number of pages."""
+    nb = kv4_page_bytes(page, Hkv, d)
+    if cache.dim() != 2 or cache.shape[1] != nb:
+        raise ValueError(f"cache must be [n_pages, kv4_page_bytes = {nb}], got "
+                         f"{tuple(cache.shape)}")
+    _expect(cache, "cache", None, _torch().uint8, device)
+    return cache.shape[0]
+
+
+def kv4_store(k, v, slots, cache, page: int, stream=None):
+    """Quantise k, v ([B,N,Hkv,d] or [Bo,Bi,N,Hkv,d] views, bf16 or fp32) to 4 bits
+    and write token (b, n) to slot slots[b, n] = page id * page + offset (int32
+    [B,N] or [Bo,Bi,N]; -1 = padding, not stored).  Returns the cache."""
+    torch = _torch()
+    _expect(k, "k", contiguous=False)
+    _expect(v, "v", k.shape, k.dtype, k.device, contiguous=False)
+    k5, v5 = _as5(k), _as5(v)
+    Bo, Bi, N, Hkv, d = k5.shape
+    _expect(slots, "slots", tuple(k.shape[:-2]), torch.int32, k.device)
+    n_pages = _kv4_cache(cache, page, Hkv, d, k.device)
+    sp, _ = _stream_on(k.device, stream)
+    check(lib().kv4_store(_ptr(k5), _ptr(v5), _ptr(slots), _ptr(cache), Bo, Bi, N, n_pages,
+                          int(page), Hkv, d, _strides(k5), _strides(v5), _dt(k), sp), "kv4_store")
+    return cache
+
+
+def kv4_load(cache, slots, Hkv: int, d: int, page: int, dtype=None, out=None, stream=None):
+    """(k, v), each [*slots.shape, Hkv, d] in dtype (bf16 unless given, or fp32):
+    the rows of the cache at int32 slots [B,N] or [Bo,Bi,N]; slot -1 gives zeros.
+    out: the two tensors to write instead (strided views allowed)."""
+    torch = _torch()
+    _expect(slots, "slots", dtype=torch.int32)
+    if slots.dim() not in (2, 3):
+        raise ValueError(f"slots must be [B, N] or [Bo, Bi, N], got {tuple(slots.shape)}")
+    n_pages = _kv4_cache(cache, page, Hkv, d, slots.device)
+    sp, ctx = _stream_on(slots.device, stream)
+    shape = tuple(slots.shape) + (Hkv, d)
+    if out is None:
+        with ctx():
+            out = tuple(torch.empty(shape, dtype=dtype or torch.bfloat16, device=slots.device)
+                        for _ in range(2))
+    if len(out) != 2:
+        raise ValueError("out must hold two tensors (k, v)")
+    k, v = out
+    _expect(k, "out[0]", shape, dtype, slots.device, contiguous=False)
+    _expect(v, "out[1]", shape, k.dtype, slots.device, contiguous=False)
+    k5, v5 = _as5(k), _as5(v)
+    check(lib().kv4_load(_ptr(cache), _ptr(slots), _ptr(k5), _ptr(v5), *k5.shape[:3], n_pages,
+                         int(page), Hkv, d, _strides(k5), _strides(v5), _dt(k), sp), "kv4_load")
+    return k, v
+
+
+def mha_fwd_kv4_workspace_bytes(B: int, Nq: int, Hq: int, Hkv: int, d: int) -> int:
+    """Bytes of device scratch of mha_fwd_kv4; zero-filled once, then reusable."""
+    return int(lib().mha_fwd_kv4_workspace_bytes(B, Nq, Hq, Hkv, d))
+
+
+def mha_fwd_kv4(q, cache, block_table, seq_lens, Hkv: int, page: int, mask: int = MASK_CAUSAL,
+                window: int = 0, scale: float = 0.0, out=None, lse=None, return_lse: bool = False,
+                workspace=None, stream=None):
+    """Attention of the last Nq tokens of each sequence (q [B,Nq,Hq,d] bf16 view)
+    over the 4-bit paged cache.  seq_lens int32 [B] counts the keys of a sequence,
+    the new tokens' own among them; key j is in page block_table[b, j // page]
+    (int32 [B, table_width]).  Token t sits at position seq_lens[b] - Nq + t.
+
+    Returns O shaped like q; with return_lse, also lse [B, Hq, Nq] fp32.
+    `workspace` (uint8 CUDA tensor of mha_fwd_kv4_workspace_bytes, zero-filled
+    before its first use, one for each call that may run at the same time) is
+    made here when not given."""
+    torch = _torch()
+    _expect(q, "q", dtype=torch.bfloat16, contiguous=False)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Nq, Hq, d]")
+    dev = q.device
+    B, Nq, Hq, d = q.shape
+    n_pages = _kv4_cache(cache, page, Hkv, d, dev)
+    _expect(block_table, "block_table", dtype=torch.int32, device=dev)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [B={B}, table_width], got "
+                         f"{tuple(block_table.shape)}")
+    _expect(seq_lens, "seq_lens", (B,), torch.int32, dev)
+    sp, ctx = _stream_on(dev, stream)
+    if out is None:
+        with ctx():
+            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    _expect(out, "out", q.shape, q.dtype, dev, contiguous=False)
+    if lse is None and return_lse:
+        with ctx():
+            lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev)
+    if lse is not None:
+        _expect(lse, "lse", (B, Hq, Nq), torch.float32, dev)
+    if workspace is None:
+        need = mha_fwd_kv4_workspace_bytes(B, Nq, Hq, Hkv, d)
+        with ctx():
+            workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+    _expect(workspace, "workspace", dtype=torch.uint8, device=dev)
+    sq, so = q.stride(), out.stride()
+    if (d > 1 and (sq[3] != 1 or so[3] != 1)):
+        raise ValueError("the head dimension must be dense")
+    check(lib().mha_fwd_kv4(_ptr(q), _ptr(cache), _ptr(block_table), _ptr(seq_lens), _ptr(out),
+                            C.c_void_p(lse.data_ptr() if lse is not None else 0), _ptr(workspace),
+                            workspace.numel(), B, Nq, Hq, Hkv, d, n_pages, int(page),
+                            block_table.shape[1], Strides(sq[0], 0, sq[1], sq[2]),
+                            Strides(so[0], 0, so[1], so[2]), float(scale), int(mask), int(window),
+                            BF16, sp), "mha_fwd_kv4")
+    return (out, lse) if return_lse else out
 
 
 # ---------------------------------------------------------------- gather / scatter

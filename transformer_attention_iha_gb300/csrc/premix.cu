@@ -27,6 +27,7 @@ struct PremixGeom {
   int64_t ntok;  // B * N
   int N, H, P, HP, d;
   float rope_base;
+  const int32_t* pos;  // forward: RoPE position per token; null: token % N
 };
 
 // ---------------------------------------------------------------- vector I/O
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(256) premix_fwd_kernel(const FwdTensors<T> ts,
     }
     float cs[4], sn[4];
     if (ROPE) {
-      const int n = (int)(tok % g.N);
+      const int n = g.pos ? __ldg(g.pos + tok) : (int)(tok % g.N);
 #pragma unroll
       for (int j = 0; j < 4; ++j) rope_cs(n, inv_freq[j], cs[j], sn[j]);
     }
@@ -590,7 +591,43 @@ PremixGeom make_geom(int B, int N, int H, int P, int d, float rope_base) {
   g.HP = H * P;
   g.d = d;
   g.rope_base = rope_base;
+  g.pos = nullptr;
   return g;
+}
+
+// Q, K and V in one launch (RoPE on Q and K), at positions pos or 0 .. N - 1.
+iha_status premix_fwd_qkv(const char* name, const void* const* x, const float* const* w,
+                          void* const* y, const int32_t* pos, int B, int N, int H, int P, int d,
+                          iha_dtype dt, int rope, float rope_base, cudaStream_t s) {
+  for (int t = 0; t < 3; ++t) {
+    iha_status st =
+        check_common(name, x[t], w[t], y[t], B, N, H, P, d, dt, t < 2 ? rope : 0, rope_base);
+    if (st != IHA_OK) return st;
+  }
+  PremixGeom g = make_geom(B, N, H, P, d, rope_base);
+  g.pos = pos;
+  const size_t es = dt == IHA_BF16 ? 2 : 4;
+  const size_t ny = g.ntok * g.HP * d * es, nx = g.ntok * H * d * es, nw = (size_t)g.HP * H * 4;
+  for (int t = 0; t < 3; ++t) {
+    for (int u = 0; u < 3; ++u)
+      if (overlaps(y[t], ny, x[u], nx) || overlaps(y[t], ny, w[u], nw) ||
+          (u != t && overlaps(y[t], ny, y[u], ny)))
+        return fail(IHA_ERR_INVALID_ARG, "%s: an output overlaps another tensor", name);
+    if (pos && overlaps(y[t], ny, pos, (size_t)g.ntok * 4))
+      return fail(IHA_ERR_INVALID_ARG, "%s: an output overlaps the positions", name);
+  }
+  if (dt == IHA_BF16 && premix_tc_supported(H, P, d))
+    return premix_fwd_tc_multi(3, x, w, y, B, N, H, P, d, rope ? 3 : 0, rope_base, s, 0, pos);
+  // CUDA-core kernel: Q, K and V in one launch, or Q, K (rotated) in one and
+  // V in another when RoPE is on
+  const int n_first = rope ? 2 : 3;
+  if (dt == IHA_BF16) launch_fwd_n<__nv_bfloat16>(g, n_first, x, w, y, rope != 0, s);
+  else launch_fwd_n<float>(g, n_first, x, w, y, rope != 0, s);
+  iha_status st = check_launch(name);
+  if (st != IHA_OK || !rope) return st;
+  if (dt == IHA_BF16) launch_fwd_n<__nv_bfloat16>(g, 1, x + 2, w + 2, y + 2, false, s);
+  else launch_fwd_n<float>(g, 1, x + 2, w + 2, y + 2, false, s);
+  return check_launch(name);
 }
 
 }  // namespace
@@ -620,36 +657,26 @@ iha_status iha_premix_fwd_qkv(const void* xq, const void* xk, const void* xv, co
                               const float* wk, const float* wv, void* yq, void* yk, void* yv,
                               int B, int N, int H, int P, int d, iha_dtype dt, int rope,
                               float rope_base, void* stream) {
-  using namespace iha;
   const void* x[3] = {xq, xk, xv};
   const float* w[3] = {wq, wk, wv};
   void* y[3] = {yq, yk, yv};
-  for (int t = 0; t < 3; ++t) {
-    iha_status st = check_common("iha_premix_fwd_qkv", x[t], w[t], y[t], B, N, H, P, d, dt,
-                                 t < 2 ? rope : 0, rope_base);
-    if (st != IHA_OK) return st;
-  }
-  const PremixGeom g = make_geom(B, N, H, P, d, rope_base);
-  const size_t es = dt == IHA_BF16 ? 2 : 4;
-  const size_t ny = g.ntok * g.HP * d * es, nx = g.ntok * H * d * es, nw = (size_t)g.HP * H * 4;
-  for (int t = 0; t < 3; ++t)
-    for (int u = 0; u < 3; ++u)
-      if (overlaps(y[t], ny, x[u], nx) || overlaps(y[t], ny, w[u], nw) ||
-          (u != t && overlaps(y[t], ny, y[u], ny)))
-        return fail(IHA_ERR_INVALID_ARG, "iha_premix_fwd_qkv: an output overlaps another tensor");
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dt == IHA_BF16 && premix_tc_supported(H, P, d))
-    return premix_fwd_tc_multi(3, x, w, y, B, N, H, P, d, rope ? 3 : 0, rope_base, s);
-  // CUDA-core kernel: Q, K and V in one launch, or Q, K (rotated) in one and
-  // V in another when RoPE is on
-  const int n_first = rope ? 2 : 3;
-  if (dt == IHA_BF16) launch_fwd_n<__nv_bfloat16>(g, n_first, x, w, y, rope != 0, s);
-  else launch_fwd_n<float>(g, n_first, x, w, y, rope != 0, s);
-  iha_status st = check_launch("iha_premix_fwd_qkv");
-  if (st != IHA_OK || !rope) return st;
-  if (dt == IHA_BF16) launch_fwd_n<__nv_bfloat16>(g, 1, x + 2, w + 2, y + 2, false, s);
-  else launch_fwd_n<float>(g, 1, x + 2, w + 2, y + 2, false, s);
-  return check_launch("iha_premix_fwd_qkv");
+  return iha::premix_fwd_qkv("iha_premix_fwd_qkv", x, w, y, nullptr, B, N, H, P, d, dt, rope,
+                             rope_base, reinterpret_cast<cudaStream_t>(stream));
+}
+
+iha_status iha_premix_fwd_qkv_at(const void* xq, const void* xk, const void* xv, const float* wq,
+                                 const float* wk, const float* wv, const int32_t* positions,
+                                 void* yq, void* yk, void* yv, int B, int N, int H, int P, int d,
+                                 iha_dtype dt, float rope_base, void* stream) {
+  using namespace iha;
+  if (!positions) return fail(IHA_ERR_INVALID_ARG, "iha_premix_fwd_qkv_at: null pointer");
+  if (reinterpret_cast<uintptr_t>(positions) & 3)
+    return fail(IHA_ERR_ALIGNMENT, "iha_premix_fwd_qkv_at: positions must be 4-byte aligned");
+  const void* x[3] = {xq, xk, xv};
+  const float* w[3] = {wq, wk, wv};
+  void* y[3] = {yq, yk, yv};
+  return premix_fwd_qkv("iha_premix_fwd_qkv_at", x, w, y, positions, B, N, H, P, d, dt, 1,
+                        rope_base, reinterpret_cast<cudaStream_t>(stream));
 }
 
 iha_status iha_premix_fwd_qkv_interleaved(const void* xq, const void* xk, const void* xv,

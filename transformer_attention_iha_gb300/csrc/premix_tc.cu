@@ -58,6 +58,7 @@ struct FwdParams {
   uint32_t stage_bytes;                  // X bytes per stage
   uint32_t w_spacing;                    // bytes between the weight tiles
   const float* w[kMaxTens];
+  const int32_t* pos;                    // RoPE position per token; null: t % N
   RopeTable rt;
 };
 
@@ -268,8 +269,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (rope && warp_active && 2 * lane < HALF) {
         float c0, s0, c1, s1;
         const float4 inv = reinterpret_cast<const float4*>(inv_tab)[lane];  // pairs 2 lane, 2 lane + 1
-        rope_cos_sin(t % p.N, inv.x, inv.y, c0, s0);
-        rope_cos_sin(t % p.N, inv.z, inv.w, c1, s1);
+        // (the last pair of an odd token count has no second token)
+        const int n = p.pos ? __ldg(p.pos + min(t, p.ntok - 1)) : t % p.N;
+        rope_cos_sin(n, inv.x, inv.y, c0, s0);
+        rope_cos_sin(n, inv.z, inv.w, c1, s1);
         tab[lane] = make_float4(c0, c1, s0, s1);
       }
       __syncwarp();
@@ -376,8 +379,10 @@ void make_rope_table(RopeTable* rt, int d, float base) {
 
 iha_status premix_fwd_tc_multi(int ntens, const void* const* x, const float* const* w,
                                void* const* y, int B, int N, int H, int P, int d, int rope_mask,
-                               float rope_base, cudaStream_t stream, int interleave) {
+                               float rope_base, cudaStream_t stream, int interleave,
+                               const int32_t* pos) {
   FwdParams p;
+  p.pos = pos;
   p.interleave = interleave;
   p.ntok = B * N;
   p.N = N;
