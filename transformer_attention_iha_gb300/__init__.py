@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes as C
+import functools
 import os
 
 from . import _build
@@ -146,20 +147,44 @@ def _stream(stream):
     return C.c_void_p(stream.cuda_stream)
 
 
-def _stream_on(device, stream):
-    """(stream pointer, context for tensors made here) for a call on `device`,
-    which must be the current one.  Tensors that a call makes itself come from
-    the memory of the stream it runs on, so that nothing pending on another
-    stream still uses them."""
+# The serving calls run for a few microseconds on the GPU, so their checks stay
+# short: a device is its index, and a passing check builds no objects.
+_NOTHING = contextlib.nullcontext()
+
+
+def _raw_stream(dev: int, stream) -> int:
+    """cudaStream_t of a call on device `dev`, which must be the current one."""
     torch = _torch()
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {device}, but the current device is "
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors on cuda:{dev}, but the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     if stream is None:
-        return C.c_void_p(torch.cuda.current_stream(device).cuda_stream), contextlib.nullcontext
-    if stream.device != device:
-        raise ValueError(f"stream on {stream.device}, tensors on {device}")
-    return C.c_void_p(stream.cuda_stream), lambda: torch.cuda.stream(stream)
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"stream on {stream.device}, tensors on cuda:{dev}")
+    return stream.cuda_stream
+
+
+def _made_on(stream):
+    """Context for tensors that a call makes itself: they come from the memory
+    of the stream that the call runs on, so that nothing pending on another
+    stream still uses them."""
+    return _NOTHING if stream is None else _torch().cuda.stream(stream)
+
+
+def _dense(t, name: str, shape, dtype, dev: int) -> None:
+    """_expect for a dense tensor on device index `dev` (>= 0: a CUDA device)."""
+    if (dev < 0 or t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous() or
+            (shape is not None and t.shape != shape)):
+        _expect(t, name, shape, dtype, _torch().device("cuda", max(dev, 0)))
+
+
+def _view(t, name: str, shape, dtype, dev: int) -> None:
+    """The same for a strided view, dense in its last dimension."""
+    if dev < 0 or t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        _expect(t, name, shape, dtype, _torch().device("cuda", max(dev, 0)), contiguous=False)
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name}: the head dimension must be dense")
 
 
 def _dt(t) -> int:
@@ -250,26 +275,29 @@ def premix_fwd_qkv_at(xs, ws, P: int, positions, rope_base: float = 10000.0, out
     if len(xs) != 3 or len(ws) != 3:
         raise ValueError("xs and ws must hold three tensors (q, k, v)")
     x0 = xs[0]
-    _expect(x0, "xq")
     if x0.dim() != 4:
         raise ValueError("x must be [B, N, H, d]")
-    B, N, H, d = x0.shape
-    for t, (x, w) in enumerate(zip(xs, ws)):
-        _expect(x, f"x[{t}]", (B, N, H, d), x0.dtype, x0.device)
-        _expect(w, f"w[{t}]", (H, P, H), torch.float32, x0.device)
-    _expect(positions, "positions", (B, N), torch.int32, x0.device)
-    sp, ctx = _stream_on(x0.device, stream)
+    B, N, H, d = shape = x0.shape
+    dt = x0.dtype
+    dev = x0.get_device()
+    for t in range(3):
+        _dense(xs[t], "x", shape, dt, dev)
+        _dense(ws[t], "w", (H, P, H), torch.float32, dev)
+    _dense(positions, "positions", (B, N), torch.int32, dev)
+    sp = _raw_stream(dev, stream)
+    oshape = (B, N, H * P, d)
     if out is None:
-        with ctx():
-            out = tuple(torch.empty((B, N, H * P, d), dtype=x0.dtype, device=x0.device)
-                        for _ in range(3))
-    if len(out) != 3:
+        with _made_on(stream):
+            out = tuple(x0.new_empty(oshape) for _ in range(3))
+    elif len(out) != 3:
         raise ValueError("out must hold three tensors")
-    for t, y in enumerate(out):
-        _expect(y, f"out[{t}]", (B, N, H * P, d), x0.dtype, x0.device)
-    check(lib().iha_premix_fwd_qkv_at(*(_ptr(x) for x in xs), *(_ptr(w) for w in ws),
-                                      _ptr(positions), *(_ptr(y) for y in out), B, N, H, P, d,
-                                      _dt(x0), float(rope_base), sp), "iha_premix_fwd_qkv_at")
+    else:
+        for y in out:
+            _dense(y, "out", oshape, dt, dev)
+    check(lib().iha_premix_fwd_qkv_at(
+        xs[0].data_ptr(), xs[1].data_ptr(), xs[2].data_ptr(), ws[0].data_ptr(), ws[1].data_ptr(),
+        ws[2].data_ptr(), positions.data_ptr(), out[0].data_ptr(), out[1].data_ptr(),
+        out[2].data_ptr(), B, N, H, P, d, _dt(x0), rope_base, sp), "iha_premix_fwd_qkv_at")
     return tuple(out)
 
 
@@ -525,6 +553,7 @@ def mha_bwd(q, k, v, o, dout, lse, mask: int = MASK_NONE, window: int = 0, scale
 
 
 # ---------------------------------------------------------------- 4-bit key-value cache
+@functools.lru_cache(maxsize=256)
 def kv4_page_bytes(page: int, Hkv: int, d: int) -> int:
     """Bytes of one page of `page` tokens (K and V of Hkv heads of d features).
     A cache is a uint8 CUDA tensor [n_pages, kv4_page_bytes(page, Hkv, d)]; it
@@ -536,30 +565,37 @@ def kv4_page_bytes(page: int, Hkv: int, d: int) -> int:
     return n
 
 
-def _kv4_cache(cache, page: int, Hkv: int, d: int, device) -> int:
+def _kv4_pages(cache, page: int, Hkv: int, d: int, dev: int) -> int:
     """Checks a cache tensor; its number of pages."""
     nb = kv4_page_bytes(page, Hkv, d)
     if cache.dim() != 2 or cache.shape[1] != nb:
         raise ValueError(f"cache must be [n_pages, kv4_page_bytes = {nb}], got "
                          f"{tuple(cache.shape)}")
-    _expect(cache, "cache", None, _torch().uint8, device)
+    _dense(cache, "cache", None, _torch().uint8, dev)
     return cache.shape[0]
+
+
+def _strides45(t) -> Strides:
+    """Strides of a [B, N, Hh, d] or [Bo, Bi, N, Hh, d] view."""
+    s = t.stride()
+    return Strides(s[0], 0, s[1], s[2]) if len(s) == 4 else Strides(s[0], s[1], s[2], s[3])
 
 
 def kv4_store(k, v, slots, cache, page: int, stream=None):
     """Quantise k, v ([B,N,Hkv,d] or [Bo,Bi,N,Hkv,d] views, bf16 or fp32) to 4 bits
     and write token (b, n) to slot slots[b, n] = page id * page + offset (int32
     [B,N] or [Bo,Bi,N]; -1 = padding, not stored).  Returns the cache."""
-    torch = _torch()
-    _expect(k, "k", contiguous=False)
-    _expect(v, "v", k.shape, k.dtype, k.device, contiguous=False)
-    k5, v5 = _as5(k), _as5(v)
-    Bo, Bi, N, Hkv, d = k5.shape
-    _expect(slots, "slots", tuple(k.shape[:-2]), torch.int32, k.device)
-    n_pages = _kv4_cache(cache, page, Hkv, d, k.device)
-    sp, _ = _stream_on(k.device, stream)
-    check(lib().kv4_store(_ptr(k5), _ptr(v5), _ptr(slots), _ptr(cache), Bo, Bi, N, n_pages,
-                          int(page), Hkv, d, _strides(k5), _strides(v5), _dt(k), sp), "kv4_store")
+    shape = k.shape
+    if len(shape) not in (4, 5):
+        raise ValueError("k and v must be [B,N,Hkv,d] or [Bo,Bi,N,Hkv,d]")
+    dev, dt, Hkv, d = k.get_device(), _dt(k), shape[-2], shape[-1]
+    _view(k, "k", shape, k.dtype, dev)
+    _view(v, "v", shape, k.dtype, dev)
+    _dense(slots, "slots", shape[:-2], _torch().int32, dev)
+    n_pages = _kv4_pages(cache, page, Hkv, d, dev)
+    check(lib().kv4_store(k.data_ptr(), v.data_ptr(), slots.data_ptr(), cache.data_ptr(), shape[0],
+                          1 if len(shape) == 4 else shape[1], shape[-3], n_pages, page, Hkv, d,
+                          _strides45(k), _strides45(v), dt, _raw_stream(dev, stream)), "kv4_store")
     return cache
 
 
@@ -568,24 +604,28 @@ def kv4_load(cache, slots, Hkv: int, d: int, page: int, dtype=None, out=None, st
     the rows of the cache at int32 slots [B,N] or [Bo,Bi,N]; slot -1 gives zeros.
     out: the two tensors to write instead (strided views allowed)."""
     torch = _torch()
-    _expect(slots, "slots", dtype=torch.int32)
+    dev = slots.get_device()
     if slots.dim() not in (2, 3):
         raise ValueError(f"slots must be [B, N] or [Bo, Bi, N], got {tuple(slots.shape)}")
-    n_pages = _kv4_cache(cache, page, Hkv, d, slots.device)
-    sp, ctx = _stream_on(slots.device, stream)
-    shape = tuple(slots.shape) + (Hkv, d)
+    _dense(slots, "slots", None, torch.int32, dev)
+    n_pages = _kv4_pages(cache, page, Hkv, d, dev)
+    sp = _raw_stream(dev, stream)
+    shape = slots.shape + (Hkv, d)
     if out is None:
-        with ctx():
-            out = tuple(torch.empty(shape, dtype=dtype or torch.bfloat16, device=slots.device)
-                        for _ in range(2))
-    if len(out) != 2:
-        raise ValueError("out must hold two tensors (k, v)")
-    k, v = out
-    _expect(k, "out[0]", shape, dtype, slots.device, contiguous=False)
-    _expect(v, "out[1]", shape, k.dtype, slots.device, contiguous=False)
-    k5, v5 = _as5(k), _as5(v)
-    check(lib().kv4_load(_ptr(cache), _ptr(slots), _ptr(k5), _ptr(v5), *k5.shape[:3], n_pages,
-                         int(page), Hkv, d, _strides(k5), _strides(v5), _dt(k), sp), "kv4_load")
+        dtype = dtype or torch.bfloat16
+        with _made_on(stream):
+            k = cache.new_empty(shape, dtype=dtype)
+            v = cache.new_empty(shape, dtype=dtype)
+    else:
+        if len(out) != 2:
+            raise ValueError("out must hold two tensors (k, v)")
+        k, v = out
+        dtype = dtype or k.dtype
+        _view(k, "out[0]", shape, dtype, dev)
+        _view(v, "out[1]", shape, dtype, dev)
+    check(lib().kv4_load(cache.data_ptr(), slots.data_ptr(), k.data_ptr(), v.data_ptr(), shape[0],
+                         1 if len(shape) == 4 else shape[1], shape[-3], n_pages, page, Hkv, d,
+                         _strides45(k), _strides45(v), _dt(k), sp), "kv4_load")
     return k, v
 
 
@@ -607,41 +647,43 @@ def mha_fwd_kv4(q, cache, block_table, seq_lens, Hkv: int, page: int, mask: int 
     before its first use, one for each call that may run at the same time) is
     made here when not given."""
     torch = _torch()
-    _expect(q, "q", dtype=torch.bfloat16, contiguous=False)
-    if q.dim() != 4:
+    shape = q.shape
+    if len(shape) != 4:
         raise ValueError("q must be [B, Nq, Hq, d]")
-    dev = q.device
-    B, Nq, Hq, d = q.shape
-    n_pages = _kv4_cache(cache, page, Hkv, d, dev)
-    _expect(block_table, "block_table", dtype=torch.int32, device=dev)
+    B, Nq, Hq, d = shape
+    dev = q.get_device()
+    _view(q, "q", shape, torch.bfloat16, dev)
+    n_pages = _kv4_pages(cache, page, Hkv, d, dev)
+    _dense(block_table, "block_table", None, torch.int32, dev)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table must be [B={B}, table_width], got "
                          f"{tuple(block_table.shape)}")
-    _expect(seq_lens, "seq_lens", (B,), torch.int32, dev)
-    sp, ctx = _stream_on(dev, stream)
+    _dense(seq_lens, "seq_lens", (B,), torch.int32, dev)
+    sp = _raw_stream(dev, stream)
     if out is None:
-        with ctx():
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    _expect(out, "out", q.shape, q.dtype, dev, contiguous=False)
-    if lse is None and return_lse:
-        with ctx():
-            lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev)
+        with _made_on(stream):
+            out = q.new_empty(shape)
+    else:
+        _view(out, "out", shape, torch.bfloat16, dev)
     if lse is not None:
-        _expect(lse, "lse", (B, Hq, Nq), torch.float32, dev)
+        _dense(lse, "lse", (B, Hq, Nq), torch.float32, dev)
+    elif return_lse:
+        with _made_on(stream):
+            lse = q.new_empty((B, Hq, Nq), dtype=torch.float32)
     if workspace is None:
-        need = mha_fwd_kv4_workspace_bytes(B, Nq, Hq, Hkv, d)
-        with ctx():
-            workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
-    _expect(workspace, "workspace", dtype=torch.uint8, device=dev)
+        with _made_on(stream):
+            workspace = torch.zeros(mha_fwd_kv4_workspace_bytes(B, Nq, Hq, Hkv, d),
+                                    dtype=torch.uint8, device=q.device)
+    else:
+        _dense(workspace, "workspace", None, torch.uint8, dev)
     sq, so = q.stride(), out.stride()
-    if (d > 1 and (sq[3] != 1 or so[3] != 1)):
-        raise ValueError("the head dimension must be dense")
-    check(lib().mha_fwd_kv4(_ptr(q), _ptr(cache), _ptr(block_table), _ptr(seq_lens), _ptr(out),
-                            C.c_void_p(lse.data_ptr() if lse is not None else 0), _ptr(workspace),
-                            workspace.numel(), B, Nq, Hq, Hkv, d, n_pages, int(page),
+    check(lib().mha_fwd_kv4(q.data_ptr(), cache.data_ptr(), block_table.data_ptr(),
+                            seq_lens.data_ptr(), out.data_ptr(),
+                            0 if lse is None else lse.data_ptr(), workspace.data_ptr(),
+                            workspace.numel(), B, Nq, Hq, Hkv, d, n_pages, page,
                             block_table.shape[1], Strides(sq[0], 0, sq[1], sq[2]),
-                            Strides(so[0], 0, so[1], so[2]), float(scale), int(mask), int(window),
-                            BF16, sp), "mha_fwd_kv4")
+                            Strides(so[0], 0, so[1], so[2]), scale, mask, window, BF16, sp),
+          "mha_fwd_kv4")
     return (out, lse) if return_lse else out
 
 
