@@ -362,9 +362,10 @@ iha_status kv4_load(const void* cache, const int32_t* slots, void* k, void* v, i
  *                flagged (iha_device_error).
  *   lse_out      nullable; float32 [B, Hq, Nq] dense, natural log, with scale
  *   workspace    device scratch of mha_fwd_kv4_workspace_bytes() bytes, 256-byte
- *                aligned, ZERO-FILLED once before its first use; every call
- *                leaves it ready for the next.  Calls that may run at the same
- *                time (other streams, graphs replayed together) need a
+ *                aligned, ZERO-FILLED once before its first use (and again
+ *                after device error 2); every call leaves it ready for the
+ *                next, of any shape that fits it.  Calls that may run at the
+ *                same time (other streams, graphs replayed together) need a
  *                workspace each.
  *   scale <= 0 selects 1/sqrt(d)
  * Hq a multiple of Hkv, d in {32, 64, 96, 128}, bf16.  No length is read on

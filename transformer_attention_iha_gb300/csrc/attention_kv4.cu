@@ -17,17 +17,19 @@
 //   Softmax in the log2 domain, fp32; a column's reference maximum moves only
 //   when a score exceeds it by more than 8, then O and the sum are rescaled.
 // Codes are never expanded in memory: 36 NG bytes per token and head are read
-// once, straight into the registers of the lanes that use them, one block
-// ahead of the block being computed.
+// once, by bulk copies of whole blocks into a ring of kStages blocks that each
+// warp owns, and unpacked in the registers of the lanes that use them.
 //
-// Work is one line of blocks: sequence by sequence, head by head, column block
-// by column block (a unit), 16 tokens after 16 tokens.  Every CTA takes an
-// equal contiguous stretch of the line, whatever the lengths of the sequences,
-// so a single long sequence and a ragged batch both fill the GPU.  Lengths are
-// read on the device (each CTA sums them up), so a captured call replays with
-// other lengths.  A unit that lies in one CTA's stretch is finished there; one
-// that spans several leaves partial results (m, l, O in fp32) in the workspace,
-// and the CTA that arrives last joins them in order.
+// Work is one line of positions: sequence by sequence, head by head, column
+// block by column block (a unit); a unit takes one position per block of 16
+// tokens it sees and kUnitCost for what a unit costs by itself (its Q, its
+// output).  Every warp of the grid takes an equal contiguous stretch of the
+// line, whatever the lengths of the sequences: one long sequence, a ragged
+// batch and many short ones all fill the GPU, and a warp's ring runs on across
+// units.  Lengths are read on the device (each CTA sums them up), so a captured
+// call replays with other lengths.  A unit that lies in one warp's stretch is
+// finished by that warp; one that spans several leaves parts (m, l, O in fp32)
+// in the workspace, and the CTA that finishes last joins them in order.
 #include <math.h>
 
 #include "kv4.cuh"
@@ -39,10 +41,13 @@ IHA_DEVICE_ERROR_WORD(attention_kv4)
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxCtas = 640;  // workspace slots; 152 SMs x 4 CTAs and some
-// A CTA's stretch is at least this many blocks (two for each warp): shorter
-// ones cost more in joining than they save.
-constexpr int kMinBlocks = 2 * kWarps;
+constexpr int kStages = 4;    // blocks of a warp's ring
+constexpr int kUnitCost = 2;  // positions a unit takes besides its blocks
+// A warp's stretch is at least this long: shorter ones cost more in joining
+// than they save.
+constexpr int kMinShare = 4;
+constexpr int kMaxCtas = 640;  // counters for 152 SMs x 4 CTAs and some
+constexpr int kCounterBytes = kMaxCtas * kWarps * 4;
 
 struct Kv4AttnParams {
   const __nv_bfloat16* q;
@@ -51,14 +56,16 @@ struct Kv4AttnParams {
   const int32_t* lens;
   __nv_bfloat16* o;
   float* lse;
-  unsigned* counters;  // [kMaxCtas], zero between calls
-  float* partials;     // [kMaxCtas][2][part_stride]
+  unsigned* counters;  // [kMaxCtas * kWarps], zero between calls
+  float* parts;        // [warps of the grid][2][part_stride]
   int part_cols, part_stride;
   int B, Nq, Hq, Hkv, G, ncols, ncb;  // ncols = Nq * G columns of a key-value head, in ncb blocks
+  unsigned long long inv_g;           // ceil(2^32 / G): col / G = col * inv_g >> 32
   int n_pages, page, blocks_per_page, table_w;
   int mask, window;
   float scale_log2;
   iha_strides sq, so;
+  uint64_t wait_ns;
 };
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -86,40 +93,25 @@ __device__ __forceinline__ uint32_t minus136(uint32_t v) {
   return *reinterpret_cast<uint32_t*>(&x);
 }
 
-// NG words of one lane (contiguous, 4 NG-byte aligned).
+// NG words of one lane (contiguous, 4 NG-byte aligned shared memory).
 template <int NG>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[NG]) {
   if constexpr (NG == 4) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
     w[0] = u.x;
     w[1] = u.y;
     w[2] = u.z;
     w[3] = u.w;
   } else if constexpr (NG == 2) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
     w[0] = u.x;
     w[1] = u.y;
   } else {
 #pragma unroll
-    for (int j = 0; j < NG; ++j) w[j] = __ldg(reinterpret_cast<const uint32_t*>(p) + j);
+    for (int j = 0; j < NG; ++j) w[j] = reinterpret_cast<const uint32_t*>(p)[j];
   }
 }
 
-// One lane's share of a 16-token block: codes of both halves, scales of
-// tokens g and g + 8.
-template <int NG>
-struct BlockRegs {
-  uint32_t k[2][NG], v[2][NG], ks[NG], vs[NG];
-  __device__ __forceinline__ void load(const uint8_t* blk, int lane) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      load_words<NG>(blk + (c * 32 + lane) * 4 * NG, k[c]);
-      load_words<NG>(blk + kv4_v_codes(NG) + (c * 32 + lane) * 4 * NG, v[c]);
-    }
-    load_words<NG>(blk + kv4_k_scales(NG) + (lane >> 2) * 4 * NG, ks);
-    load_words<NG>(blk + kv4_v_scales(NG) + (lane >> 2) * 4 * NG, vs);
-  }
-};
 // Scale of token half c, group j, from a lane's NG scale words.
 template <int NG>
 __device__ __forceinline__ float scale_of(const uint32_t (&w)[NG], int c, int j) {
@@ -127,10 +119,14 @@ __device__ __forceinline__ float scale_of(const uint32_t (&w)[NG], int c, int j)
   return (h & 1) ? bf16hi_to_f32(w[h >> 1]) : bf16lo_to_f32(w[h >> 1]);
 }
 
+__device__ __forceinline__ int token_of(const Kv4AttnParams& p, int col) {
+  return (int)((unsigned long long)(unsigned)col * p.inv_g >> 32);
+}
+
 // Four features of one output row: O / l, and with the first four the row's lse.
 __device__ __forceinline__ void write_out(const Kv4AttnParams& p, int b, int hk, int col, int f,
                                           float4 o, float ref, float l) {
-  const int qi = col / p.G, qh = hk * p.G + (col - qi * p.G);
+  const int qi = token_of(p, col), qh = hk * p.G + (col - qi * p.G);
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint2 u;
   u.x = pack_bf16x2(o.x * inv, o.y * inv);
@@ -144,432 +140,590 @@ __device__ __forceinline__ void write_out(const Kv4AttnParams& p, int b, int hk,
 // Visible keys [lo, hi) of column col of a sequence of len keys.
 __device__ __forceinline__ void col_range(const Kv4AttnParams& p, int len, int col, int& lo,
                                           int& hi) {
-  const int i = len - p.Nq + col / p.G;  // position of the new token
+  const int i = len - p.Nq + token_of(p, col);  // position of the new token
   hi = p.mask == IHA_MASK_NONE ? len : min(len, i + 1);
   lo = p.mask == IHA_MASK_CAUSAL_WINDOW && i >= p.window ? i - p.window + 1 : 0;
 }
 
-// Blocks [b0, b1) that column block cb (COLS columns) of a sequence sees.
+// First block and number of blocks that column block cb (COLS columns) sees.
 template <int COLS>
 __device__ __forceinline__ void unit_blocks(const Kv4AttnParams& p, int len, int cb, int& b0,
-                                            int& b1) {
+                                            int& n) {
   int lo, hi, x;
   col_range(p, len, cb * COLS, lo, x);
   col_range(p, len, min(p.ncols, cb * COLS + COLS) - 1, x, hi);
   b0 = lo / kKv4Tok;
-  b1 = max(b0, (hi + kKv4Tok - 1) / kKv4Tok);
+  n = max(0, (hi + kKv4Tok - 1) / kKv4Tok - b0);
 }
 
 __device__ __forceinline__ int seq_len(const Kv4AttnParams& p, int b) {
   return min(max(__ldg(p.lens + b), 0), p.table_w * p.page);
 }
 
-// Blocks of one head of sequence b over its column blocks; a unit that sees
-// nothing counts as one block, so that some CTA writes its empty rows.
+// Positions of one head of a sequence over its column blocks.
 template <int COLS>
-__device__ __forceinline__ int head_blocks(const Kv4AttnParams& p, int len) {
-  int n = 0;
+__device__ __forceinline__ int head_positions(const Kv4AttnParams& p, int len) {
+  int sum = p.ncb * kUnitCost;
   for (int cb = 0; cb < p.ncb; ++cb) {
-    int b0, b1;
-    unit_blocks<COLS>(p, len, cb, b0, b1);
-    n += max(1, b1 - b0);
+    int b0, n;
+    unit_blocks<COLS>(p, len, cb, b0, n);
+    sum += n;
   }
-  return n;
+  return sum;
 }
 
 // Sum over the CTA; every thread gets it (s: kWarps entries).
 __device__ __forceinline__ long long cta_sum(long long v, long long* s) {
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
-  __syncthreads();
   if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
   __syncthreads();
   v = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) v += s[w];
+  __syncthreads();
   return v;
+}
+
+// A unit of the line, and a warp's share of it.
+struct Unit {
+  int b, hk, cb, len, b0, n;
+  int at;  // the unit's first position, from the start of the warp's stretch
+};
+// Blocks [r0, r1) of the unit that positions [0, stretch) hold.
+__device__ __forceinline__ void my_blocks(const Unit& u, int stretch, int& r0, int& r1) {
+  r0 = max(0, -u.at - kUnitCost);
+  r1 = min(u.n, stretch - u.at - kUnitCost);
+}
+// The unit after u; false behind the last sequence.
+template <int COLS>
+__device__ __forceinline__ bool next_unit(const Kv4AttnParams& p, Unit& u) {
+  u.at += u.n + kUnitCost;
+  if (++u.cb == p.ncb) {
+    u.cb = 0;
+    if (++u.hk == p.Hkv) {
+      u.hk = 0;
+      if (++u.b == p.B) return false;
+      u.len = seq_len(p, u.b);
+    }
+  }
+  unit_blocks<COLS>(p, u.len, u.cb, u.b0, u.n);
+  return true;
+}
+
+template <int NG, int NT>
+struct Smem {
+  uint8_t ring[kWarps][kStages][kv4_block_bytes(NG)];
+  uint4 q[NT > 1 ? kWarps : 1][NT > 1 ? NT * NG * 32 : 1];
+  float qc[kWarps][NT * NG][8];  // -136 * sum of a group's q, per column
+  uint64_t full[kWarps][kStages];
+  long long scan[kWarps], base[kWarps];
+  int seq[kWarps];
+  // units that span warps: at each end of a warp's stretch, {sequence, head,
+  // column block, first warp, last warp} (first warp -1: none)
+  int span[kWarps + 1][5];
+  int last[kWarps + 1];
+  int abort;
+};
+
+// Joins parts first .. last of a unit (all threads of the CTA).
+template <int NG, int NT>
+__device__ __forceinline__ void join_parts(const Kv4AttnParams& p, const int* span, float* scratch) {
+  constexpr int D = 32 * NG, COLS = 8 * NT;
+  const int b = span[0], hk = span[1], c_first = span[2] * COLS, first = span[3], last = span[4];
+  const int ncolv = min(COLS, p.ncols - c_first), items = ncolv * (D / 4);
+  // few items: several threads share one, each taking every groups-th part
+  const int groups = items >= kThreads ? 1 : kThreads / items;
+  const int tid = threadIdx.x;
+  for (int i0 = 0; i0 < items; i0 += kThreads) {
+    const int grp = groups > 1 ? tid / items : 0, i = groups > 1 ? tid - grp * items : i0 + tid;
+    const bool mine = i < items && grp < groups;
+    const int cc = mine ? i / (D / 4) : 0, f = mine ? (i - cc * (D / 4)) * 4 : 0;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (mine) {
+      constexpr int U = 4;
+      for (int w0 = first + grp; w0 <= last; w0 += U * groups) {
+        float pm[U], pl[U];
+        float4 po[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const int w = w0 + k * groups;
+          pm[k] = -INFINITY;
+          pl[k] = 0.f;
+          po[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (w <= last) {
+            const float* pp = p.parts + ((int64_t)w * 2 + (w == first ? 1 : 0)) * p.part_stride;
+            pm[k] = __ldcg(pp + p.part_cols * D + cc);
+            pl[k] = __ldcg(pp + p.part_cols * D + p.part_cols + cc);
+            po[k] = __ldcg(reinterpret_cast<const float4*>(pp + cc * D + f));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const float n = fmaxf(m, pm[k]), ref = n == -INFINITY ? 0.f : n;
+          const float a = exp2f(m - ref), c = exp2f(pm[k] - ref);
+          m = n;
+          l = fmaf(l, a, pl[k] * c);
+          o.x = fmaf(o.x, a, po[k].x * c);
+          o.y = fmaf(o.y, a, po[k].y * c);
+          o.z = fmaf(o.z, a, po[k].z * c);
+          o.w = fmaf(o.w, a, po[k].w * c);
+        }
+      }
+    }
+    if (groups > 1) {
+      float* s = scratch + tid * 6;
+      s[0] = m;
+      s[1] = l;
+      s[2] = o.x;
+      s[3] = o.y;
+      s[4] = o.z;
+      s[5] = o.w;
+      __syncthreads();
+      if (grp == 0) {
+        for (int k = 1; k < groups; ++k) {
+          const float* t = scratch + (tid + k * items) * 6;
+          const float n = fmaxf(m, t[0]), ref = n == -INFINITY ? 0.f : n;
+          const float a = exp2f(m - ref), c = exp2f(t[0] - ref);
+          m = n;
+          l = fmaf(l, a, t[1] * c);
+          o.x = fmaf(o.x, a, t[2] * c);
+          o.y = fmaf(o.y, a, t[3] * c);
+          o.z = fmaf(o.z, a, t[4] * c);
+          o.w = fmaf(o.w, a, t[5] * c);
+        }
+      }
+      __syncthreads();
+    }
+    if (mine && grp == 0) write_out(p, b, hk, c_first + cc, f, o, m == -INFINITY ? 0.f : m, l);
+  }
 }
 
 template <int NG, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
     attn_kv4_kernel(const Kv4AttnParams p) {
-  constexpr int D = 32 * NG, COLS = 8 * NT;
-  __shared__ float sm_m[kWarps][COLS], sm_l[kWarps][COLS];
-  __shared__ __align__(16) float sm_o[kWarps][8][D + 4];
-  __shared__ uint4 sm_q[NT > 1 ? NT * NG * 32 : 1];
-  __shared__ __align__(16) float sm_qc[NT * NG][8];  // -136 * sum of a group's q, per column
-  __shared__ long long sm_scan[kWarps];
-  __shared__ long long sm_base;
-  __shared__ int sm_seq, sm_last;
+  constexpr int D = 32 * NG, COLS = 8 * NT, BYTES = kv4_block_bytes(NG);
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Smem<NG, NT>& sm = *reinterpret_cast<Smem<NG, NT>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  volatile int* abort_flag = &sm.abort;
 
-  // ---- this CTA's stretch of the line
+  // ---- this warp's stretch of the line
+  if (lane == 0)
+    for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&sm.full[warp][i]), 1);
+  if (tid <= kWarps) sm.span[tid][3] = -1;
+  if (tid == 0) sm.abort = 0;
+  mbar_init_fence();
   long long mine = 0;
   for (int b = tid; b < p.B; b += kThreads) {
     const int raw = __ldg(p.lens + b), len = seq_len(p, b);
     if (blockIdx.x == 0 && raw != len) atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
-    mine += (long long)head_blocks<COLS>(p, len) * p.Hkv;
+    mine += (long long)head_positions<COLS>(p, len) * p.Hkv;
   }
-  const long long total = cta_sum(mine, sm_scan);
-  const long long share = max((long long)kMinBlocks, (total + gridDim.x - 1) / gridDim.x);
-  long long w = share * blockIdx.x;
-  const long long w_end = min(total, w + share);
-  if (w >= total) return;
-  // the sequence that holds w
-  {
+  const long long total = cta_sum(mine, sm.scan);
+  const int workers = gridDim.x * kWarps;
+  const long long share64 = max((long long)kMinShare, (total + workers - 1) / workers);
+  const int share = (int)share64;
+  const int me = blockIdx.x * kWarps + warp;
+  if (share64 * (blockIdx.x * kWarps) >= total) return;  // the whole CTA
+  const long long w = share64 * me;
+  const int stretch = (int)min((long long)share, max(0ll, total - w));
+  {  // the sequence that holds position w, for each warp
     long long base = 0;
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
       const int b = b0 + tid;
       const long long v =
-          b < p.B ? (long long)head_blocks<COLS>(p, seq_len(p, b)) * p.Hkv : 0;
+          b < p.B ? (long long)head_positions<COLS>(p, seq_len(p, b)) * p.Hkv : 0;
       long long incl = v;
 #pragma unroll
       for (int k = 1; k < 32; k <<= 1) {
         const long long u = __shfl_up_sync(0xffffffffu, incl, k);
         if (lane >= k) incl += u;
       }
-      __syncthreads();
-      if (lane == 31) sm_scan[warp] = incl;
+      if (lane == 31) sm.scan[warp] = incl;
       __syncthreads();
       long long all = 0;
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
-        if (k < warp) incl += sm_scan[k];
-        all += sm_scan[k];
+        if (k < warp) incl += sm.scan[k];
+        all += sm.scan[k];
       }
-      if (w >= base + incl - v && w < base + incl) {
-        sm_seq = b;
-        sm_base = base + incl - v;
+      const long long lo = base + incl - v, hi = base + incl;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        const long long wk = share64 * (blockIdx.x * kWarps + k);
+        if (wk >= lo && wk < hi) {
+          sm.seq[k] = b;
+          sm.base[k] = lo;
+        }
       }
       base += all;
-      if (base > w) break;  // the same for every thread
+      __syncthreads();
+      if (base > share64 * (blockIdx.x * kWarps + kWarps - 1)) break;  // the same everywhere
     }
-    __syncthreads();
   }
-  int b = sm_seq;
-  long long seq_base = sm_base;
 
-  // ---- units of the stretch
-  while (w < w_end && b < p.B) {
-    const int len = seq_len(p, b);
-    const int per_head = head_blocks<COLS>(p, len);
-    const long long rel = w - seq_base;
-    const int hk = (int)(rel / per_head);
-    int s0 = (int)(rel - (long long)hk * per_head);
-    int cb = 0, ub0, ub1, n;
-    for (;; ++cb) {
-      unit_blocks<COLS>(p, len, cb, ub0, ub1);
-      n = max(1, ub1 - ub0);
-      if (s0 < n || cb == p.ncb - 1) break;
-      s0 -= n;
-    }
-    const int s1 = (int)min((long long)n, s0 + (w_end - w));
-    const long long unit_w = w - s0;  // the unit's place on the line
-    const int c_first = cb * COLS, ncolv = min(COLS, p.ncols - c_first);
-
-    int lo_full, hi_full, x_;  // keys that every column of the unit sees
-    col_range(p, len, c_first, x_, hi_full);
-    col_range(p, len, c_first + ncolv - 1, lo_full, x_);
-
-    // this warp's blocks
-    const int nblk = min(ub0 + s1, ub1) - (ub0 + s0);
-    const int per_warp = (nblk + kWarps - 1) / kWarps;
-    int blk = ub0 + s0 + warp * per_warp;
-    const int blk_end = min(ub0 + s0 + nblk, blk + per_warp);
-
-    // pages: the id of the current page and of the next one, read ahead
-    int pi = blk / p.blocks_per_page, in_page = blk - pi * p.blocks_per_page;
-    const int32_t* trow = p.table + (int64_t)b * p.table_w;
-    const int pi_end = (blk_end + p.blocks_per_page - 1) / p.blocks_per_page;
-    auto page_id = [&](int i) { return i < pi_end ? __ldg(trow + i) : 0; };
-    int id = -1, id_next = 0;
-    if (blk < blk_end) {
-      id = page_id(pi);
-      id_next = page_id(pi + 1);
-    }
-    BlockRegs<NG> nx;  // the block being fetched
-    bool nx_ok = false;
-    auto fetch = [&]() {
-      nx_ok = id >= 0 && id < p.n_pages;
-      if (nx_ok)
-        nx.load(p.cache + kv4_block_of(id, in_page, hk, p.Hkv, p.blocks_per_page, NG), lane);
-      else if (lane == 0)
-        atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
-      if (++in_page == p.blocks_per_page) {
-        in_page = 0;
-        ++pi;
-        id = id_next;
-        id_next = page_id(pi + 1);
+  bool ok = true;
+  if (stretch > 0) {
+    Unit u;
+    u.b = sm.seq[warp];
+    u.len = seq_len(p, u.b);
+    {
+      const int per_head = head_positions<COLS>(p, u.len);
+      const long long rel = w - sm.base[warp];
+      u.hk = (rel >> 31) == 0 ? (int)((unsigned)rel / (unsigned)per_head) : (int)(rel / per_head);
+      int s = (int)(rel - (long long)u.hk * per_head);
+      for (u.cb = 0;; ++u.cb) {
+        unit_blocks<COLS>(p, u.len, u.cb, u.b0, u.n);
+        if (s < u.n + kUnitCost || u.cb == p.ncb - 1) break;
+        s -= u.n + kUnitCost;
       }
+      u.at = -s;
+    }
+
+    // ---- the ring: blocks are fetched kStages ahead, in runs inside one page;
+    // the page id of the run after the current one is read ahead
+    Unit pu = u;
+    int pr, pr_end;
+    my_blocks(pu, stretch, pr, pr_end);
+    bool more = true;
+    struct Run {
+      int id, head, in_page, cnt;
     };
-    if (blk < blk_end) fetch();
-
-    // Q as B operand: column 8 nt + g, feature pairs (i, i + 4) of octet t
-    uint32_t qf[NT == 1 ? NG : 1][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int col = c_first + 8 * nt + g;
-      const bool ok = col < p.ncols;
-      const int qi = ok ? col / p.G : 0, qh = hk * p.G + (ok ? col - qi * p.G : 0);
-      const __nv_bfloat16* qp = p.q + b * p.sq.b_outer + qi * p.sq.seq + qh * p.sq.head;
-#pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (ok) u = __ldg(reinterpret_cast<const uint4*>(qp + 32 * j + 8 * t));
-        const uint32_t f0 = __byte_perm(u.x, u.z, 0x5410), f1 = __byte_perm(u.x, u.z, 0x7632);
-        const uint32_t f2 = __byte_perm(u.y, u.w, 0x5410), f3 = __byte_perm(u.y, u.w, 0x7632);
-        if constexpr (NT == 1) {
-          qf[j][0] = f0;
-          qf[j][1] = f1;
-          qf[j][2] = f2;
-          qf[j][3] = f3;
-        } else if (warp == 0) {
-          sm_q[(nt * NG + j) * 32 + lane] = make_uint4(f0, f1, f2, f3);
-        }
-        float s = bf16lo_to_f32(u.x) + bf16hi_to_f32(u.x) + bf16lo_to_f32(u.y) +
-                  bf16hi_to_f32(u.y) + bf16lo_to_f32(u.z) + bf16hi_to_f32(u.z) +
-                  bf16lo_to_f32(u.w) + bf16hi_to_f32(u.w);
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        if (warp == 0 && t == 0) sm_qc[nt * NG + j][g] = -136.f * s;
+    auto next_run = [&]() {
+      Run r = {0, 0, 0, 0};
+      while (more && pr >= pr_end) {
+        more = pu.at + pu.n + kUnitCost < stretch && next_unit<COLS>(p, pu);
+        if (more) my_blocks(pu, stretch, pr, pr_end);
       }
-    }
-    __syncthreads();
-
-    float m[NT][2], l[NT][2];
-    float acc[NT][NG][2][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-      for (int j = 0; j < NG; ++j)
-#pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[nt][j][a][e] = 0.f;
-    }
-
-    for (; blk < blk_end; ++blk) {
-      const BlockRegs<NG> r = nx;
-      const bool ok = nx_ok;
-      if (blk + 1 < blk_end) fetch();
-      if (!ok) continue;
-      float x[NT][4];  // (token g, columns 2t, 2t+1), (token g + 8, ...)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[nt][e] = 0.f;
-#pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        uint32_t a[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[2 * i] = nibbles(r.k[0][j], i);
-          a[2 * i + 1] = nibbles(r.k[1][j], i);
+      if (more) {
+        const int blk = pu.b0 + pr, pi = blk / p.blocks_per_page;
+        r.in_page = blk - pi * p.blocks_per_page;
+        r.cnt = min(p.blocks_per_page - r.in_page, pr_end - pr);
+        r.head = pu.hk;
+        r.id = __ldg(p.table + (int64_t)pu.b * p.table_w + pi);
+        pr += r.cnt;
+      }
+      return r;
+    };
+    Run run = next_run(), run_next = next_run();
+    uint32_t bad = 0, phase = 0;  // stages with no copy under way; parity of the barriers
+    const uint32_t ring = smem_u32(sm.ring[warp]), bars = smem_u32(sm.full[warp]);
+    auto fetch = [&](int stage) {
+      bad |= 1u << stage;
+      if (run.cnt == 0) {
+        run = run_next;
+        if (run.cnt == 0) return;
+        run_next = next_run();
+      }
+      if (run.id >= 0 && run.id < p.n_pages) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bars + 8 * stage, BYTES);
+          bulk_load(ring + stage * BYTES,
+                    p.cache + kv4_block_of(run.id, run.in_page, run.head, p.Hkv, p.blocks_per_page,
+                                           NG),
+                    BYTES, bars + 8 * stage);
         }
-        const float k0 = scale_of<NG>(r.ks, 0, j), k1 = scale_of<NG>(r.ks, 1, j);
+        bad ^= 1u << stage;
+      } else if (lane == 0) {
+        atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
+      }
+      ++run.in_page;
+      --run.cnt;
+    };
+#pragma unroll 1
+    for (int i = 0; i < kStages; ++i) fetch(i);
+    int stage = 0;
+
+    // ---- units of the stretch
+    for (;;) {
+      int r0, r1;
+      my_blocks(u, stretch, r0, r1);
+      const int empty_at = u.at + kUnitCost - 1;  // an empty unit belongs to this position
+      const bool empty = u.n == 0 && empty_at >= 0 && empty_at < stretch;
+      if (r0 < r1 || empty) {
+        const int c_first = u.cb * COLS, ncolv = min(COLS, p.ncols - c_first);
+        int lo_full, hi_full, x_;  // keys that every column of the unit sees
+        col_range(p, u.len, c_first, x_, hi_full);
+        col_range(p, u.len, c_first + ncolv - 1, lo_full, x_);
+
+        // Q as B operand: column 8 nt + g, feature pairs (i, i + 4) of octet t
+        uint32_t qf[NT == 1 ? NG : 1][4];
+        __syncwarp();  // the Q of the unit before has been read
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float2 qc = *reinterpret_cast<const float2*>(&sm_qc[nt * NG + j][2 * t]);
-          float c[4] = {qc.x, qc.y, qc.x, qc.y};
-          if constexpr (NT == 1) {
-            mma_bf16(c, a[0], a[1], a[2], a[3], qf[j][0], qf[j][1]);
-            mma_bf16(c, a[4], a[5], a[6], a[7], qf[j][2], qf[j][3]);
-          } else {
-            const uint4 f = sm_q[(nt * NG + j) * 32 + lane];
-            mma_bf16(c, a[0], a[1], a[2], a[3], f.x, f.y);
-            mma_bf16(c, a[4], a[5], a[6], a[7], f.z, f.w);
+          const int col = c_first + 8 * nt + g;
+          const bool in = col < p.ncols;
+          const int qi = in ? token_of(p, col) : 0, qh = u.hk * p.G + (in ? col - qi * p.G : 0);
+          const __nv_bfloat16* qp =
+              p.q + u.b * p.sq.b_outer + qi * p.sq.seq + qh * p.sq.head + 8 * t;
+          uint4 v[NG];
+#pragma unroll
+          for (int j = 0; j < NG; ++j)
+            v[j] = in ? __ldg(reinterpret_cast<const uint4*>(qp + 32 * j)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int j = 0; j < NG; ++j) {
+            const uint32_t f0 = __byte_perm(v[j].x, v[j].z, 0x5410);
+            const uint32_t f1 = __byte_perm(v[j].x, v[j].z, 0x7632);
+            const uint32_t f2 = __byte_perm(v[j].y, v[j].w, 0x5410);
+            const uint32_t f3 = __byte_perm(v[j].y, v[j].w, 0x7632);
+            if constexpr (NT == 1) {
+              qf[j][0] = f0;
+              qf[j][1] = f1;
+              qf[j][2] = f2;
+              qf[j][3] = f3;
+            } else {
+              sm.q[warp][(nt * NG + j) * 32 + lane] = make_uint4(f0, f1, f2, f3);
+            }
+            float s = bf16lo_to_f32(v[j].x) + bf16hi_to_f32(v[j].x) + bf16lo_to_f32(v[j].y) +
+                      bf16hi_to_f32(v[j].y) + bf16lo_to_f32(v[j].z) + bf16hi_to_f32(v[j].z) +
+                      bf16lo_to_f32(v[j].w) + bf16hi_to_f32(v[j].w);
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            if (t == 0) sm.qc[warp][nt * NG + j][g] = -136.f * s;
           }
-          x[nt][0] = fmaf(k0, c[0], x[nt][0]);
-          x[nt][1] = fmaf(k0, c[1], x[nt][1]);
-          x[nt][2] = fmaf(k1, c[2], x[nt][2]);
-          x[nt][3] = fmaf(k1, c[3], x[nt][3]);
         }
-      }
-      const bool edge = blk * kKv4Tok < lo_full || (blk + 1) * kKv4Tok > hi_full;
-      uint32_t hidden = 0;  // bit 4 nt + e
-      if (edge) {
-        const int key = blk * kKv4Tok + g;
+        __syncwarp();
+
+        float m[NT][2], l[NT][2];
+        float acc[NT][NG][2][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          m[nt][0] = m[nt][1] = -INFINITY;
+          l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+          for (int j = 0; j < NG; ++j)
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[nt][j][a][e] = 0.f;
+        }
+
+#pragma unroll 1
+        for (int r = r0; r < r1; ++r, stage = stage + 1 == kStages ? 0 : stage + 1) {
+          if ((bad >> stage) & 1u) {  // no such page: its keys are hidden
+            fetch(stage);
+            continue;
+          }
+          if (!mbar_wait_warp(bars + 8 * stage, (phase >> stage) & 1u, abort_flag, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          phase ^= 1u << stage;
+          const uint8_t* blk_s = sm.ring[warp][stage];
+          uint32_t kw[2][NG], ks[NG];
+          load_words<NG>(blk_s + lane * 4 * NG, kw[0]);
+          load_words<NG>(blk_s + (32 + lane) * 4 * NG, kw[1]);
+          load_words<NG>(blk_s + kv4_k_scales(NG) + g * 4 * NG, ks);
+          float x[NT][4];  // (token g, columns 2t, 2t+1), (token g + 8, ...)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[nt][e] = 0.f;
+#pragma unroll
+          for (int j = 0; j < NG; ++j) {
+            uint32_t a[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              a[2 * i] = nibbles(kw[0][j], i);
+              a[2 * i + 1] = nibbles(kw[1][j], i);
+            }
+            const float k0 = scale_of<NG>(ks, 0, j), k1 = scale_of<NG>(ks, 1, j);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const float2 qc = *reinterpret_cast<const float2*>(&sm.qc[warp][nt * NG + j][2 * t]);
+              float c[4] = {qc.x, qc.y, qc.x, qc.y};
+              if constexpr (NT == 1) {
+                mma_bf16(c, a[0], a[1], a[2], a[3], qf[j][0], qf[j][1]);
+                mma_bf16(c, a[4], a[5], a[6], a[7], qf[j][2], qf[j][3]);
+              } else {
+                const uint4 f = sm.q[warp][(nt * NG + j) * 32 + lane];
+                mma_bf16(c, a[0], a[1], a[2], a[3], f.x, f.y);
+                mma_bf16(c, a[4], a[5], a[6], a[7], f.z, f.w);
+              }
+              x[nt][0] = fmaf(k0, c[0], x[nt][0]);
+              x[nt][1] = fmaf(k0, c[1], x[nt][1]);
+              x[nt][2] = fmaf(k1, c[2], x[nt][2]);
+              x[nt][3] = fmaf(k1, c[3], x[nt][3]);
+            }
+          }
+          uint32_t vw[2][NG], vs[NG];
+          load_words<NG>(blk_s + kv4_v_codes(NG) + lane * 4 * NG, vw[0]);
+          load_words<NG>(blk_s + kv4_v_codes(NG) + (32 + lane) * 4 * NG, vw[1]);
+          load_words<NG>(blk_s + kv4_v_scales(NG) + g * 4 * NG, vs);
+          __syncwarp();  // the stage has been read
+          fetch(stage);
+
+          const int key0 = (u.b0 + r) * kKv4Tok;
+          const bool edge = key0 < lo_full || key0 + kKv4Tok > hi_full;
+          uint32_t hidden = 0;  // bit 4 nt + e
+          if (edge) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int col = c_first + 8 * nt + 2 * t + (e & 1), kk = key0 + g + 8 * (e >> 1);
+                int lo, hi;
+                col_range(p, u.len, col, lo, hi);
+                if (col >= p.ncols || kk < lo || kk >= hi) {
+                  hidden |= 1u << (4 * nt + e);
+                  x[nt][e] = -INFINITY;
+                }
+              }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[nt][e] *= p.scale_log2;
+            const float t0 = fmaxf(x[nt][0], x[nt][2]), t1 = fmaxf(x[nt][1], x[nt][3]);
+            if (__any_sync(0xffffffffu, t0 > m[nt][0] + 8.f || t1 > m[nt][1] + 8.f)) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float v = e ? t1 : t0;
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                v = fmaxf(v, m[nt][e]);
+                const float f = m[nt][e] == -INFINITY ? 0.f : exp2f(m[nt][e] - v);
+                m[nt][e] = v;
+                l[nt][e] *= f;
+#pragma unroll
+                for (int j = 0; j < NG; ++j)
+#pragma unroll
+                  for (int a = 0; a < 2; ++a) {
+                    acc[nt][j][a][e] *= f;
+                    acc[nt][j][a][e + 2] *= f;
+                  }
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // x becomes p
+              const float ref = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
+              x[nt][e] = fast_exp2(x[nt][e] - ref);
+            }
+            l[nt][0] += x[nt][0] + x[nt][2];
+            l[nt][1] += x[nt][1] + x[nt][3];
+          }
+#pragma unroll
+          for (int j = 0; j < NG; ++j) {
+            const float v0 = scale_of<NG>(vs, 0, j), v1 = scale_of<NG>(vs, 1, j);
+            uint32_t a[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              a[2 * i] = minus136(nibbles(vw[0][j], i));
+              a[2 * i + 1] = minus136(nibbles(vw[1][j], i));
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float y[4] = {x[nt][0] * v0, x[nt][1] * v0, x[nt][2] * v1, x[nt][3] * v1};
+              if (edge) {  // a hidden token's scale may be anything, NaN too
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if ((hidden >> (4 * nt + e)) & 1u) y[e] = 0.f;
+              }
+              const uint32_t b0 = transpose8x8(pack_bf16x2(y[0], y[1]));
+              const uint32_t b1 = transpose8x8(pack_bf16x2(y[2], y[3]));
+              mma_bf16(acc[nt][j][0], a[0], a[2], a[1], a[3], b0, b1);
+              mma_bf16(acc[nt][j][1], a[4], a[6], a[5], a[7], b0, b1);
+            }
+          }
+        }
+        if (!ok) break;
+
+        // ---- the unit's rows, or this warp's part of them
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int col = c_first + 8 * nt + 2 * t + (e & 1), kk = key + 8 * (e >> 1);
-            int lo, hi;
-            col_range(p, len, col, lo, hi);
-            if (col >= p.ncols || kk < lo || kk >= hi) {
-              hidden |= 1u << (4 * nt + e);
-              x[nt][e] = -INFINITY;
-            }
-          }
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[nt][e] *= p.scale_log2;
-        const float t0 = fmaxf(x[nt][0], x[nt][2]), t1 = fmaxf(x[nt][1], x[nt][3]);
-        if (__any_sync(0xffffffffu, t0 > m[nt][0] + 8.f || t1 > m[nt][1] + 8.f)) {
-#pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float v = e ? t1 : t0;
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-            v = fmaxf(v, m[nt][e]);
-            const float f = m[nt][e] == -INFINITY ? 0.f : exp2f(m[nt][e] - v);
-            m[nt][e] = v;
-            l[nt][e] *= f;
+            l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 4);
+            l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
+            l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
+          }
+        if (r0 <= 0 && r1 >= u.n) {
 #pragma unroll
-            for (int j = 0; j < NG; ++j)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int a = 0; a < 2; ++a) {
-                acc[nt][j][a][e] *= f;
-                acc[nt][j][a][e + 2] *= f;
+            for (int e = 0; e < 2; ++e) {
+              const int cc = 8 * nt + 2 * t + e;
+              if (cc < ncolv) {
+                const float ref = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+#pragma unroll
+                for (int j = 0; j < NG; ++j)
+                  write_out(p, u.b, u.hk, c_first + cc, 32 * j + 4 * g,
+                            make_float4(acc[nt][j][0][e], acc[nt][j][0][e + 2], acc[nt][j][1][e],
+                                        acc[nt][j][1][e + 2]),
+                            ref, l[nt][e]);
+              }
+            }
+        } else {
+          float* part = p.parts + ((int64_t)me * 2 + (r0 > 0 ? 0 : 1)) * p.part_stride;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int cc = 8 * nt + 2 * t + e;
+              if (cc < ncolv) {
+#pragma unroll
+                for (int j = 0; j < NG; ++j)
+                  *reinterpret_cast<float4*>(part + cc * D + 32 * j + 4 * g) =
+                      make_float4(acc[nt][j][0][e], acc[nt][j][0][e + 2], acc[nt][j][1][e],
+                                  acc[nt][j][1][e + 2]);
+                if (g == 0) {
+                  part[p.part_cols * D + cc] = m[nt][e];
+                  part[p.part_cols * D + p.part_cols + cc] = l[nt][e];
+                }
+              }
+            }
+          if (lane == 0) {
+            const int p0 = u.at + kUnitCost;  // position of the unit's first block
+            const int first = r0 > 0 ? me - (-p0 + share - 1) / share : me;
+            const int last = me + (p0 + u.n - 1) / share;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              if (k ? r1 < u.n : (r0 > 0 && warp == 0)) {
+                int* sp = sm.span[k ? warp + 1 : 0];
+                sp[0] = u.b;
+                sp[1] = u.hk;
+                sp[2] = u.cb;
+                sp[3] = first;
+                sp[4] = last;
               }
           }
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {  // x becomes p
-          const float ref = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
-          x[nt][e] = fast_exp2(x[nt][e] - ref);
-        }
-        l[nt][0] += x[nt][0] + x[nt][2];
-        l[nt][1] += x[nt][1] + x[nt][3];
       }
-#pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        const float v0 = scale_of<NG>(r.vs, 0, j), v1 = scale_of<NG>(r.vs, 1, j);
-        uint32_t a[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[2 * i] = minus136(nibbles(r.v[0][j], i));
-          a[2 * i + 1] = minus136(nibbles(r.v[1][j], i));
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float y[4] = {x[nt][0] * v0, x[nt][1] * v0, x[nt][2] * v1, x[nt][3] * v1};
-          if (edge) {  // a hidden token's scale may be anything, NaN too
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if ((hidden >> (4 * nt + e)) & 1u) y[e] = 0.f;
-          }
-          const uint32_t b0 = transpose8x8(pack_bf16x2(y[0], y[1]));
-          const uint32_t b1 = transpose8x8(pack_bf16x2(y[2], y[3]));
-          mma_bf16(acc[nt][j][0], a[0], a[2], a[1], a[3], b0, b1);
-          mma_bf16(acc[nt][j][1], a[4], a[6], a[5], a[7], b0, b1);
-        }
-      }
+      if (u.at + u.n + kUnitCost >= stretch || !next_unit<COLS>(p, u)) break;
     }
-
-    // ---- join the warps: m, l, O of the CTA's part of the unit
-    const bool whole = s0 == 0 && s1 == n;
-    const int first_cta = (int)(unit_w / share), last_cta = (int)((unit_w + n - 1) / share);
-    float* part = p.partials +
-                  ((int64_t)blockIdx.x * 2 + ((int)blockIdx.x == first_cta ? 1 : 0)) *
-                      p.part_stride;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float v = l[nt][e];
-        v += __shfl_xor_sync(0xffffffffu, v, 4);
-        v += __shfl_xor_sync(0xffffffffu, v, 8);
-        v += __shfl_xor_sync(0xffffffffu, v, 16);
-        if (g == 0) {
-          sm_m[warp][8 * nt + 2 * t + e] = m[nt][e];
-          sm_l[warp][8 * nt + 2 * t + e] = v;
-        }
-      }
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int cols = min(8, ncolv - 8 * nt);
-      if (NT > 1 && cols <= 0) break;
-      if (nt > 0) __syncthreads();
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (2 * t + e < cols)
-#pragma unroll
-          for (int j = 0; j < NG; ++j)
-            *reinterpret_cast<float4*>(&sm_o[warp][2 * t + e][32 * j + 4 * g]) =
-                make_float4(acc[nt][j][0][e], acc[nt][j][0][e + 2], acc[nt][j][1][e],
-                            acc[nt][j][1][e + 2]);
-      __syncthreads();
-      for (int i = tid; i < cols * (D / 4); i += kThreads) {
-        const int c = i / (D / 4), f = (i - c * (D / 4)) * 4, cc = 8 * nt + c;
-        float mm = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, sm_m[k][cc]);
-        const float ref = mm == -INFINITY ? 0.f : mm;
-        float ll = 0.f;
-        float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-          const float a = exp2f(sm_m[k][cc] - ref);
-          const float4 v = *reinterpret_cast<const float4*>(&sm_o[k][c][f]);
-          ll = fmaf(a, sm_l[k][cc], ll);
-          oo.x = fmaf(a, v.x, oo.x);
-          oo.y = fmaf(a, v.y, oo.y);
-          oo.z = fmaf(a, v.z, oo.z);
-          oo.w = fmaf(a, v.w, oo.w);
-        }
-        if (whole) {
-          write_out(p, b, hk, c_first + cc, f, oo, ref, ll);
-        } else {
-          *reinterpret_cast<float4*>(part + cc * D + f) = oo;
-          if (f == 0) {
-            part[p.part_cols * D + cc] = mm;
-            part[p.part_cols * D + p.part_cols + cc] = ll;
-          }
-        }
-      }
-    }
-
-    // ---- a unit of several CTAs: the last to arrive joins the parts
-    if (!whole) {
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const unsigned parts = (unsigned)(last_cta - first_cta);  // others than the last
-        sm_last = atomicAdd(p.counters + first_cta, 1u) == parts;
-        if (sm_last) p.counters[first_cta] = 0u;  // ready for the next call
-      }
-      __syncthreads();
-      if (sm_last) {
-        __threadfence();
-        auto part_of = [&](int c) {
-          return p.partials + ((int64_t)c * 2 + (c == first_cta ? 1 : 0)) * p.part_stride;
-        };
-        for (int i = tid; i < ncolv * (D / 4); i += kThreads) {
-          const int cc = i / (D / 4), f = (i - cc * (D / 4)) * 4;
-          float mm = -INFINITY;
-          for (int c = first_cta; c <= last_cta; ++c)
-            mm = fmaxf(mm, __ldcg(part_of(c) + p.part_cols * D + cc));
-          const float ref = mm == -INFINITY ? 0.f : mm;
-          float ll = 0.f;
-          float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int c = first_cta; c <= last_cta; ++c) {
-            const float* pp = part_of(c);
-            const float a = exp2f(__ldcg(pp + p.part_cols * D + cc) - ref);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(pp + cc * D + f));
-            ll = fmaf(a, __ldcg(pp + p.part_cols * D + p.part_cols + cc), ll);
-            oo.x = fmaf(a, v.x, oo.x);
-            oo.y = fmaf(a, v.y, oo.y);
-            oo.z = fmaf(a, v.z, oo.z);
-            oo.w = fmaf(a, v.w, oo.w);
-          }
-          write_out(p, b, hk, c_first + cc, f, oo, ref, ll);
-        }
-      }
-    }
-    __syncthreads();  // the unit's shared memory has been read
-    w += s1 - s0;
-    if (w == seq_base + (long long)per_head * p.Hkv) {
-      seq_base = w;
-      ++b;
+    if (!ok) {  // a copy never came: report it, let what is in flight land
+      *abort_flag = 1;
+      if (lane == 0) atomicOr(&g_dev_error, DEV_ERR_WAIT_TIMEOUT);
+      volatile int no_abort = 0;
+      for (int i = 0; i < kStages; ++i)
+        if (!((bad >> i) & 1u)) mbar_wait(bars + 8 * i, (phase >> i) & 1u, &no_abort, p.wait_ns);
     }
   }
+
+  // ---- units that span warps: the CTA that arrives last joins the parts
+  __threadfence();
+  __syncthreads();
+  if (sm.abort) return;
+  if (tid <= kWarps) {
+    const int first = sm.span[tid][3], last = sm.span[tid][4];
+    bool join = first >= 0 && (tid == 0 || sm.span[tid - 1][3] != first);
+    if (join) {
+      const unsigned others = (unsigned)(last / kWarps - first / kWarps);
+      if (others > 0) {
+        join = atomicAdd(p.counters + first, 1u) == others;
+        if (join) p.counters[first] = 0u;  // ready for the next call
+      }
+    }
+    sm.last[tid] = join;
+  }
+  __syncthreads();
+  __threadfence();
+#pragma unroll 1
+  for (int k = 0; k <= kWarps; ++k)
+    if (sm.last[k]) join_parts<NG, NT>(p, sm.span[k], reinterpret_cast<float*>(sm.ring));
 }
 
 bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
@@ -589,14 +743,25 @@ int part_stride(int64_t ncols, int d) {  // floats: O, then m, then l
   return (part_cols(ncols) * (d + 2) + 3) & ~3;
 }
 
+// CTAs an SM holds at once (registers bound it; __launch_bounds__ asks for it).
+int ctas_per_sm(int nt) { return nt == 1 ? 4 : (nt == 2 ? 3 : 2); }
+
+template <int NG, int NT>
+iha_status launch_nt(const Kv4AttnParams& p, int grid, cudaStream_t s) {
+  static_assert(sizeof(Smem<NG, NT>) <= (NT == 1 ? 55 : (NT == 2 ? 73 : 110)) * 1024,
+                "4-bit attention: the CTAs of an SM do not fit its shared memory");
+  static_assert(sizeof(Smem<NG, NT>::ring) >= kThreads * 6 * sizeof(float), "scratch of the join");
+  static SmemLimit limit;
+  const cudaError_t e = limit.ensure(attn_kv4_kernel<NG, NT>, (int)sizeof(Smem<NG, NT>));
+  if (e != cudaSuccess)
+    return fail(IHA_ERR_CUDA, "mha_fwd_kv4 (smem attribute): %s", cudaGetErrorString(e));
+  attn_kv4_kernel<NG, NT><<<grid, kThreads, sizeof(Smem<NG, NT>), s>>>(p);
+  return check_launch("mha_fwd_kv4");
+}
 template <int NG>
-void launch(const Kv4AttnParams& p, int nt, int grid, cudaStream_t s) {
-  if (nt == 1)
-    attn_kv4_kernel<NG, 1><<<grid, kThreads, 0, s>>>(p);
-  else if (nt == 2)
-    attn_kv4_kernel<NG, 2><<<grid, kThreads, 0, s>>>(p);
-  else
-    attn_kv4_kernel<NG, 4><<<grid, kThreads, 0, s>>>(p);
+iha_status launch(const Kv4AttnParams& p, int nt, int grid, cudaStream_t s) {
+  return nt == 1 ? launch_nt<NG, 1>(p, grid, s)
+                 : (nt == 2 ? launch_nt<NG, 2>(p, grid, s) : launch_nt<NG, 4>(p, grid, s));
 }
 
 }  // namespace
@@ -607,8 +772,9 @@ extern "C" {
 size_t mha_fwd_kv4_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d) {
   if (B <= 0 || Nq <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv || d <= 0) return 0;
   const int64_t ncols = (int64_t)Nq * (Hq / Hkv);
-  return sizeof(unsigned) * iha::kMaxCtas +
-         (size_t)iha::kMaxCtas * 2 * iha::part_stride(ncols, d) * sizeof(float);
+  const int ctas = iha::kMaxCtas * iha::ctas_per_sm(iha::pick_nt(ncols)) / iha::ctas_per_sm(1);
+  return iha::kCounterBytes +
+         (size_t)ctas * iha::kWarps * 2 * iha::part_stride(ncols, d) * sizeof(float);
 }
 
 iha_status mha_fwd_kv4(const void* q, const void* cache, const int32_t* block_table,
@@ -639,7 +805,7 @@ iha_status mha_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
   const int64_t ncols = (int64_t)Nq * G;
   const int nt = pick_nt(ncols);
   const int64_t ncb = (ncols + 8 * nt - 1) / (8 * nt);
-  if (ncols > (1 << 20) || ncb * ((int64_t)table_width * page / kKv4Tok) > INT32_MAX)
+  if (ncols > (1 << 20) || G > 2048 || ncb * ((int64_t)table_width * page / kKv4Tok + kUnitCost) > INT32_MAX)
     return fail(IHA_ERR_UNSUPPORTED, "%s: too many new tokens or keys for one launch", name);
   if (!aligned16(q) || !aligned16(o))
     return fail(IHA_ERR_ALIGNMENT, "%s: q and o must be 16-byte aligned", name);
@@ -690,8 +856,10 @@ iha_status mha_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
   p.G = G;
   p.ncols = (int)ncols;
   p.ncb = (int)ncb;
+  p.inv_g = ((1ull << 32) + G - 1) / G;
+  p.wait_ns = kWaitLimitNs;
   p.counters = static_cast<unsigned*>(workspace);
-  p.partials = reinterpret_cast<float*>(p.counters + kMaxCtas);
+  p.parts = reinterpret_cast<float*>(p.counters + kMaxCtas * kWarps);
   p.part_cols = part_cols(ncols);
   p.part_stride = part_stride(ncols, d);
   p.n_pages = n_pages;
@@ -705,18 +873,22 @@ iha_status mha_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
   p.sq = sq;
   p.so = so;
   // every CTA resident at once; no more of them than there can be work
-  const int64_t most = (int64_t)B * Hkv * ncb * ((int64_t)table_width * page / kKv4Tok);
-  int64_t grid = (int64_t)sm_count() * (nt == 1 ? 4 : (nt == 2 ? 3 : 2));
-  if (grid > (most + kMinBlocks - 1) / kMinBlocks) grid = (most + kMinBlocks - 1) / kMinBlocks;
-  if (grid > kMaxCtas) grid = kMaxCtas;
+  const int64_t most =
+      (int64_t)B * Hkv * ncb * ((int64_t)table_width * page / kKv4Tok + kUnitCost);
+  int64_t grid = (int64_t)sm_count() * ctas_per_sm(nt);
+  const int64_t cap = (int64_t)kMaxCtas * ctas_per_sm(nt) / ctas_per_sm(1);
+  const int64_t useful = (most + kMinShare * kWarps - 1) / (kMinShare * kWarps);
+  if (grid > useful) grid = useful;
+  if (grid > cap) grid = cap;
+  if (most / (grid * kWarps) > (1 << 30))
+    return fail(IHA_ERR_UNSUPPORTED, "%s: too many new tokens or keys for one launch", name);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   switch (d / kKv4Group) {
-    case 1: launch<1>(p, nt, (int)grid, s); break;
-    case 2: launch<2>(p, nt, (int)grid, s); break;
-    case 3: launch<3>(p, nt, (int)grid, s); break;
-    default: launch<4>(p, nt, (int)grid, s); break;
+    case 1: return launch<1>(p, nt, (int)grid, s);
+    case 2: return launch<2>(p, nt, (int)grid, s);
+    case 3: return launch<3>(p, nt, (int)grid, s);
+    default: return launch<4>(p, nt, (int)grid, s);
   }
-  return check_launch(name);
 }
 
 }  // extern "C"
