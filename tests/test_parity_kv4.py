@@ -9,8 +9,13 @@ the result), and a score is off by at most
      + 2^-20 |x|
 (fp32 sums of values up to 143 |q|, a few 2^-23 steps each), which moves p by
 2 dx relative and lse by dx:
-  |o - r|     <= 2^-8 |r| + (2^-8 + 2 dx + 2^-16) sum_j p_j |v_j|
+  |o - r|     <= 2^-8 |r| + (2^-8 + 2 dx + 2^-16) sum_j p_j |v_j| + 2^-11 S
   |lse - r|   <= dx + 2^-20 (1 + |r|).
+S, the largest scale of the group among the keys: up to two columns the codes
+enter the MMAs as n = c + 8 <= 15, and 8 sum p s leaves O every 256 tokens.
+Until then O holds at most 15 S sum p (over those tokens); each of its 16 MMAs
+adds 16 products with at most 17 truncations of 2^-23 of that.  Summed over all
+tokens, with sum p = 1: 16 * 17 * 2^-23 * 15 S < 2^-11 S.
 """
 import math
 
@@ -204,7 +209,10 @@ def check_rows(T, o, lse, q, kv, vv, mask, window, scale=None):
     dx = sc * 143 * 2.0 ** -21 * (qa * np.repeat(s, Hq // Hkv, 0)).sum(-1)       # [Nq, Hq]
     dx = dx + 2.0 ** -20 * sc * 7 * (qa * np.repeat(s, Hq // Hkv, 0)).sum(-1)
     g = to_f64(o)
-    bound = 2.0 ** -8 * np.abs(r) + (2.0 ** -8 + 2 * dx[..., None] + 2.0 ** -16) * ra
+    sv = np.abs(vv).reshape(n, Hkv, d // 32, 32).max(-1).max(0, initial=0.0) / 7
+    S_ = np.repeat(np.repeat(sv, Hq // Hkv, 0), 32, -1)[None]                    # [1, Hq, d]
+    bound = (2.0 ** -8 * np.abs(r) + (2.0 ** -8 + 2 * dx[..., None] + 2.0 ** -16) * ra +
+             2.0 ** -11 * S_)
     assert np.isfinite(g).all()
     err = np.abs(g - r)
     assert (err <= bound).all(), (float((err / np.maximum(bound, 1e-30)).max()),

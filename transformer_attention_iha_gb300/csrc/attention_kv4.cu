@@ -6,19 +6,29 @@
 // One warp works on a block of 16 tokens of one key-value head at a time, for
 // 8 NT columns; a column is one (new token, query head of the group) pair.
 //   S^T [16 tokens x 8 columns] = K Q^T: per group of 32 features two
-//     mma.m16n8k16 with the codes as the A operand.  A nibble n becomes the
-//     bf16 value 128 + n by one OR (exact: 7 mantissa bits), and the
-//     accumulator starts at -136 sum_f q_f, so it ends at sum_f q_f c_f; the
-//     group's scale multiplies it in fp32.
-//   O^T [d x 8 columns] += V^T P^T: the codes c = (128 + n) - 136 are exact in
-//     bf16; the scale of a token and group goes into P: bf16(p s), the one
-//     rounding of this product (2^-9 relative per term, as P has in the bf16
-//     attention).  P^T turns from accumulator to B operand by movmatrix.
+//     mma.m16n8k16 on fp16, with the codes as the A operand.  A nibble n masked
+//     in place is the fp16 subnormal n 2^-24 (or 16 n 2^-24 from the upper half
+//     of a byte; those features of Q are divided by 16): one AND a pair.  The
+//     accumulator starts at -8 2^-24 sum_f q_f, so it ends at 2^-24 sum_f q_f
+//     c_f, and the group's scale multiplies it in fp32.  Q's row is scaled by a
+//     power of two to below 2^15, so that its 8-bit mantissas are exact in fp16
+//     (features below 2^-28 of the largest lose bits).
+//   O^T [d x 8 columns] += V^T P^T, the scale of a token and group inside P:
+//     up to 2 columns (one token of unshared heads, the common case): the 8
+//       columns of the operand hold the 2 columns four times, once per group,
+//       each with its group's scale, so P is scaled, rounded and turned once
+//       instead of four times.  P s F in fp16 (2^-11 a term) with a power of two
+//       F per column and group that keeps it in range, codes as for K; -8 sum P
+//       comes from one more MMA with a constant A operand (the same rounded P)
+//       and is taken out of O every kFlush blocks.
+//     more columns: P s in bf16 (2^-8 a term, as P has in the bf16 attention),
+//       the codes as bf16 (128 + n) - 136, exact.
+//     P^T turns from accumulator to B operand by movmatrix.
 //   Softmax in the log2 domain, fp32; a column's reference maximum moves only
 //   when a score exceeds it by more than 8, then O and the sum are rescaled.
 // Codes are never expanded in memory: 36 NG bytes per token and head are read
-// once, by bulk copies of whole blocks into a ring of kStages blocks that each
-// warp owns, and unpacked in the registers of the lanes that use them.
+// once, by bulk copies of whole blocks into a ring of kStages x kRun blocks that
+// each warp owns, and unpacked in the registers of the lanes that use them.
 //
 // Work is one line of positions: sequence by sequence, head by head, column
 // block by column block (a unit); a unit takes one position per block of 16
@@ -41,7 +51,11 @@ IHA_DEVICE_ERROR_WORD(attention_kv4)
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 4;    // blocks of a warp's ring
+constexpr int kStages = 2;    // a warp's ring: stages of up to kRun blocks
+constexpr int kRun = 2;
+// FEW: the codes' offset leaves O after this many blocks (256 tokens): it costs
+// 32 FMAs, and O has grown by 8 s per unit of probability until then.
+constexpr int kFlush = 16;
 constexpr int kUnitCost = 2;  // positions a unit takes besides its blocks
 // A warp's stretch is at least this long: shorter ones cost more in joining
 // than they save.
@@ -68,6 +82,25 @@ struct Kv4AttnParams {
   uint64_t wait_ns;
 };
 
+// d = a b + c on fp16 or bf16 operands, fp32 accumulators.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1,
+                                        const float (&c)[4]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
+        "f"(c[3]));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -76,12 +109,26 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// Nibbles i and i + 4 of w as the bf16 pair (128 + n, 128 + n').
+// The four nibble pairs of a word (nibble i of each half) as fp16 subnormals:
+// n 2^-24 for i = 0, 2 and 16 n 2^-24 for i = 1, 3.
+__device__ __forceinline__ void nibbles_f16(uint32_t w, uint32_t (&v)[4]) {
+  const uint32_t h = w >> 8;
+  v[0] = w & 0x000F000Fu;
+  v[1] = w & 0x00F000F0u;
+  v[2] = h & 0x000F000Fu;
+  v[3] = h & 0x00F000F0u;
+}
+// Nibble i of each half of w as the bf16 pair (128 + n, 128 + n').
 __device__ __forceinline__ uint32_t nibbles(uint32_t w, int i) {
   return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
 }
@@ -213,9 +260,10 @@ __device__ __forceinline__ bool next_unit(const Kv4AttnParams& p, Unit& u) {
 
 template <int NG, int NT>
 struct Smem {
-  uint8_t ring[kWarps][kStages][kv4_block_bytes(NG)];
+  uint8_t ring[kWarps][kStages][kRun][kv4_block_bytes(NG)];
   uint4 q[NT > 1 ? kWarps : 1][NT > 1 ? NT * NG * 32 : 1];
-  float qc[kWarps][NT * NG][8];  // -136 * sum of a group's q, per column
+  // -8 2^-24 sum of a group's q of columns 2 t and 2 t + 1, twice: an accumulator's start
+  float4 qc[kWarps][NT * NG][4];
   uint64_t full[kWarps][kStages];
   long long scan[kWarps], base[kWarps];
   int seq[kWarps];
@@ -300,13 +348,15 @@ __device__ __forceinline__ void join_parts(const Kv4AttnParams& p, const int* sp
   }
 }
 
-template <int NG, int NT>
+template <int NG, int NT, bool FEW>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
     attn_kv4_kernel(const Kv4AttnParams p) {
   constexpr int D = 32 * NG, COLS = 8 * NT, BYTES = kv4_block_bytes(NG);
+  constexpr int NB = NT == 1 ? 2 : 1;  // blocks computed together (registers allow)
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem<NG, NT>& sm = *reinterpret_cast<Smem<NG, NT>*>(smem_raw);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in the warp, for the compiler too
   volatile int* abort_flag = &sm.abort;
 
   // ---- this warp's stretch of the line
@@ -382,17 +432,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
       u.at = -s;
     }
 
-    // ---- the ring: blocks are fetched kStages ahead, in runs inside one page;
-    // the page id of the run after the current one is read ahead
+    // ---- the ring: stages of up to kRun blocks of one unit, kStages ahead, copied
+    // in runs inside a page; the page id of the run after the current one is
+    // read ahead
     Unit pu = u;
     int pr, pr_end;
     my_blocks(pu, stretch, pr, pr_end);
     bool more = true;
     struct Run {
-      int id, head, in_page, cnt;
+      int id, head, in_page, cnt;  // cnt blocks of the page, 0: no more
+      int left;                    // blocks of the unit from this run on
     };
     auto next_run = [&]() {
-      Run r = {0, 0, 0, 0};
+      Run r = {0, 0, 0, 0, 0};
       while (more && pr >= pr_end) {
         more = pu.at + pu.n + kUnitCost < stretch && next_unit<COLS>(p, pu);
         if (more) my_blocks(pu, stretch, pr, pr_end);
@@ -400,37 +452,56 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
       if (more) {
         const int blk = pu.b0 + pr, pi = blk / p.blocks_per_page;
         r.in_page = blk - pi * p.blocks_per_page;
-        r.cnt = min(p.blocks_per_page - r.in_page, pr_end - pr);
+        r.left = pr_end - pr;
+        r.cnt = min(p.blocks_per_page - r.in_page, r.left);
         r.head = pu.hk;
         r.id = __ldg(p.table + (int64_t)pu.b * p.table_w + pi);
         pr += r.cnt;
       }
       return r;
     };
-    Run run = next_run(), run_next = next_run();
-    uint32_t bad = 0, phase = 0;  // stages with no copy under way; parity of the barriers
+    Run run, run_next = next_run();
+    const uint8_t* src = nullptr;  // the run's next block; null: no such page
+    auto take_run = [&]() {
+      run = run_next;
+      if (run.cnt > 0) {
+        run_next = next_run();
+        const bool in = run.id >= 0 && run.id < p.n_pages;
+        if (!in && lane == 0) atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
+        src = in ? p.cache + kv4_block_of(run.id, run.in_page, run.head, p.Hkv, p.blocks_per_page,
+                                          NG)
+                 : nullptr;
+      }
+    };
+    take_run();
+    // bit per block of the ring: no such page; bit per stage: copies under way,
+    // and the parity of its barrier
+    uint32_t bad = 0, flying = 0, phase = 0;
     const uint32_t ring = smem_u32(sm.ring[warp]), bars = smem_u32(sm.full[warp]);
     auto fetch = [&](int stage) {
-      bad |= 1u << stage;
-      if (run.cnt == 0) {
-        run = run_next;
-        if (run.cnt == 0) return;
-        run_next = next_run();
-      }
-      if (run.id >= 0 && run.id < p.n_pages) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bars + 8 * stage, BYTES);
-          bulk_load(ring + stage * BYTES,
-                    p.cache + kv4_block_of(run.id, run.in_page, run.head, p.Hkv, p.blocks_per_page,
-                                           NG),
-                    BYTES, bars + 8 * stage);
+      bad &= ~(((1u << kRun) - 1u) << (stage * kRun));
+      flying &= ~(1u << stage);
+      if (run.cnt == 0) return;
+      const int want = min(kRun, run.left);
+      uint32_t bytes = 0;
+      int have = 0;
+      do {
+        const int c = min(want - have, run.cnt);
+        if (src != nullptr) {
+          if (lane == 0)
+            bulk_load(ring + (stage * kRun + have) * BYTES, src, c * BYTES, bars + 8 * stage);
+          bytes += c * BYTES;
+          src += c * BYTES;
+        } else {
+          bad |= ((1u << c) - 1u) << (stage * kRun + have);
         }
-        bad ^= 1u << stage;
-      } else if (lane == 0) {
-        atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
-      }
-      ++run.in_page;
-      --run.cnt;
+        have += c;
+        run.cnt -= c;
+        run.left -= c;
+        if (run.cnt == 0) take_run();
+      } while (have < want);
+      if (lane == 0) mbar_arrive_expect_tx(bars + 8 * stage, bytes);
+      flying |= 1u << stage;
     };
 #pragma unroll 1
     for (int i = 0; i < kStages; ++i) fetch(i);
@@ -448,49 +519,76 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
         col_range(p, u.len, c_first, x_, hi_full);
         col_range(p, u.len, c_first + ncolv - 1, lo_full, x_);
 
-        // Q as B operand: column 8 nt + g, feature pairs (i, i + 4) of octet t
+        // Q as B operand: column 8 nt + g (FEW: column g % 2), feature pairs
+        // (i, i + 4) of octet t, those of odd i divided by 16
         uint32_t qf[NT == 1 ? NG : 1][4];
-        __syncwarp();  // the Q of the unit before has been read
+        float cm[NT][2];  // accumulators of columns 2 t, 2 t + 1 to scores, log2 domain
+        __syncwarp();     // the Q of the unit before has been read
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const int col = c_first + 8 * nt + g;
+          const int col = c_first + 8 * nt + (FEW ? g & 1 : g);
           const bool in = col < p.ncols;
           const int qi = in ? token_of(p, col) : 0, qh = u.hk * p.G + (in ? col - qi * p.G : 0);
           const __nv_bfloat16* qp =
               p.q + u.b * p.sq.b_outer + qi * p.sq.seq + qh * p.sq.head + 8 * t;
           uint4 v[NG];
+          uint32_t top = 0;
 #pragma unroll
           for (int j = 0; j < NG; ++j)
             v[j] = in ? __ldg(reinterpret_cast<const uint4*>(qp + 32 * j)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
           for (int j = 0; j < NG; ++j) {
-            const uint32_t f0 = __byte_perm(v[j].x, v[j].z, 0x5410);
-            const uint32_t f1 = __byte_perm(v[j].x, v[j].z, 0x7632);
-            const uint32_t f2 = __byte_perm(v[j].y, v[j].w, 0x5410);
-            const uint32_t f3 = __byte_perm(v[j].y, v[j].w, 0x7632);
+            top = __vmaxu2(top, __vmaxu2(v[j].x & 0x7FFF7FFFu, v[j].y & 0x7FFF7FFFu));
+            top = __vmaxu2(top, __vmaxu2(v[j].z & 0x7FFF7FFFu, v[j].w & 0x7FFF7FFFu));
+          }
+          top = max(top & 0xFFFFu, top >> 16);
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // largest |q| in [2^e, 2^(e + 1)): Q is scaled by 2^(14 - e)
+          const int e = max((int)(top >> 7) - 127, -112);
+          const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+          // above 0: a hidden score is -inf times this
+          const float back = fmaxf(ldexpf(p.scale_log2, e + 10), 1.1754944e-38f);
+          cm[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);
+          cm[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+#pragma unroll
+          for (int j = 0; j < NG; ++j) {
+            const float f0 = bf16lo_to_f32(v[j].x) * up, f1 = bf16hi_to_f32(v[j].x) * up;
+            const float f2 = bf16lo_to_f32(v[j].y) * up, f3 = bf16hi_to_f32(v[j].y) * up;
+            const float f4 = bf16lo_to_f32(v[j].z) * up, f5 = bf16hi_to_f32(v[j].z) * up;
+            const float f6 = bf16lo_to_f32(v[j].w) * up, f7 = bf16hi_to_f32(v[j].w) * up;
+            const uint32_t h0 = pack_f16x2(f0, f4), h1 = pack_f16x2(f1 * 0.0625f, f5 * 0.0625f);
+            const uint32_t h2 = pack_f16x2(f2, f6), h3 = pack_f16x2(f3 * 0.0625f, f7 * 0.0625f);
             if constexpr (NT == 1) {
-              qf[j][0] = f0;
-              qf[j][1] = f1;
-              qf[j][2] = f2;
-              qf[j][3] = f3;
+              qf[j][0] = h0;
+              qf[j][1] = h1;
+              qf[j][2] = h2;
+              qf[j][3] = h3;
             } else {
-              sm.q[warp][(nt * NG + j) * 32 + lane] = make_uint4(f0, f1, f2, f3);
+              sm.q[warp][(nt * NG + j) * 32 + lane] = make_uint4(h0, h1, h2, h3);
             }
-            float s = bf16lo_to_f32(v[j].x) + bf16hi_to_f32(v[j].x) + bf16lo_to_f32(v[j].y) +
-                      bf16hi_to_f32(v[j].y) + bf16lo_to_f32(v[j].z) + bf16hi_to_f32(v[j].z) +
-                      bf16lo_to_f32(v[j].w) + bf16hi_to_f32(v[j].w);
+            float s = ((f0 + f1) + (f2 + f3)) + ((f4 + f5) + (f6 + f7));
             s += __shfl_xor_sync(0xffffffffu, s, 1);
             s += __shfl_xor_sync(0xffffffffu, s, 2);
-            if (t == 0) sm.qc[warp][nt * NG + j][g] = -136.f * s;
+            if (t == 0) {  // column g of the pair (g & ~1, g | 1)
+              float* c = reinterpret_cast<float*>(&sm.qc[warp][nt * NG + j][g >> 1]) + (g & 1);
+              c[0] = c[2] = -4.76837158203125e-07f * s;  // -8 2^-24
+            }
           }
         }
         __syncwarp();
 
-        float m[NT][2], l[NT][2];
+        // running maximum m of a column: mlim = m + 8, mref = m, or 0 while no key
+        // has been seen (m = -inf)
+        float mlim[NT][2], mref[NT][2], l[NT][2];
+        float off[4] = {0.f, 0.f, 0.f, 0.f};  // FEW: -8 2^-24 sum P since the last flush
+        float F[2] = {0.f, 0.f}, F_lim[2];  // FEW: see below; lanes without a group never ask
+        F_lim[0] = F_lim[1] = t < NG ? -1.f : INFINITY;
         float acc[NT][NG][2][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          m[nt][0] = m[nt][1] = -INFINITY;
+          mlim[nt][0] = mlim[nt][1] = -INFINITY;
+          mref[nt][0] = mref[nt][1] = 0.f;
           l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
           for (int j = 0; j < NG; ++j)
@@ -500,134 +598,253 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
               for (int e = 0; e < 4; ++e) acc[nt][j][a][e] = 0.f;
         }
 
+        auto flush = [&]() {  // take the codes' offset out of O
+#pragma unroll
+          for (int j = 0; j < NG; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                acc[0][j][h][e] += off[e];
+                acc[0][j][h][e + 2] = fmaf(16.f, off[e], acc[0][j][h][e + 2]);
+              }
+          off[0] = off[1] = off[2] = off[3] = 0.f;
+        };
+        // blocks r with rf0 <= r - b0 < rf0 + rf_n are visible to every column
+        const int rf0 = (lo_full + kKv4Tok - 1) / kKv4Tok - u.b0;
+        const unsigned rf_n = (unsigned)max(0, (hi_full >> 4) - u.b0 - rf0);
 #pragma unroll 1
-        for (int r = r0; r < r1; ++r, stage = stage + 1 == kStages ? 0 : stage + 1) {
-          if ((bad >> stage) & 1u) {  // no such page: its keys are hidden
-            fetch(stage);
-            continue;
-          }
+        for (int r = r0; r < r1; r += kRun) {
           if (!mbar_wait_warp(bars + 8 * stage, (phase >> stage) & 1u, abort_flag, p.wait_ns)) {
             ok = false;
             break;
           }
           phase ^= 1u << stage;
-          const uint8_t* blk_s = sm.ring[warp][stage];
-          uint32_t kw[2][NG], ks[NG];
-          load_words<NG>(blk_s + lane * 4 * NG, kw[0]);
-          load_words<NG>(blk_s + (32 + lane) * 4 * NG, kw[1]);
-          load_words<NG>(blk_s + kv4_k_scales(NG) + g * 4 * NG, ks);
-          float x[NT][4];  // (token g, columns 2t, 2t+1), (token g + 8, ...)
+          // blocks of the stage that no page holds, or past the unit's end, are
+          // computed like the others and hidden
+          uint32_t gone = (bad >> (stage * kRun)) & ((1u << kRun) - 1u);
+          if (r1 - r < kRun) gone |= ~0u << (r1 - r);
+#pragma unroll 1
+          for (int k0 = 0; k0 < kRun; k0 += NB) {
+            const int rk = r + k0;
+            if (NB < kRun && rk >= r1) break;
+            const uint8_t* blk_s = sm.ring[warp][stage][k0];
+            float x[NT][NB][4];  // (token g, columns 2t, 2t+1), (token g + 8, ...)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+            for (int b = 0; b < NB; ++b) {
+              uint32_t kw[2][NG], ks[NG];
+              load_words<NG>(blk_s + b * BYTES + lane * 4 * NG, kw[0]);
+              load_words<NG>(blk_s + b * BYTES + (32 + lane) * 4 * NG, kw[1]);
+              load_words<NG>(blk_s + b * BYTES + kv4_k_scales(NG) + g * 4 * NG, ks);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[nt][e] = 0.f;
+              for (int j = 0; j < NG; ++j) {
+                uint32_t a[4], c8[4];  // rows g and g + 8
+                nibbles_f16(kw[0][j], a);
+                nibbles_f16(kw[1][j], c8);
+                const float k0_ = scale_of<NG>(ks, 0, j), k1_ = scale_of<NG>(ks, 1, j);
 #pragma unroll
-          for (int j = 0; j < NG; ++j) {
-            uint32_t a[8];
+                for (int nt = 0; nt < NT; ++nt) {
+                  const float4 q4 = sm.qc[warp][nt * NG + j][t];
+                  const float c0[4] = {q4.x, q4.y, q4.z, q4.w};
+                  float c[4], d[4];
+                  if constexpr (NT == 1) {
+                    mma_f16(c, a[0], c8[0], a[1], c8[1], qf[j][0], qf[j][1], c0);
+                    mma_f16(d, a[2], c8[2], a[3], c8[3], qf[j][2], qf[j][3], c);
+                  } else {
+                    const uint4 f = sm.q[warp][(nt * NG + j) * 32 + lane];
+                    mma_f16(c, a[0], c8[0], a[1], c8[1], f.x, f.y, c0);
+                    mma_f16(d, a[2], c8[2], a[3], c8[3], f.z, f.w, c);
+                  }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              a[2 * i] = nibbles(kw[0][j], i);
-              a[2 * i + 1] = nibbles(kw[1][j], i);
-            }
-            const float k0 = scale_of<NG>(ks, 0, j), k1 = scale_of<NG>(ks, 1, j);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const float2 qc = *reinterpret_cast<const float2*>(&sm.qc[warp][nt * NG + j][2 * t]);
-              float c[4] = {qc.x, qc.y, qc.x, qc.y};
-              if constexpr (NT == 1) {
-                mma_bf16(c, a[0], a[1], a[2], a[3], qf[j][0], qf[j][1]);
-                mma_bf16(c, a[4], a[5], a[6], a[7], qf[j][2], qf[j][3]);
-              } else {
-                const uint4 f = sm.q[warp][(nt * NG + j) * 32 + lane];
-                mma_bf16(c, a[0], a[1], a[2], a[3], f.x, f.y);
-                mma_bf16(c, a[4], a[5], a[6], a[7], f.z, f.w);
-              }
-              x[nt][0] = fmaf(k0, c[0], x[nt][0]);
-              x[nt][1] = fmaf(k0, c[1], x[nt][1]);
-              x[nt][2] = fmaf(k1, c[2], x[nt][2]);
-              x[nt][3] = fmaf(k1, c[3], x[nt][3]);
-            }
-          }
-          uint32_t vw[2][NG], vs[NG];
-          load_words<NG>(blk_s + kv4_v_codes(NG) + lane * 4 * NG, vw[0]);
-          load_words<NG>(blk_s + kv4_v_codes(NG) + (32 + lane) * 4 * NG, vw[1]);
-          load_words<NG>(blk_s + kv4_v_scales(NG) + g * 4 * NG, vs);
-          __syncwarp();  // the stage has been read
-          fetch(stage);
-
-          const int key0 = (u.b0 + r) * kKv4Tok;
-          const bool edge = key0 < lo_full || key0 + kKv4Tok > hi_full;
-          uint32_t hidden = 0;  // bit 4 nt + e
-          if (edge) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int col = c_first + 8 * nt + 2 * t + (e & 1), kk = key0 + g + 8 * (e >> 1);
-                int lo, hi;
-                col_range(p, u.len, col, lo, hi);
-                if (col >= p.ncols || kk < lo || kk >= hi) {
-                  hidden |= 1u << (4 * nt + e);
-                  x[nt][e] = -INFINITY;
+                  for (int e = 0; e < 4; ++e)
+                    x[nt][b][e] = j == 0 ? (e < 2 ? k0_ : k1_) * d[e]
+                                         : fmaf(e < 2 ? k0_ : k1_, d[e], x[nt][b][e]);
                 }
               }
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[nt][e] *= p.scale_log2;
-            const float t0 = fmaxf(x[nt][0], x[nt][2]), t1 = fmaxf(x[nt][1], x[nt][3]);
-            if (__any_sync(0xffffffffu, t0 > m[nt][0] + 8.f || t1 > m[nt][1] + 8.f)) {
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float v = e ? t1 : t0;
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                v = fmaxf(v, m[nt][e]);
-                const float f = m[nt][e] == -INFINITY ? 0.f : exp2f(m[nt][e] - v);
-                m[nt][e] = v;
-                l[nt][e] *= f;
-#pragma unroll
-                for (int j = 0; j < NG; ++j)
-#pragma unroll
-                  for (int a = 0; a < 2; ++a) {
-                    acc[nt][j][a][e] *= f;
-                    acc[nt][j][a][e + 2] *= f;
-                  }
-              }
             }
+
+            const bool edge = (unsigned)(rk - rf0) >= rf_n || (unsigned)(rk + NB - 1 - rf0) >= rf_n ||
+                              gone != 0;
+            uint32_t hidden = 0;  // bit 4 (nt NB + b) + e
+            if (edge) {
+              const int key = (u.b0 + rk) * kKv4Tok + g;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {  // x becomes p
-              const float ref = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
-              x[nt][e] = fast_exp2(x[nt][e] - ref);
-            }
-            l[nt][0] += x[nt][0] + x[nt][2];
-            l[nt][1] += x[nt][1] + x[nt][3];
-          }
+              for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < NG; ++j) {
-            const float v0 = scale_of<NG>(vs, 0, j), v1 = scale_of<NG>(vs, 1, j);
-            uint32_t a[8];
+                for (int e = 0; e < 2; ++e) {
+                  const int col = c_first + (FEW ? e : 8 * nt + 2 * t + e);
+                  int lo, hi;
+                  col_range(p, u.len, col, lo, hi);
+                  if (col >= p.ncols) hi = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              a[2 * i] = minus136(nibbles(vw[0][j], i));
-              a[2 * i + 1] = minus136(nibbles(vw[1][j], i));
+                  for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                      const int kk = key + b * kKv4Tok + 8 * h;
+                      if (kk < lo || kk >= hi || ((gone >> (k0 + b)) & 1u)) {
+                        hidden |= 1u << (4 * (nt * NB + b) + 2 * h + e);
+                        x[nt][b][2 * h + e] = -INFINITY;
+                      }
+                    }
+                }
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              float y[4] = {x[nt][0] * v0, x[nt][1] * v0, x[nt][2] * v1, x[nt][3] * v1};
+              float top[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                top[e] = fmaxf(x[nt][0][e], x[nt][0][e + 2]);
+#pragma unroll
+                for (int b = 1; b < NB; ++b)
+                  top[e] = fmax3f(top[e], x[nt][b][e], x[nt][b][e + 2]);
+                top[e] *= cm[nt][e];
+              }
+              if (__any_sync(0xffffffffu, top[0] > mlim[nt][0] || top[1] > mlim[nt][1])) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  float v = top[e];
+                  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                  if (mlim[nt][e] != -INFINITY) v = fmaxf(v, mref[nt][e]);
+                  const float ref = v == -INFINITY ? 0.f : v;
+                  const float f = mlim[nt][e] == -INFINITY ? 0.f : exp2f(mref[nt][e] - ref);
+                  mlim[nt][e] = v + 8.f;
+                  mref[nt][e] = ref;
+                  l[nt][e] *= f;
+                  if constexpr (FEW) off[e] *= f;
+#pragma unroll
+                  for (int j = 0; j < NG; ++j)
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) {
+                      acc[nt][j][a][e] *= f;
+                      acc[nt][j][a][e + 2] *= f;
+                    }
+                }
+              }
+#pragma unroll
+              for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)  // x becomes p
+                  x[nt][b][e] = fast_exp2(fmaf(x[nt][b][e], cm[nt][e & 1], -mref[nt][e & 1]));
+                l[nt][0] += x[nt][b][0] + x[nt][b][2];
+                l[nt][1] += x[nt][b][1] + x[nt][b][3];
+              }
+            }
+            if constexpr (FEW) {
+              // w = p s of this lane's group; P = w F.  F is 0 until the first
+              // w > 0 of the column and group, then a power of two that keeps
+              // the largest w F so far between 1 and 2^15.
+              float w[NB][4];
+#pragma unroll
+              for (int b = 0; b < NB; ++b) {
+                float f0 = 0.f, f1 = 0.f;  // scales of tokens g, g + 8 in group t
+                if (NG == 4 || t < NG) {
+                  const uint16_t* sp = reinterpret_cast<const uint16_t*>(blk_s + b * BYTES +
+                                                                         kv4_v_scales(NG)) +
+                                       g * 2 * NG + t;
+                  f0 = __uint_as_float((uint32_t)sp[0] << 16);
+                  f1 = __uint_as_float((uint32_t)sp[NG] << 16);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[b][e] = x[0][b][e] * (e < 2 ? f0 : f1);
+              }
               if (edge) {  // a hidden token's scale may be anything, NaN too
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if ((hidden >> (4 * nt + e)) & 1u) y[e] = 0.f;
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    if ((hidden >> (4 * b + e)) & 1u) w[b][e] = 0.f;
               }
-              const uint32_t b0 = transpose8x8(pack_bf16x2(y[0], y[1]));
-              const uint32_t b1 = transpose8x8(pack_bf16x2(y[2], y[3]));
-              mma_bf16(acc[nt][j][0], a[0], a[2], a[1], a[3], b0, b1);
-              mma_bf16(acc[nt][j][1], a[4], a[6], a[5], a[7], b0, b1);
+              float top[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                top[e] = fmaxf(w[0][e], w[0][e + 2]);
+#pragma unroll
+                for (int b = 1; b < NB; ++b) top[e] = fmax3f(top[e], w[b][e], w[b][e + 2]);
+              }
+              if (__any_sync(0xffffffffu, top[0] * F[0] > F_lim[0] || top[1] * F[1] > F_lim[1])) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  float v = top[e];
+                  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                  // 2^-(exponent of v), from its bits; v is 0 or positive, infinite at most
+                  const int ex = max((int)(__float_as_uint(v) >> 23), 1);
+                  const float to = __uint_as_float((uint32_t)max(254 - ex, 1) << 23);
+                  if (v > 0.f && (F[e] == 0.f || to < F[e])) {
+                    const float f = F[e] == 0.f ? 0.f : to / F[e];
+                    F[e] = to;
+                    F_lim[e] = 32768.f;
+                    off[e] *= f;
+#pragma unroll
+                    for (int j = 0; j < NG; ++j)
+#pragma unroll
+                      for (int a = 0; a < 2; ++a) {
+                        acc[0][j][a][e] *= f;
+                        acc[0][j][a][e + 2] *= f;
+                      }
+                  }
+                }
+              }
+#pragma unroll
+              for (int b = 0; b < NB; ++b) {
+                uint32_t vw[2][NG];
+                load_words<NG>(blk_s + b * BYTES + kv4_v_codes(NG) + lane * 4 * NG, vw[0]);
+                load_words<NG>(blk_s + b * BYTES + kv4_v_codes(NG) + (32 + lane) * 4 * NG, vw[1]);
+                const uint32_t b0 = transpose8x8(pack_f16x2(w[b][0] * F[0], w[b][1] * F[1]));
+                const uint32_t b1 = transpose8x8(pack_f16x2(w[b][2] * F[0], w[b][3] * F[1]));
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                  uint32_t a[4], c8[4];  // tokens 2 t, 2 t + 1 of each half
+                  nibbles_f16(vw[0][j], a);
+                  nibbles_f16(vw[1][j], c8);
+#pragma unroll
+                  for (int h = 0; h < 2; ++h)  // feature rows i = 2 h and 2 h + 1 (16 times)
+                    mma_f16(acc[0][j][h], a[2 * h], a[2 * h + 1], c8[2 * h], c8[2 * h + 1], b0, b1);
+                }
+                mma_f16(off, 0x80088008u, 0x80088008u, 0x80088008u, 0x80088008u, b0, b1);
+              }
+              if (((rk - r0) & (kFlush - NB)) == kFlush - NB) flush();
+            } else {
+#pragma unroll
+              for (int b = 0; b < NB; ++b) {
+                uint32_t vw[2][NG], vs[NG];
+                load_words<NG>(blk_s + b * BYTES + kv4_v_codes(NG) + lane * 4 * NG, vw[0]);
+                load_words<NG>(blk_s + b * BYTES + kv4_v_codes(NG) + (32 + lane) * 4 * NG, vw[1]);
+                load_words<NG>(blk_s + b * BYTES + kv4_v_scales(NG) + g * 4 * NG, vs);
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                  const float v0 = scale_of<NG>(vs, 0, j), v1 = scale_of<NG>(vs, 1, j);
+                  uint32_t a[8];
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    a[2 * i] = minus136(nibbles(vw[0][j], i));
+                    a[2 * i + 1] = minus136(nibbles(vw[1][j], i));
+                  }
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) {
+                    float y[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = x[nt][b][e] * (e < 2 ? v0 : v1);
+                    if (edge) {
+#pragma unroll
+                      for (int e = 0; e < 4; ++e)
+                        if ((hidden >> (4 * (nt * NB + b) + e)) & 1u) y[e] = 0.f;
+                    }
+                    const uint32_t b0 = transpose8x8(pack_bf16x2(y[0], y[1]));
+                    const uint32_t b1 = transpose8x8(pack_bf16x2(y[2], y[3]));
+                    mma_bf16(acc[nt][j][0], a[0], a[2], a[1], a[3], b0, b1);
+                    mma_bf16(acc[nt][j][1], a[4], a[6], a[5], a[7], b0, b1);
+                  }
+                }
+              }
             }
           }
+          __syncwarp();  // the stage has been read
+          fetch(stage);
+          stage = stage + 1 == kStages ? 0 : stage + 1;
         }
         if (!ok) break;
 
@@ -640,41 +857,55 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
             l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
             l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
           }
-        if (r0 <= 0 && r1 >= u.n) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int cc = 8 * nt + 2 * t + e;
-              if (cc < ncolv) {
-                const float ref = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
-#pragma unroll
-                for (int j = 0; j < NG; ++j)
-                  write_out(p, u.b, u.hk, c_first + cc, 32 * j + 4 * g,
-                            make_float4(acc[nt][j][0][e], acc[nt][j][0][e + 2], acc[nt][j][1][e],
-                                        acc[nt][j][1][e + 2]),
-                            ref, l[nt][e]);
-              }
+        const bool whole = r0 <= 0 && r1 >= u.n;
+        float* part = p.parts + ((int64_t)me * 2 + (r0 > 0 ? 0 : 1)) * p.part_stride;
+        // features 32 j + 4 g .. + 3 of column cc
+        auto put = [&](int cc, int j, float4 o, float lim, float ref, float ll) {
+          if (whole) {
+            write_out(p, u.b, u.hk, c_first + cc, 32 * j + 4 * g, o, ref, ll);
+          } else {
+            *reinterpret_cast<float4*>(part + cc * D + 32 * j + 4 * g) = o;
+            if (j == 0 && g == 0) {
+              part[p.part_cols * D + cc] = lim == -INFINITY ? lim : ref;
+              part[p.part_cols * D + p.part_cols + cc] = ll;
             }
+          }
+        };
+        if constexpr (FEW) {  // lane t holds group t
+          flush();
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < NG; ++j)
+              if (t == j) {
+                o[0] = acc[0][j][0][e];
+                o[1] = acc[0][j][0][e + 2];
+                o[2] = acc[0][j][1][e];
+                o[3] = acc[0][j][1][e + 2];
+              }
+            // F = 0: every w was 0 (or NaN, and O is NaN)
+            const float f = F[e] == 0.f ? 1.f : 16777216.f / F[e], h = f * 0.0625f;
+            if (t < NG && e < ncolv)
+              put(e, t, make_float4(o[0] * f, o[1] * h, o[2] * f, o[3] * h), mlim[0][e], mref[0][e],
+                  l[0][e]);
+          }
         } else {
-          float* part = p.parts + ((int64_t)me * 2 + (r0 > 0 ? 0 : 1)) * p.part_stride;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int cc = 8 * nt + 2 * t + e;
-              if (cc < ncolv) {
+              if (cc < ncolv)
 #pragma unroll
                 for (int j = 0; j < NG; ++j)
-                  *reinterpret_cast<float4*>(part + cc * D + 32 * j + 4 * g) =
+                  put(cc, j,
                       make_float4(acc[nt][j][0][e], acc[nt][j][0][e + 2], acc[nt][j][1][e],
-                                  acc[nt][j][1][e + 2]);
-                if (g == 0) {
-                  part[p.part_cols * D + cc] = m[nt][e];
-                  part[p.part_cols * D + p.part_cols + cc] = l[nt][e];
-                }
-              }
+                                  acc[nt][j][1][e + 2]),
+                      mlim[nt][e], mref[nt][e], l[nt][e]);
             }
+        }
+        if (!whole) {
           if (lane == 0) {
             const int p0 = u.at + kUnitCost;  // position of the unit's first block
             const int first = r0 > 0 ? me - (-p0 + share - 1) / share : me;
@@ -699,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
       if (lane == 0) atomicOr(&g_dev_error, DEV_ERR_WAIT_TIMEOUT);
       volatile int no_abort = 0;
       for (int i = 0; i < kStages; ++i)
-        if (!((bad >> i) & 1u)) mbar_wait(bars + 8 * i, (phase >> i) & 1u, &no_abort, p.wait_ns);
+        if ((flying >> i) & 1u) mbar_wait(bars + 8 * i, (phase >> i) & 1u, &no_abort, p.wait_ns);
     }
   }
 
@@ -746,22 +977,23 @@ int part_stride(int64_t ncols, int d) {  // floats: O, then m, then l
 // CTAs an SM holds at once (registers bound it; __launch_bounds__ asks for it).
 int ctas_per_sm(int nt) { return nt == 1 ? 4 : (nt == 2 ? 3 : 2); }
 
-template <int NG, int NT>
+template <int NG, int NT, bool FEW>
 iha_status launch_nt(const Kv4AttnParams& p, int grid, cudaStream_t s) {
   static_assert(sizeof(Smem<NG, NT>) <= (NT == 1 ? 55 : (NT == 2 ? 73 : 110)) * 1024,
                 "4-bit attention: the CTAs of an SM do not fit its shared memory");
   static_assert(sizeof(Smem<NG, NT>::ring) >= kThreads * 6 * sizeof(float), "scratch of the join");
   static SmemLimit limit;
-  const cudaError_t e = limit.ensure(attn_kv4_kernel<NG, NT>, (int)sizeof(Smem<NG, NT>));
+  const cudaError_t e = limit.ensure(attn_kv4_kernel<NG, NT, FEW>, (int)sizeof(Smem<NG, NT>));
   if (e != cudaSuccess)
     return fail(IHA_ERR_CUDA, "mha_fwd_kv4 (smem attribute): %s", cudaGetErrorString(e));
-  attn_kv4_kernel<NG, NT><<<grid, kThreads, sizeof(Smem<NG, NT>), s>>>(p);
+  attn_kv4_kernel<NG, NT, FEW><<<grid, kThreads, sizeof(Smem<NG, NT>), s>>>(p);
   return check_launch("mha_fwd_kv4");
 }
 template <int NG>
 iha_status launch(const Kv4AttnParams& p, int nt, int grid, cudaStream_t s) {
-  return nt == 1 ? launch_nt<NG, 1>(p, grid, s)
-                 : (nt == 2 ? launch_nt<NG, 2>(p, grid, s) : launch_nt<NG, 4>(p, grid, s));
+  if (p.ncols <= 2) return launch_nt<NG, 1, true>(p, grid, s);
+  if (nt == 1) return launch_nt<NG, 1, false>(p, grid, s);
+  return nt == 2 ? launch_nt<NG, 2, false>(p, grid, s) : launch_nt<NG, 4, false>(p, grid, s);
 }
 
 }  // namespace
