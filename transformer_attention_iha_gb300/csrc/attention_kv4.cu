@@ -38,8 +38,9 @@
 // batch and many short ones all fill the GPU, and a warp's ring runs on across
 // units.  Lengths are read on the device (each CTA sums them up), so a captured
 // call replays with other lengths.  A unit that lies in one warp's stretch is
-// finished by that warp; one that spans several leaves parts (m, l, O in fp32)
-// in the workspace, and the CTA that finishes last joins them in order.
+// finished by that warp; one that spans several is joined from the warps' parts
+// (m, l, O in fp32), first inside each CTA, then, if it spans CTAs, through the
+// workspace by the CTA that arrives last, always in the order of the line.
 #include <math.h>
 
 #include "kv4.cuh"
@@ -56,12 +57,13 @@ constexpr int kRun = 2;
 // FEW: the codes' offset leaves O after this many blocks (256 tokens): it costs
 // 32 FMAs, and O has grown by 8 s per unit of probability until then.
 constexpr int kFlush = 16;
-constexpr int kUnitCost = 2;  // positions a unit takes besides its blocks
+constexpr int kUnitCost = 4;  // positions a unit takes besides its blocks
 // A warp's stretch is at least this long: shorter ones cost more in joining
 // than they save.
 constexpr int kMinShare = 4;
 constexpr int kMaxCtas = 640;  // counters for 152 SMs x 4 CTAs and some
-constexpr int kCounterBytes = kMaxCtas * kWarps * 4;
+constexpr int kCounterBytes = kMaxCtas * 4;
+constexpr int kCtaParts = 2 + 2 * kWarps;
 
 struct Kv4AttnParams {
   const __nv_bfloat16* q;
@@ -70,8 +72,9 @@ struct Kv4AttnParams {
   const int32_t* lens;
   __nv_bfloat16* o;
   float* lse;
-  unsigned* counters;  // [kMaxCtas * kWarps], zero between calls
-  float* parts;        // [warps of the grid][2][part_stride]
+  unsigned* counters;  // [kMaxCtas], zero between calls
+  float* parts;        // [CTAs][2 + 2 kWarps][part_stride]: units begun before the CTA and
+                       // in it; heads and tails of its warps that shared memory cannot hold
   int part_cols, part_stride;
   int B, Nq, Hq, Hkv, G, ncols, ncb;  // ncols = Nq * G columns of a key-value head, in ncb blocks
   unsigned long long inv_g;           // ceil(2^32 / G): col / G = col * inv_g >> 32
@@ -219,19 +222,6 @@ __device__ __forceinline__ int head_positions(const Kv4AttnParams& p, int len) {
   return sum;
 }
 
-// Sum over the CTA; every thread gets it (s: kWarps entries).
-__device__ __forceinline__ long long cta_sum(long long v, long long* s) {
-#pragma unroll
-  for (int k = 16; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) v += s[w];
-  __syncthreads();
-  return v;
-}
-
 // A unit of the line, and a warp's share of it.
 struct Unit {
   int b, hk, cb, len, b0, n;
@@ -258,9 +248,18 @@ __device__ __forceinline__ bool next_unit(const Kv4AttnParams& p, Unit& u) {
   return true;
 }
 
+// A part of a unit's result: O [columns][D], then m, then l, of up to COLS columns.
+template <int NG, int NT>
+struct Part {
+  static constexpr int D = 32 * NG, COLS = 8 * NT, FLOATS = COLS * (D + 2);
+};
+
 template <int NG, int NT>
 struct Smem {
+  // a warp's ring; when it has run out, the part of the unit its stretch ends in
   uint8_t ring[kWarps][kStages][kRun][kv4_block_bytes(NG)];
+  // the part of the unit a warp's stretch begins in
+  float head[NT == 1 ? kWarps : 1][NT == 1 ? Part<NG, NT>::FLOATS : 4];
   uint4 q[NT > 1 ? kWarps : 1][NT > 1 ? NT * NG * 32 : 1];
   // -8 2^-24 sum of a group's q of columns 2 t and 2 t + 1, twice: an accumulator's start
   float4 qc[kWarps][NT * NG][4];
@@ -270,15 +269,42 @@ struct Smem {
   // units that span warps: at each end of a warp's stretch, {sequence, head,
   // column block, first warp, last warp} (first warp -1: none)
   int span[kWarps + 1][5];
-  int last[kWarps + 1];
+  int last[2];
   int abort;
+  static constexpr bool kTailInRing =
+      sizeof(uint8_t[kStages][kRun][kv4_block_bytes(NG)]) >= sizeof(float) * Part<NG, NT>::FLOATS;
 };
 
-// Joins parts first .. last of a unit (all threads of the CTA).
+// Running join of softmax parts.
+struct Joined {
+  float m, l;
+  float4 o;
+  __device__ __forceinline__ void clear() {
+    m = -INFINITY;
+    l = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __device__ __forceinline__ void add(float pm, float pl, float4 po) {
+    const float n = fmaxf(m, pm), ref = n == -INFINITY ? 0.f : n;
+    const float a = exp2f(m - ref), c = exp2f(pm - ref);
+    m = n;
+    l = fmaf(l, a, pl * c);
+    o.x = fmaf(o.x, a, po.x * c);
+    o.y = fmaf(o.y, a, po.y * c);
+    o.z = fmaf(o.z, a, po.z * c);
+    o.w = fmaf(o.w, a, po.w * c);
+  }
+  __device__ __forceinline__ void write(const Kv4AttnParams& p, const int* span, int col,
+                                        int f) const {
+    write_out(p, span[0], span[1], col, f, o, m == -INFINITY ? 0.f : m, l);
+  }
+};
+
+// Joins the parts that CTAs first .. last left of a unit (all threads of the CTA).
 template <int NG, int NT>
-__device__ __forceinline__ void join_parts(const Kv4AttnParams& p, const int* span, float* scratch) {
+__device__ __forceinline__ void join_ctas(const Kv4AttnParams& p, const int* span, float* scratch) {
   constexpr int D = 32 * NG, COLS = 8 * NT;
-  const int b = span[0], hk = span[1], c_first = span[2] * COLS, first = span[3], last = span[4];
+  const int c_first = span[2] * COLS, first = span[3] / kWarps, last = span[4] / kWarps;
   const int ncolv = min(COLS, p.ncols - c_first), items = ncolv * (D / 4);
   // few items: several threads share one, each taking every groups-th part
   const int groups = items >= kThreads ? 1 : kThreads / items;
@@ -287,65 +313,57 @@ __device__ __forceinline__ void join_parts(const Kv4AttnParams& p, const int* sp
     const int grp = groups > 1 ? tid / items : 0, i = groups > 1 ? tid - grp * items : i0 + tid;
     const bool mine = i < items && grp < groups;
     const int cc = mine ? i / (D / 4) : 0, f = mine ? (i - cc * (D / 4)) * 4 : 0;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    Joined a;
+    a.clear();
     if (mine) {
-      constexpr int U = 4;
-      for (int w0 = first + grp; w0 <= last; w0 += U * groups) {
+      constexpr int U = 8;  // parts read at once: the join waits for memory, not for bandwidth
+      for (int c0 = first + grp; c0 <= last; c0 += U * groups) {
         float pm[U], pl[U];
         float4 po[U];
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-          const int w = w0 + k * groups;
+          const int c = c0 + k * groups;
           pm[k] = -INFINITY;
           pl[k] = 0.f;
           po[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (w <= last) {
-            const float* pp = p.parts + ((int64_t)w * 2 + (w == first ? 1 : 0)) * p.part_stride;
+          if (c <= last) {
+            const float* pp =
+                p.parts + ((int64_t)c * kCtaParts + (c == first ? 1 : 0)) * p.part_stride;
             pm[k] = __ldcg(pp + p.part_cols * D + cc);
             pl[k] = __ldcg(pp + p.part_cols * D + p.part_cols + cc);
             po[k] = __ldcg(reinterpret_cast<const float4*>(pp + cc * D + f));
           }
         }
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-          const float n = fmaxf(m, pm[k]), ref = n == -INFINITY ? 0.f : n;
-          const float a = exp2f(m - ref), c = exp2f(pm[k] - ref);
-          m = n;
-          l = fmaf(l, a, pl[k] * c);
-          o.x = fmaf(o.x, a, po[k].x * c);
-          o.y = fmaf(o.y, a, po[k].y * c);
-          o.z = fmaf(o.z, a, po[k].z * c);
-          o.w = fmaf(o.w, a, po[k].w * c);
-        }
+        for (int k = 0; k < U; ++k) a.add(pm[k], pl[k], po[k]);
       }
     }
     if (groups > 1) {
       float* s = scratch + tid * 6;
-      s[0] = m;
-      s[1] = l;
-      s[2] = o.x;
-      s[3] = o.y;
-      s[4] = o.z;
-      s[5] = o.w;
+      s[0] = a.m;
+      s[1] = a.l;
+      s[2] = a.o.x;
+      s[3] = a.o.y;
+      s[4] = a.o.z;
+      s[5] = a.o.w;
       __syncthreads();
-      if (grp == 0) {
+      if (grp == 0)
         for (int k = 1; k < groups; ++k) {
           const float* t = scratch + (tid + k * items) * 6;
-          const float n = fmaxf(m, t[0]), ref = n == -INFINITY ? 0.f : n;
-          const float a = exp2f(m - ref), c = exp2f(t[0] - ref);
-          m = n;
-          l = fmaf(l, a, t[1] * c);
-          o.x = fmaf(o.x, a, t[2] * c);
-          o.y = fmaf(o.y, a, t[3] * c);
-          o.z = fmaf(o.z, a, t[4] * c);
-          o.w = fmaf(o.w, a, t[5] * c);
+          a.add(t[0], t[1], make_float4(t[2], t[3], t[4], t[5]));
         }
-      }
       __syncthreads();
     }
-    if (mine && grp == 0) write_out(p, b, hk, c_first + cc, f, o, m == -INFINITY ? 0.f : m, l);
+    if (mine && grp == 0) a.write(p, span, c_first + cc, f);
   }
+}
+
+// One more arrival at a unit's counter; releases what the CTA wrote before its
+// last barrier, and acquires what the CTAs that arrived earlier wrote.
+__device__ __forceinline__ unsigned arrive(unsigned* counter) {
+  unsigned old;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+  return old;
 }
 
 template <int NG, int NT, bool FEW>
@@ -365,55 +383,73 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
   if (tid <= kWarps) sm.span[tid][3] = -1;
   if (tid == 0) sm.abort = 0;
   mbar_init_fence();
-  long long mine = 0;
-  for (int b = tid; b < p.B; b += kThreads) {
-    const int raw = __ldg(p.lens + b), len = seq_len(p, b);
-    if (blockIdx.x == 0 && raw != len) atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
-    mine += (long long)head_positions<COLS>(p, len) * p.Hkv;
+  // positions of this thread's sequence, and of all; batches longer than the
+  // CTA are summed first and scanned in a second pass
+  auto positions = [&](int b, bool check) {
+    if (b >= p.B) return 0ll;
+    const int raw = __ldg(p.lens + b), len = min(max(raw, 0), p.table_w * p.page);
+    if (check && blockIdx.x == 0 && raw != len) atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
+    return (long long)head_positions<COLS>(p, len) * p.Hkv;
+  };
+  auto scan = [&](long long v, long long& all) {  // inclusive sum over the CTA's threads
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, v, k);
+      if (lane >= k) v += u;
+    }
+    if (lane == 31) sm.scan[warp] = v;
+    __syncthreads();
+    all = 0;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+      if (k < warp) v += sm.scan[k];
+      all += sm.scan[k];
+    }
+    return v;
+  };
+  long long v = positions(tid, true), all, incl = scan(v, all), total = all;
+  for (int b0 = kThreads; b0 < p.B; b0 += kThreads) {
+    long long more;
+    __syncthreads();
+    scan(positions(b0 + tid, true), more);
+    total += more;
   }
-  const long long total = cta_sum(mine, sm.scan);
   const int workers = gridDim.x * kWarps;
   const long long share64 = max((long long)kMinShare, (total + workers - 1) / workers);
   const int share = (int)share64;
   const int me = blockIdx.x * kWarps + warp;
-  if (share64 * (blockIdx.x * kWarps) >= total) return;  // the whole CTA
-  const long long w = share64 * me;
+  const long long w_cta = share64 * (blockIdx.x * kWarps), w = w_cta + share64 * warp;
+  if (w_cta >= total) return;  // the whole CTA
   const int stretch = (int)min((long long)share, max(0ll, total - w));
-  {  // the sequence that holds position w, for each warp
-    long long base = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-      const int b = b0 + tid;
-      const long long v =
-          b < p.B ? (long long)head_positions<COLS>(p, seq_len(p, b)) * p.Hkv : 0;
-      long long incl = v;
+  // the sequence that holds position w, for each warp
+  for (long long base = 0, b0 = 0;;) {
+    const long long lo = base + incl - v, hi = base + incl;
 #pragma unroll
-      for (int k = 1; k < 32; k <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, incl, k);
-        if (lane >= k) incl += u;
+    for (int k = 0; k < kWarps; ++k) {
+      const long long wk = w_cta + share64 * k;
+      if (wk >= lo && wk < hi) {
+        sm.seq[k] = (int)b0 + tid;
+        sm.base[k] = lo;
       }
-      if (lane == 31) sm.scan[warp] = incl;
-      __syncthreads();
-      long long all = 0;
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k) {
-        if (k < warp) incl += sm.scan[k];
-        all += sm.scan[k];
-      }
-      const long long lo = base + incl - v, hi = base + incl;
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k) {
-        const long long wk = share64 * (blockIdx.x * kWarps + k);
-        if (wk >= lo && wk < hi) {
-          sm.seq[k] = b;
-          sm.base[k] = lo;
-        }
-      }
-      base += all;
-      __syncthreads();
-      if (base > share64 * (blockIdx.x * kWarps + kWarps - 1)) break;  // the same everywhere
     }
+    base += all;
+    b0 += kThreads;
+    __syncthreads();
+    if (b0 >= p.B || base > w_cta + share64 * (kWarps - 1)) break;  // the same everywhere
+    v = positions((int)b0 + tid, false);
+    incl = scan(v, all);
   }
 
+  // where a warp of this CTA leaves its part of a unit that ends in its stretch
+  // after beginning before it, and of one that goes on after it
+  float* const cta_parts = p.parts + (int64_t)blockIdx.x * kCtaParts * p.part_stride;
+  auto head_of = [&](int w) {
+    return NT == 1 ? sm.head[w % (NT == 1 ? kWarps : 1)] : cta_parts + (2 + w) * p.part_stride;
+  };
+  auto tail_of = [&](int w) {
+    return Smem<NG, NT>::kTailInRing ? reinterpret_cast<float*>(sm.ring[w])
+                                     : cta_parts + (2 + kWarps + w) * p.part_stride;
+  };
   bool ok = true;
   if (stretch > 0) {
     Unit u;
@@ -431,6 +467,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
       }
       u.at = -s;
     }
+
+    // Q of the unit this warp comes to next, on its way while the unit before is computed
+    auto prefetch_q = [&](const Unit& n) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int col = n.cb * COLS + 8 * nt + (FEW ? g & 1 : g);
+        if (col < p.ncols && t < (NG + 1) / 2) {  // lines of 128 bytes: 64 features
+          const int qi = token_of(p, col), qh = n.hk * p.G + col - qi * p.G;
+          const __nv_bfloat16* qp =
+              p.q + n.b * p.sq.b_outer + qi * p.sq.seq + qh * p.sq.head + 64 * t;
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(qp));
+        }
+      }
+    };
+    prefetch_q(u);
 
     // ---- the ring: stages of up to kRun blocks of one unit, kStages ahead, copied
     // in runs inside a page; the page id of the run after the current one is
@@ -577,6 +628,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
           }
         }
         __syncwarp();
+        {
+          Unit n = u;
+          if (u.at + u.n + kUnitCost < stretch && next_unit<COLS>(p, n)) prefetch_q(n);
+        }
 
         // running maximum m of a column: mlim = m + 8, mref = m, or 0 while no key
         // has been seen (m = -inf)
@@ -858,7 +913,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
             l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
           }
         const bool whole = r0 <= 0 && r1 >= u.n;
-        float* part = p.parts + ((int64_t)me * 2 + (r0 > 0 ? 0 : 1)) * p.part_stride;
+        // r1 < u.n: the unit goes on in the next warp, and this one is done
+        float* part = r1 < u.n ? tail_of(warp) : head_of(warp);
         // features 32 j + 4 g .. + 3 of column cc
         auto put = [&](int cc, int j, float4 o, float lim, float ref, float ll) {
           if (whole) {
@@ -934,27 +990,56 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
     }
   }
 
-  // ---- units that span warps: the CTA that arrives last joins the parts
-  __threadfence();
+  // ---- units that span warps: join this CTA's parts
   __syncthreads();
   if (sm.abort) return;
-  if (tid <= kWarps) {
-    const int first = sm.span[tid][3], last = sm.span[tid][4];
-    bool join = first >= 0 && (tid == 0 || sm.span[tid - 1][3] != first);
-    if (join) {
-      const unsigned others = (unsigned)(last / kWarps - first / kWarps);
-      if (others > 0) {
-        join = atomicAdd(p.counters + first, 1u) == others;
-        if (join) p.counters[first] = 0u;  // ready for the next call
+  const int w0 = blockIdx.x * kWarps;
+#pragma unroll 1
+  for (int k = 0; k <= kWarps; ++k) {
+    const int* span = sm.span[k];
+    const int first = span[3], last = span[4];
+    if (first < 0 || (k > 0 && sm.span[k - 1][3] == first)) continue;
+    const int c_first = span[2] * COLS, ncolv = min(COLS, p.ncols - c_first);
+    const int lo = max(first, w0) - w0, hi = min(last, w0 + kWarps - 1) - w0;
+    float* to = cta_parts + (first >= w0 ? 1 : 0) * p.part_stride;
+    for (int i = tid; i < ncolv * (D / 4); i += kThreads) {
+      const int cc = i / (D / 4), f = (i - cc * (D / 4)) * 4;
+      Joined a;
+      a.clear();
+      for (int x = lo; x <= hi; ++x) {
+        const float* pp = w0 + x == last ? head_of(x) : tail_of(x);
+        a.add(pp[p.part_cols * D + cc], pp[p.part_cols * D + p.part_cols + cc],
+              *reinterpret_cast<const float4*>(pp + cc * D + f));
       }
+      if (first >= w0 && last < w0 + kWarps) {
+        a.write(p, span, c_first + cc, f);
+      } else {
+        *reinterpret_cast<float4*>(to + cc * D + f) = a.o;
+        if (f == 0) {
+          to[p.part_cols * D + cc] = a.m;
+          to[p.part_cols * D + p.part_cols + cc] = a.l;
+        }
+      }
+    }
+  }
+  // ---- units that span CTAs, the one the CTA begins in and the one it ends in:
+  // the CTA that arrives last joins them
+  __syncthreads();
+  if (tid < 2) {
+    const int* span = sm.span[tid == 0 ? 0 : kWarps];
+    const int first = span[3] / kWarps, last = span[4] / kWarps;
+    bool join = span[3] >= 0 && first != last && (tid == 0 || sm.span[0][3] != span[3]);
+    if (join) {
+      join = arrive(p.counters + first) == (unsigned)(last - first);
+      if (join) p.counters[first] = 0u;  // ready for the next call
     }
     sm.last[tid] = join;
   }
   __syncthreads();
-  __threadfence();
 #pragma unroll 1
-  for (int k = 0; k <= kWarps; ++k)
-    if (sm.last[k]) join_parts<NG, NT>(p, sm.span[k], reinterpret_cast<float*>(sm.ring));
+  for (int k = 0; k < 2; ++k)
+    if (sm.last[k])
+      join_ctas<NG, NT>(p, sm.span[k == 0 ? 0 : kWarps], reinterpret_cast<float*>(sm.ring));
 }
 
 bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
@@ -1006,7 +1091,7 @@ size_t mha_fwd_kv4_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d) {
   const int64_t ncols = (int64_t)Nq * (Hq / Hkv);
   const int ctas = iha::kMaxCtas * iha::ctas_per_sm(iha::pick_nt(ncols)) / iha::ctas_per_sm(1);
   return iha::kCounterBytes +
-         (size_t)ctas * iha::kWarps * 2 * iha::part_stride(ncols, d) * sizeof(float);
+         (size_t)ctas * iha::kCtaParts * iha::part_stride(ncols, d) * sizeof(float);
 }
 
 iha_status mha_fwd_kv4(const void* q, const void* cache, const int32_t* block_table,
@@ -1091,7 +1176,7 @@ iha_status mha_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
   p.inv_g = ((1ull << 32) + G - 1) / G;
   p.wait_ns = kWaitLimitNs;
   p.counters = static_cast<unsigned*>(workspace);
-  p.parts = reinterpret_cast<float*>(p.counters + kMaxCtas * kWarps);
+  p.parts = reinterpret_cast<float*>(p.counters + kMaxCtas);
   p.part_cols = part_cols(ncols);
   p.part_stride = part_stride(ncols, d);
   p.n_pages = n_pages;
