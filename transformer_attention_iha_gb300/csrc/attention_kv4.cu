@@ -17,7 +17,7 @@
 //     up to 2 columns (one token of unshared heads, the common case): the 8
 //       columns of the operand hold the 2 columns four times, once per group,
 //       each with its group's scale, so P is scaled, rounded and turned once
-//       instead of four times.  P s F in fp16 (2^-11 a term) with a power of two
+//       instead of four times; up to 4 columns, twice, for two groups.  P s F in fp16 (2^-11 a term) with a power of two
 //       F per column and group that keeps it in range, codes as for K; -8 sum P
 //       comes from one more MMA with a constant A operand (the same rounded P)
 //       and is taken out of O every kFlush blocks.
@@ -27,8 +27,7 @@
 //   Softmax in the log2 domain, fp32; a column's reference maximum moves only
 //   when a score exceeds it by more than 8, then O and the sum are rescaled.
 // Codes are never expanded in memory: 36 NG bytes per token and head are read
-// once, by bulk copies of whole blocks into a ring of kStages x kRun blocks that
-// each warp owns, and unpacked in the registers of the lanes that use them.
+// once, by bulk copies of whole blocks into a ring that each warp owns, and unpacked in the registers of the lanes that use them.
 //
 // Work is one line of positions: sequence by sequence, head by head, column
 // block by column block (a unit); a unit takes one position per block of 16
@@ -52,16 +51,21 @@ IHA_DEVICE_ERROR_WORD(attention_kv4)
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 2;    // a warp's ring: stages of up to kRun blocks
-constexpr int kRun = 2;
+// A warp's ring: stages of up to run_of(NT) blocks.  Longer stages spread the
+// cost of a wait and a refill; 12 warps of 2 x 4 blocks measured better than 16
+// of 2 x 2 (131071 keys x 80 heads: 241 against 260 us; 8 warps: 256).
+constexpr int kStages = 2;
+__host__ __device__ constexpr int run_of(int nt) { return nt == 1 ? 4 : 2; }
+// CTAs an SM holds at once (registers and shared memory allow that many).
+__host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 4 ? 2 : 3; }
 // FEW: the codes' offset leaves O after this many blocks (256 tokens): it costs
 // 32 FMAs, and O has grown by 8 s per unit of probability until then.
 constexpr int kFlush = 16;
-constexpr int kUnitCost = 4;  // positions a unit takes besides its blocks
+constexpr int kUnitCost = 6;  // positions a unit takes besides its blocks
 // A warp's stretch is at least this long: shorter ones cost more in joining
 // than they save.
 constexpr int kMinShare = 4;
-constexpr int kMaxCtas = 640;  // counters for 152 SMs x 4 CTAs and some
+constexpr int kMaxCtas = 480;  // counters for 152 SMs x 3 CTAs and some
 constexpr int kCounterBytes = kMaxCtas * 4;
 constexpr int kCtaParts = 2 + 2 * kWarps;
 
@@ -257,9 +261,7 @@ struct Part {
 template <int NG, int NT>
 struct Smem {
   // a warp's ring; when it has run out, the part of the unit its stretch ends in
-  uint8_t ring[kWarps][kStages][kRun][kv4_block_bytes(NG)];
-  // the part of the unit a warp's stretch begins in
-  float head[NT == 1 ? kWarps : 1][NT == 1 ? Part<NG, NT>::FLOATS : 4];
+  uint8_t ring[kWarps][kStages][run_of(NT)][kv4_block_bytes(NG)];
   uint4 q[NT > 1 ? kWarps : 1][NT > 1 ? NT * NG * 32 : 1];
   // -8 2^-24 sum of a group's q of columns 2 t and 2 t + 1, twice: an accumulator's start
   float4 qc[kWarps][NT * NG][4];
@@ -267,12 +269,13 @@ struct Smem {
   long long scan[kWarps], base[kWarps];
   int seq[kWarps];
   // units that span warps: at each end of a warp's stretch, {sequence, head,
-  // column block, first warp, last warp} (first warp -1: none)
-  int span[kWarps + 1][5];
-  int last[2];
+  // column block, first and last warp (-1, kWarps: in other CTAs), blocks (0: none),
+  // CTAs it began before this one, CTAs it ends behind this one}
+  int span[kWarps + 1][8];
+  int last[2], of[2][2];  // unit at each end of the stretch: joined here, its CTAs
   int abort;
   static constexpr bool kTailInRing =
-      sizeof(uint8_t[kStages][kRun][kv4_block_bytes(NG)]) >= sizeof(float) * Part<NG, NT>::FLOATS;
+      sizeof(uint8_t[kStages][run_of(NT)][kv4_block_bytes(NG)]) >= sizeof(float) * Part<NG, NT>::FLOATS;
 };
 
 // Running join of softmax parts.
@@ -300,11 +303,12 @@ struct Joined {
   }
 };
 
-// Joins the parts that CTAs first .. last left of a unit (all threads of the CTA).
+// Joins the parts that CTAs of[0] .. of[1] left of a unit (all threads of the CTA).
 template <int NG, int NT>
-__device__ __forceinline__ void join_ctas(const Kv4AttnParams& p, const int* span, float* scratch) {
+__device__ __forceinline__ void join_ctas(const Kv4AttnParams& p, const int* span,
+                                          const int* of, float* scratch) {
   constexpr int D = 32 * NG, COLS = 8 * NT;
-  const int c_first = span[2] * COLS, first = span[3] / kWarps, last = span[4] / kWarps;
+  const int c_first = span[2] * COLS, first = of[0], last = of[1];
   const int ncolv = min(COLS, p.ncols - c_first), items = ncolv * (D / 4);
   // few items: several threads share one, each taking every groups-th part
   const int groups = items >= kThreads ? 1 : kThreads / items;
@@ -366,21 +370,30 @@ __device__ __forceinline__ unsigned arrive(unsigned* counter) {
   return old;
 }
 
-template <int NG, int NT, bool FEW>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
+// GC: groups that share a P operand (4, 2: see above; 1: none).  ONE: a single
+// column, the odd columns of the operands are not computed.
+template <int NG, int NT, int GC, bool ONE>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
     attn_kv4_kernel(const Kv4AttnParams p) {
   constexpr int D = 32 * NG, COLS = 8 * NT, BYTES = kv4_block_bytes(NG);
   constexpr int NB = NT == 1 ? 2 : 1;  // blocks computed together (registers allow)
+  constexpr int kRun = run_of(NT);
+  constexpr int ES = ONE ? 2 : 1;      // step over the columns of a pair
+  constexpr bool FEW = GC > 1;
+  constexpr int REAL = FEW ? 8 / GC : 8;           // columns of a B operand that differ
+  constexpr int SH = FEW ? (NG + GC - 1) / GC : 1;  // P operands of a block
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem<NG, NT>& sm = *reinterpret_cast<Smem<NG, NT>*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in the warp, for the compiler too
   volatile int* abort_flag = &sm.abort;
+  // FEW: of operand s, columns 2 t, 2 t + 1 are columns tc, tc + 1 scaled for group GC s + tg
+  const int tg = FEW ? 2 * t / REAL : 0, tc = FEW ? 2 * t % REAL : 2 * t;
 
   // ---- this warp's stretch of the line
   if (lane == 0)
     for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&sm.full[warp][i]), 1);
-  if (tid <= kWarps) sm.span[tid][3] = -1;
+  if (tid <= kWarps) sm.span[tid][5] = 0;
   if (tid == 0) sm.abort = 0;
   mbar_init_fence();
   // positions of this thread's sequence, and of all; batches longer than the
@@ -414,11 +427,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
     scan(positions(b0 + tid, true), more);
     total += more;
   }
-  const int workers = gridDim.x * kWarps;
-  const long long share64 = max((long long)kMinShare, (total + workers - 1) / workers);
-  const int share = (int)share64;
-  const int me = blockIdx.x * kWarps + warp;
-  const long long w_cta = share64 * (blockIdx.x * kWarps), w = w_cta + share64 * warp;
+  const long long workers = gridDim.x * kWarps;
+  const int share = max(kMinShare, (int)((total + workers - 1) / workers));
+  const long long w_cta = (long long)share * (blockIdx.x * kWarps), w = w_cta + share * warp;
   if (w_cta >= total) return;  // the whole CTA
   const int stretch = (int)min((long long)share, max(0ll, total - w));
   // the sequence that holds position w, for each warp
@@ -426,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
     const long long lo = base + incl - v, hi = base + incl;
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) {
-      const long long wk = w_cta + share64 * k;
+      const long long wk = w_cta + share * k;
       if (wk >= lo && wk < hi) {
         sm.seq[k] = (int)b0 + tid;
         sm.base[k] = lo;
@@ -435,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
     base += all;
     b0 += kThreads;
     __syncthreads();
-    if (b0 >= p.B || base > w_cta + share64 * (kWarps - 1)) break;  // the same everywhere
+    if (b0 >= p.B || base > w_cta + share * (kWarps - 1)) break;  // the same everywhere
     v = positions((int)b0 + tid, false);
     incl = scan(v, all);
   }
@@ -444,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
   // after beginning before it, and of one that goes on after it
   float* const cta_parts = p.parts + (int64_t)blockIdx.x * kCtaParts * p.part_stride;
   auto head_of = [&](int w) {
-    return NT == 1 ? sm.head[w % (NT == 1 ? kWarps : 1)] : cta_parts + (2 + w) * p.part_stride;
+    return cta_parts + (2 + w) * p.part_stride;
   };
   auto tail_of = [&](int w) {
     return Smem<NG, NT>::kTailInRing ? reinterpret_cast<float*>(sm.ring[w])
@@ -472,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
     auto prefetch_q = [&](const Unit& n) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int col = n.cb * COLS + 8 * nt + (FEW ? g & 1 : g);
+        const int col = n.cb * COLS + 8 * nt + g % REAL;
         if (col < p.ncols && t < (NG + 1) / 2) {  // lines of 128 bytes: 64 features
           const int qi = token_of(p, col), qh = n.hk * p.G + col - qi * p.G;
           const __nv_bfloat16* qp =
@@ -570,14 +581,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
         col_range(p, u.len, c_first, x_, hi_full);
         col_range(p, u.len, c_first + ncolv - 1, lo_full, x_);
 
-        // Q as B operand: column 8 nt + g (FEW: column g % 2), feature pairs
+        // Q as B operand: column 8 nt + g (FEW: column g % REAL), feature pairs
         // (i, i + 4) of octet t, those of odd i divided by 16
         uint32_t qf[NT == 1 ? NG : 1][4];
         float cm[NT][2];  // accumulators of columns 2 t, 2 t + 1 to scores, log2 domain
         __syncwarp();     // the Q of the unit before has been read
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const int col = c_first + 8 * nt + (FEW ? g & 1 : g);
+          const int col = c_first + 8 * nt + g % REAL;
           const bool in = col < p.ncols;
           const int qi = in ? token_of(p, col) : 0, qh = u.hk * p.G + (in ? col - qi * p.G : 0);
           const __nv_bfloat16* qp =
@@ -636,9 +647,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
         // running maximum m of a column: mlim = m + 8, mref = m, or 0 while no key
         // has been seen (m = -inf)
         float mlim[NT][2], mref[NT][2], l[NT][2];
-        float off[4] = {0.f, 0.f, 0.f, 0.f};  // FEW: -8 2^-24 sum P since the last flush
-        float F[2] = {0.f, 0.f}, F_lim[2];  // FEW: see below; lanes without a group never ask
-        F_lim[0] = F_lim[1] = t < NG ? -1.f : INFINITY;
+        float off[SH][4];        // FEW: -8 2^-24 sum P since the last flush
+        float F[SH][2], F_lim[SH][2];  // FEW: see below; lanes without a group never ask
+#pragma unroll
+        for (int s = 0; s < SH; ++s) {
+          off[s][0] = off[s][1] = off[s][2] = off[s][3] = 0.f;
+          F[s][0] = F[s][1] = 0.f;
+          F_lim[s][0] = F_lim[s][1] = GC * s + tg < NG ? -1.f : INFINITY;
+        }
         float acc[NT][NG][2][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -660,10 +676,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
             for (int h = 0; h < 2; ++h)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                acc[0][j][h][e] += off[e];
-                acc[0][j][h][e + 2] = fmaf(16.f, off[e], acc[0][j][h][e + 2]);
+                acc[0][j][h][e] += off[j / GC % SH][e];
+                acc[0][j][h][e + 2] = fmaf(16.f, off[j / GC % SH][e], acc[0][j][h][e + 2]);
               }
-          off[0] = off[1] = off[2] = off[3] = 0.f;
+#pragma unroll
+          for (int s = 0; s < SH; ++s) off[s][0] = off[s][1] = off[s][2] = off[s][3] = 0.f;
         };
         // blocks r with rf0 <= r - b0 < rf0 + rf_n are visible to every column
         const int rf0 = (lo_full + kKv4Tok - 1) / kKv4Tok - u.b0;
@@ -711,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
                     mma_f16(d, a[2], c8[2], a[3], c8[3], f.z, f.w, c);
                   }
 #pragma unroll
-                  for (int e = 0; e < 4; ++e)
+                  for (int e = 0; e < 4; e += ES)
                     x[nt][b][e] = j == 0 ? (e < 2 ? k0_ : k1_) * d[e]
                                          : fmaf(e < 2 ? k0_ : k1_, d[e], x[nt][b][e]);
                 }
@@ -726,8 +743,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int col = c_first + (FEW ? e : 8 * nt + 2 * t + e);
+                for (int e = 0; e < 2; e += ES) {
+                  const int col = c_first + 8 * nt + tc + e;
                   int lo, hi;
                   col_range(p, u.len, col, lo, hi);
                   if (col >= p.ncols) hi = 0;
@@ -747,16 +764,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
             for (int nt = 0; nt < NT; ++nt) {
               float top[2];
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
+              for (int e = 0; e < 2; e += ES) {
                 top[e] = fmaxf(x[nt][0][e], x[nt][0][e + 2]);
 #pragma unroll
                 for (int b = 1; b < NB; ++b)
                   top[e] = fmax3f(top[e], x[nt][b][e], x[nt][b][e + 2]);
                 top[e] *= cm[nt][e];
               }
-              if (__any_sync(0xffffffffu, top[0] > mlim[nt][0] || top[1] > mlim[nt][1])) {
+              if (__any_sync(0xffffffffu, top[0] > mlim[nt][0] || (!ONE && top[1] > mlim[nt][1]))) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < 2; e += ES) {
                   float v = top[e];
                   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
@@ -767,7 +784,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
                   mlim[nt][e] = v + 8.f;
                   mref[nt][e] = ref;
                   l[nt][e] *= f;
-                  if constexpr (FEW) off[e] *= f;
+                  if constexpr (FEW) {
+#pragma unroll
+                    for (int s = 0; s < SH; ++s) off[s][e] *= f;
+                  }
 #pragma unroll
                   for (int j = 0; j < NG; ++j)
 #pragma unroll
@@ -780,86 +800,100 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
 #pragma unroll
               for (int b = 0; b < NB; ++b) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)  // x becomes p
+                for (int e = 0; e < 4; e += ES)  // x becomes p
                   x[nt][b][e] = fast_exp2(fmaf(x[nt][b][e], cm[nt][e & 1], -mref[nt][e & 1]));
                 l[nt][0] += x[nt][b][0] + x[nt][b][2];
-                l[nt][1] += x[nt][b][1] + x[nt][b][3];
+                if (!ONE) l[nt][1] += x[nt][b][1] + x[nt][b][3];
               }
             }
             if constexpr (FEW) {
               // w = p s of this lane's group; P = w F.  F is 0 until the first
               // w > 0 of the column and group, then a power of two that keeps
               // the largest w F so far between 1 and 2^15.
-              float w[NB][4];
+              float w[SH][NB][4];
+              bool grow = false;
+              float top[SH][2];
 #pragma unroll
-              for (int b = 0; b < NB; ++b) {
-                float f0 = 0.f, f1 = 0.f;  // scales of tokens g, g + 8 in group t
-                if (NG == 4 || t < NG) {
-                  const uint16_t* sp = reinterpret_cast<const uint16_t*>(blk_s + b * BYTES +
-                                                                         kv4_v_scales(NG)) +
-                                       g * 2 * NG + t;
-                  f0 = __uint_as_float((uint32_t)sp[0] << 16);
-                  f1 = __uint_as_float((uint32_t)sp[NG] << 16);
-                }
+              for (int s = 0; s < SH; ++s) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[b][e] = x[0][b][e] * (e < 2 ? f0 : f1);
-              }
-              if (edge) {  // a hidden token's scale may be anything, NaN too
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    if ((hidden >> (4 * b + e)) & 1u) w[b][e] = 0.f;
-              }
-              float top[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                top[e] = fmaxf(w[0][e], w[0][e + 2]);
-#pragma unroll
-                for (int b = 1; b < NB; ++b) top[e] = fmax3f(top[e], w[b][e], w[b][e + 2]);
-              }
-              if (__any_sync(0xffffffffu, top[0] * F[0] > F_lim[0] || top[1] * F[1] > F_lim[1])) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  float v = top[e];
-                  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                  // 2^-(exponent of v), from its bits; v is 0 or positive, infinite at most
-                  const int ex = max((int)(__float_as_uint(v) >> 23), 1);
-                  const float to = __uint_as_float((uint32_t)max(254 - ex, 1) << 23);
-                  if (v > 0.f && (F[e] == 0.f || to < F[e])) {
-                    const float f = F[e] == 0.f ? 0.f : to / F[e];
-                    F[e] = to;
-                    F_lim[e] = 32768.f;
-                    off[e] *= f;
-#pragma unroll
-                    for (int j = 0; j < NG; ++j)
-#pragma unroll
-                      for (int a = 0; a < 2; ++a) {
-                        acc[0][j][a][e] *= f;
-                        acc[0][j][a][e + 2] *= f;
-                      }
+                for (int b = 0; b < NB; ++b) {
+                  float f0 = 0.f, f1 = 0.f;  // scales of tokens g, g + 8 in this lane's group
+                  if (GC * (s + 1) <= NG || GC * s + tg < NG) {
+                    const uint16_t* sp = reinterpret_cast<const uint16_t*>(blk_s + b * BYTES +
+                                                                           kv4_v_scales(NG)) +
+                                         g * 2 * NG + GC * s + tg;
+                    f0 = __uint_as_float((uint32_t)sp[0] << 16);
+                    f1 = __uint_as_float((uint32_t)sp[NG] << 16);
                   }
+#pragma unroll
+                  for (int e = 0; e < 4; e += ES) w[s][b][e] = x[0][b][e] * (e < 2 ? f0 : f1);
                 }
+                if (edge) {  // a hidden token's scale may be anything, NaN too
+#pragma unroll
+                  for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int e = 0; e < 4; e += ES)
+                      if ((hidden >> (4 * b + e)) & 1u) w[s][b][e] = 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; e += ES) {
+                  top[s][e] = fmaxf(w[s][0][e], w[s][0][e + 2]);
+#pragma unroll
+                  for (int b = 1; b < NB; ++b)
+                    top[s][e] = fmax3f(top[s][e], w[s][b][e], w[s][b][e + 2]);
+                  grow |= top[s][e] * F[s][e] > F_lim[s][e];
+                }
+              }
+              if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int s = 0; s < SH; ++s)
+#pragma unroll
+                  for (int e = 0; e < 2; e += ES) {
+                    float v = top[s][e];
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                    // 2^-(exponent of v), from its bits; v is 0 or positive, infinite at most
+                    const int ex = max((int)(__float_as_uint(v) >> 23), 1);
+                    const float to = __uint_as_float((uint32_t)max(254 - ex, 1) << 23);
+                    if (v > 0.f && (F[s][e] == 0.f || to < F[s][e])) {
+                      const float f = F[s][e] == 0.f ? 0.f : to / F[s][e];
+                      F[s][e] = to;
+                      F_lim[s][e] = 32768.f;
+                      off[s][e] *= f;
+#pragma unroll
+                      for (int j = GC * s; j < (GC * (s + 1) < NG ? GC * (s + 1) : NG); ++j)
+#pragma unroll
+                        for (int a = 0; a < 2; ++a) {
+                          acc[0][j][a][e] *= f;
+                          acc[0][j][a][e + 2] *= f;
+                        }
+                    }
+                  }
               }
 #pragma unroll
               for (int b = 0; b < NB; ++b) {
                 uint32_t vw[2][NG];
                 load_words<NG>(blk_s + b * BYTES + kv4_v_codes(NG) + lane * 4 * NG, vw[0]);
                 load_words<NG>(blk_s + b * BYTES + kv4_v_codes(NG) + (32 + lane) * 4 * NG, vw[1]);
-                const uint32_t b0 = transpose8x8(pack_f16x2(w[b][0] * F[0], w[b][1] * F[1]));
-                const uint32_t b1 = transpose8x8(pack_f16x2(w[b][2] * F[0], w[b][3] * F[1]));
 #pragma unroll
-                for (int j = 0; j < NG; ++j) {
-                  uint32_t a[4], c8[4];  // tokens 2 t, 2 t + 1 of each half
-                  nibbles_f16(vw[0][j], a);
-                  nibbles_f16(vw[1][j], c8);
+                for (int s = 0; s < SH; ++s) {
+                  const uint32_t b0 =
+                      transpose8x8(pack_f16x2(w[s][b][0] * F[s][0], ONE ? 0.f : w[s][b][1] * F[s][1]));
+                  const uint32_t b1 =
+                      transpose8x8(pack_f16x2(w[s][b][2] * F[s][0], ONE ? 0.f : w[s][b][3] * F[s][1]));
 #pragma unroll
-                  for (int h = 0; h < 2; ++h)  // feature rows i = 2 h and 2 h + 1 (16 times)
-                    mma_f16(acc[0][j][h], a[2 * h], a[2 * h + 1], c8[2 * h], c8[2 * h + 1], b0, b1);
+                  for (int j = GC * s; j < (GC * (s + 1) < NG ? GC * (s + 1) : NG); ++j) {
+                    uint32_t a[4], c8[4];  // tokens 2 t, 2 t + 1 of each half
+                    nibbles_f16(vw[0][j], a);
+                    nibbles_f16(vw[1][j], c8);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)  // feature rows i = 2 h and 2 h + 1 (16 times)
+                      mma_f16(acc[0][j][h], a[2 * h], a[2 * h + 1], c8[2 * h], c8[2 * h + 1], b0,
+                              b1);
+                  }
+                  mma_f16(off[s], 0x80088008u, 0x80088008u, 0x80088008u, 0x80088008u, b0, b1);
                 }
-                mma_f16(off, 0x80088008u, 0x80088008u, 0x80088008u, 0x80088008u, b0, b1);
               }
               if (((rk - r0) & (kFlush - NB)) == kFlush - NB) flush();
             } else {
@@ -927,25 +961,26 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
             }
           }
         };
-        if constexpr (FEW) {  // lane t holds group t
+        if constexpr (FEW) {  // a lane holds the groups GC s + tg, columns tc and tc + 1
           flush();
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float o[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int s = 0; s < SH; ++s)
 #pragma unroll
-            for (int j = 0; j < NG; ++j)
-              if (t == j) {
-                o[0] = acc[0][j][0][e];
-                o[1] = acc[0][j][0][e + 2];
-                o[2] = acc[0][j][1][e];
-                o[3] = acc[0][j][1][e + 2];
-              }
-            // F = 0: every w was 0 (or NaN, and O is NaN)
-            const float f = F[e] == 0.f ? 1.f : 16777216.f / F[e], h = f * 0.0625f;
-            if (t < NG && e < ncolv)
-              put(e, t, make_float4(o[0] * f, o[1] * h, o[2] * f, o[3] * h), mlim[0][e], mref[0][e],
-                  l[0][e]);
-          }
+            for (int e = 0; e < 2; ++e) {
+              float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int j = GC * s; j < (GC * (s + 1) < NG ? GC * (s + 1) : NG); ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  o[k] = __uint_as_float(sel_u32(GC * s + tg == j,
+                                                 __float_as_uint(acc[0][j][k >> 1][2 * (k & 1) + e]),
+                                                 __float_as_uint(o[k])));
+              // F = 0: every w was 0 (or NaN, and O is NaN)
+              const float f = F[s][e] == 0.f ? 1.f : 16777216.f / F[s][e], h = f * 0.0625f;
+              if (GC * s + tg < NG && tc + e < ncolv)
+                put(tc + e, GC * s + tg, make_float4(o[0] * f, o[1] * h, o[2] * f, o[3] * h),
+                    mlim[0][e], mref[0][e], l[0][e]);
+            }
         } else {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -963,9 +998,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
         }
         if (!whole) {
           if (lane == 0) {
-            const int p0 = u.at + kUnitCost;  // position of the unit's first block
-            const int first = r0 > 0 ? me - (-p0 + share - 1) / share : me;
-            const int last = me + (p0 + u.n - 1) / share;
+            const int p0 = share * warp + u.at + kUnitCost;  // of the unit's first block, in the CTA
 #pragma unroll
             for (int k = 0; k < 2; ++k)
               if (k ? r1 < u.n : (r0 > 0 && warp == 0)) {
@@ -973,8 +1006,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
                 sp[0] = u.b;
                 sp[1] = u.hk;
                 sp[2] = u.cb;
-                sp[3] = first;
-                sp[4] = last;
+                sp[3] = p0 >= 0 ? p0 / share : -1;
+                sp[4] = min((p0 + u.n - 1) / share, kWarps);
+                sp[5] = u.n;
+                // (in 32 bits: a 64-bit division is a call, and costs the loop registers)
+                sp[6] = p0 >= 0 ? 0 : (-p0 + share * kWarps - 1) / (share * kWarps);
+                sp[7] = (p0 + u.n - 1) / (share * kWarps);
               }
           }
         }
@@ -993,25 +1030,28 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
   // ---- units that span warps: join this CTA's parts
   __syncthreads();
   if (sm.abort) return;
-  const int w0 = blockIdx.x * kWarps;
+  auto same_unit = [&](int i, int k) {
+    return sm.span[i][5] != 0 && sm.span[i][0] == sm.span[k][0] && sm.span[i][1] == sm.span[k][1] &&
+           sm.span[i][2] == sm.span[k][2];
+  };
 #pragma unroll 1
   for (int k = 0; k <= kWarps; ++k) {
     const int* span = sm.span[k];
     const int first = span[3], last = span[4];
-    if (first < 0 || (k > 0 && sm.span[k - 1][3] == first)) continue;
+    if (span[5] == 0 || (k > 0 && same_unit(k - 1, k))) continue;
     const int c_first = span[2] * COLS, ncolv = min(COLS, p.ncols - c_first);
-    const int lo = max(first, w0) - w0, hi = min(last, w0 + kWarps - 1) - w0;
-    float* to = cta_parts + (first >= w0 ? 1 : 0) * p.part_stride;
+    const int lo = max(first, 0), hi = min(last, kWarps - 1);
+    float* to = cta_parts + (first >= 0 ? 1 : 0) * p.part_stride;
     for (int i = tid; i < ncolv * (D / 4); i += kThreads) {
       const int cc = i / (D / 4), f = (i - cc * (D / 4)) * 4;
       Joined a;
       a.clear();
       for (int x = lo; x <= hi; ++x) {
-        const float* pp = w0 + x == last ? head_of(x) : tail_of(x);
+        const float* pp = x == last ? head_of(x) : tail_of(x);
         a.add(pp[p.part_cols * D + cc], pp[p.part_cols * D + p.part_cols + cc],
               *reinterpret_cast<const float4*>(pp + cc * D + f));
       }
-      if (first >= w0 && last < w0 + kWarps) {
+      if (first >= 0 && last < kWarps) {
         a.write(p, span, c_first + cc, f);
       } else {
         *reinterpret_cast<float4*>(to + cc * D + f) = a.o;
@@ -1027,11 +1067,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
   __syncthreads();
   if (tid < 2) {
     const int* span = sm.span[tid == 0 ? 0 : kWarps];
-    const int first = span[3] / kWarps, last = span[4] / kWarps;
-    bool join = span[3] >= 0 && first != last && (tid == 0 || sm.span[0][3] != span[3]);
+    bool join = span[5] != 0 && (tid == 0 || !same_unit(0, kWarps));
     if (join) {
-      join = arrive(p.counters + first) == (unsigned)(last - first);
+      // CTAs of the unit's first and last block
+      const int first = blockIdx.x - span[6], last = blockIdx.x + span[7];
+      join = first != last && arrive(p.counters + first) == (unsigned)(last - first);
       if (join) p.counters[first] = 0u;  // ready for the next call
+      sm.of[tid][0] = first;
+      sm.of[tid][1] = last;
     }
     sm.last[tid] = join;
   }
@@ -1039,7 +1082,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
 #pragma unroll 1
   for (int k = 0; k < 2; ++k)
     if (sm.last[k])
-      join_ctas<NG, NT>(p, sm.span[k == 0 ? 0 : kWarps], reinterpret_cast<float*>(sm.ring));
+      join_ctas<NG, NT>(p, sm.span[k == 0 ? 0 : kWarps], sm.of[k],
+                        reinterpret_cast<float*>(sm.ring));
 }
 
 bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
@@ -1059,26 +1103,25 @@ int part_stride(int64_t ncols, int d) {  // floats: O, then m, then l
   return (part_cols(ncols) * (d + 2) + 3) & ~3;
 }
 
-// CTAs an SM holds at once (registers bound it; __launch_bounds__ asks for it).
-int ctas_per_sm(int nt) { return nt == 1 ? 4 : (nt == 2 ? 3 : 2); }
-
-template <int NG, int NT, bool FEW>
+template <int NG, int NT, int GC, bool ONE>
 iha_status launch_nt(const Kv4AttnParams& p, int grid, cudaStream_t s) {
-  static_assert(sizeof(Smem<NG, NT>) <= (NT == 1 ? 55 : (NT == 2 ? 73 : 110)) * 1024,
+  static_assert((sizeof(Smem<NG, NT>) + 1024) * ctas_per_sm(NT) <= 228 * 1024,
                 "4-bit attention: the CTAs of an SM do not fit its shared memory");
   static_assert(sizeof(Smem<NG, NT>::ring) >= kThreads * 6 * sizeof(float), "scratch of the join");
   static SmemLimit limit;
-  const cudaError_t e = limit.ensure(attn_kv4_kernel<NG, NT, FEW>, (int)sizeof(Smem<NG, NT>));
+  const cudaError_t e = limit.ensure(attn_kv4_kernel<NG, NT, GC, ONE>, (int)sizeof(Smem<NG, NT>));
   if (e != cudaSuccess)
     return fail(IHA_ERR_CUDA, "mha_fwd_kv4 (smem attribute): %s", cudaGetErrorString(e));
-  attn_kv4_kernel<NG, NT, FEW><<<grid, kThreads, sizeof(Smem<NG, NT>), s>>>(p);
+  attn_kv4_kernel<NG, NT, GC, ONE><<<grid, kThreads, sizeof(Smem<NG, NT>), s>>>(p);
   return check_launch("mha_fwd_kv4");
 }
 template <int NG>
 iha_status launch(const Kv4AttnParams& p, int nt, int grid, cudaStream_t s) {
-  if (p.ncols <= 2) return launch_nt<NG, 1, true>(p, grid, s);
-  if (nt == 1) return launch_nt<NG, 1, false>(p, grid, s);
-  return nt == 2 ? launch_nt<NG, 2, false>(p, grid, s) : launch_nt<NG, 4, false>(p, grid, s);
+  if (p.ncols == 1) return launch_nt<NG, 1, 4, true>(p, grid, s);
+  if (p.ncols == 2) return launch_nt<NG, 1, 4, false>(p, grid, s);
+  if (p.ncols <= 4) return launch_nt<NG, 1, 2, false>(p, grid, s);
+  if (nt == 1) return launch_nt<NG, 1, 1, false>(p, grid, s);
+  return nt == 2 ? launch_nt<NG, 2, 1, false>(p, grid, s) : launch_nt<NG, 4, 1, false>(p, grid, s);
 }
 
 }  // namespace
@@ -1197,7 +1240,7 @@ iha_status mha_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
   const int64_t useful = (most + kMinShare * kWarps - 1) / (kMinShare * kWarps);
   if (grid > useful) grid = useful;
   if (grid > cap) grid = cap;
-  if (most / (grid * kWarps) > (1 << 30))
+  if (most / (grid * kWarps) > (1 << 29))
     return fail(IHA_ERR_UNSUPPORTED, "%s: too many new tokens or keys for one launch", name);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   switch (d / kKv4Group) {
