@@ -20,7 +20,6 @@ PyTorch supplies device memory and the current stream only.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import functools
 import os
@@ -135,9 +134,15 @@ def device_error(clear: bool = True) -> int:
 
 
 # ---------------------------------------------------------------- torch helpers
+_torch_mod = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_mod
+    if _torch_mod is None:
+        import torch
+        _torch_mod = torch
+    return _torch_mod
 
 
 def _stream(stream):
@@ -149,39 +154,41 @@ def _stream(stream):
 
 # The serving calls run for a few microseconds on the GPU, so their checks stay
 # short: a device is its index, and a passing check builds no objects.
-_NOTHING = contextlib.nullcontext()
-
-
 def _raw_stream(dev: int, stream) -> int:
     """cudaStream_t of a call on device `dev`, which must be the current one."""
-    torch = _torch()
-    if dev != torch.cuda.current_device():
+    torch_c = _torch()._C
+    if dev != torch_c._cuda_getDevice():
         raise ValueError(f"tensors on cuda:{dev}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+                         f"cuda:{torch_c._cuda_getDevice()}")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return torch_c._cuda_getCurrentRawStream(dev)
     if stream.device.index != dev:
         raise ValueError(f"stream on {stream.device}, tensors on cuda:{dev}")
     return stream.cuda_stream
 
 
-def _made_on(stream):
-    """Context for tensors that a call makes itself: they come from the memory
-    of the stream that the call runs on, so that nothing pending on another
-    stream still uses them."""
-    return _NOTHING if stream is None else _torch().cuda.stream(stream)
+def _make(shape, dtype, like, stream, zero: bool = False):
+    """A tensor that a call makes itself, on like's device.  It comes from the
+    memory of the stream that the call runs on, so that nothing pending on
+    another stream still uses it."""
+    torch = _torch()
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=like.device)
 
 
 def _dense(t, name: str, shape, dtype, dev: int) -> None:
     """_expect for a dense tensor on device index `dev` (>= 0: a CUDA device)."""
-    if (dev < 0 or t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous() or
-            (shape is not None and t.shape != shape)):
+    if (t.dtype is not dtype or t.get_device() != dev or dev < 0 or
+            (shape is not None and t.shape != shape) or not t.is_contiguous()):
         _expect(t, name, shape, dtype, _torch().device("cuda", max(dev, 0)))
 
 
 def _view(t, name: str, shape, dtype, dev: int) -> None:
     """The same for a strided view, dense in its last dimension."""
-    if dev < 0 or t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+    if t.dtype is not dtype or t.get_device() != dev or dev < 0 or t.shape != shape:
         _expect(t, name, shape, dtype, _torch().device("cuda", max(dev, 0)), contiguous=False)
     if t.stride(-1) != 1:
         raise ValueError(f"{name}: the head dimension must be dense")
@@ -287,8 +294,8 @@ def premix_fwd_qkv_at(xs, ws, P: int, positions, rope_base: float = 10000.0, out
     sp = _raw_stream(dev, stream)
     oshape = (B, N, H * P, d)
     if out is None:
-        with _made_on(stream):
-            out = tuple(x0.new_empty(oshape) for _ in range(3))
+        out = (_make(oshape, dt, x0, stream), _make(oshape, dt, x0, stream),
+               _make(oshape, dt, x0, stream))
     elif len(out) != 3:
         raise ValueError("out must hold three tensors")
     else:
@@ -593,7 +600,7 @@ def kv4_store(k, v, slots, cache, page: int, stream=None):
     _view(v, "v", shape, k.dtype, dev)
     _dense(slots, "slots", shape[:-2], _torch().int32, dev)
     n_pages = _kv4_pages(cache, page, Hkv, d, dev)
-    check(lib().kv4_store(k.data_ptr(), v.data_ptr(), slots.data_ptr(), cache.data_ptr(), shape[0],
+    check((_lib or lib()).kv4_store(k.data_ptr(), v.data_ptr(), slots.data_ptr(), cache.data_ptr(), shape[0],
                           1 if len(shape) == 4 else shape[1], shape[-3], n_pages, page, Hkv, d,
                           _strides45(k), _strides45(v), dt, _raw_stream(dev, stream)), "kv4_store")
     return cache
@@ -613,9 +620,8 @@ def kv4_load(cache, slots, Hkv: int, d: int, page: int, dtype=None, out=None, st
     shape = slots.shape + (Hkv, d)
     if out is None:
         dtype = dtype or torch.bfloat16
-        with _made_on(stream):
-            k = cache.new_empty(shape, dtype=dtype)
-            v = cache.new_empty(shape, dtype=dtype)
+        k = _make(shape, dtype, cache, stream)
+        v = _make(shape, dtype, cache, stream)
     else:
         if len(out) != 2:
             raise ValueError("out must hold two tensors (k, v)")
@@ -623,7 +629,7 @@ def kv4_load(cache, slots, Hkv: int, d: int, page: int, dtype=None, out=None, st
         dtype = dtype or k.dtype
         _view(k, "out[0]", shape, dtype, dev)
         _view(v, "out[1]", shape, dtype, dev)
-    check(lib().kv4_load(cache.data_ptr(), slots.data_ptr(), k.data_ptr(), v.data_ptr(), shape[0],
+    check((_lib or lib()).kv4_load(cache.data_ptr(), slots.data_ptr(), k.data_ptr(), v.data_ptr(), shape[0],
                          1 if len(shape) == 4 else shape[1], shape[-3], n_pages, page, Hkv, d,
                          _strides45(k), _strides45(v), _dt(k), sp), "kv4_load")
     return k, v
@@ -661,23 +667,20 @@ def mha_fwd_kv4(q, cache, block_table, seq_lens, Hkv: int, page: int, mask: int 
     _dense(seq_lens, "seq_lens", (B,), torch.int32, dev)
     sp = _raw_stream(dev, stream)
     if out is None:
-        with _made_on(stream):
-            out = q.new_empty(shape)
+        out = _make(shape, torch.bfloat16, q, stream)
     else:
         _view(out, "out", shape, torch.bfloat16, dev)
     if lse is not None:
         _dense(lse, "lse", (B, Hq, Nq), torch.float32, dev)
     elif return_lse:
-        with _made_on(stream):
-            lse = q.new_empty((B, Hq, Nq), dtype=torch.float32)
+        lse = _make((B, Hq, Nq), torch.float32, q, stream)
     if workspace is None:
-        with _made_on(stream):
-            workspace = torch.zeros(mha_fwd_kv4_workspace_bytes(B, Nq, Hq, Hkv, d),
-                                    dtype=torch.uint8, device=q.device)
+        workspace = _make(mha_fwd_kv4_workspace_bytes(B, Nq, Hq, Hkv, d), torch.uint8, q, stream,
+                          zero=True)
     else:
         _dense(workspace, "workspace", None, torch.uint8, dev)
     sq, so = q.stride(), out.stride()
-    check(lib().mha_fwd_kv4(q.data_ptr(), cache.data_ptr(), block_table.data_ptr(),
+    check((_lib or lib()).mha_fwd_kv4(q.data_ptr(), cache.data_ptr(), block_table.data_ptr(),
                             seq_lens.data_ptr(), out.data_ptr(),
                             0 if lse is None else lse.data_ptr(), workspace.data_ptr(),
                             workspace.numel(), B, Nq, Hq, Hkv, d, n_pages, page,

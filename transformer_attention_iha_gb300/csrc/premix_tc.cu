@@ -366,6 +366,15 @@ bool premix_tc_supported(int H, int P, int d) {
 }
 
 void make_rope_table(RopeTable* rt, int d, float base) {
+  // A program uses one d and base: the last table of each host thread is kept
+  // (64 calls of pow take longer than the launch).
+  thread_local int last_d = 0;
+  thread_local float last_base = 0.f;
+  thread_local RopeTable last;
+  if (d == last_d && base == last_base) {
+    *rt = last;
+    return;
+  }
   for (int i = 0; i < 64; ++i) {
     if (i < d / 2) {
       const double inv = pow((double)base, -2.0 * (double)i / (double)d);
@@ -375,6 +384,9 @@ void make_rope_table(RopeTable* rt, int d, float base) {
       rt->hi[i] = rt->lo[i] = 0.f;
     }
   }
+  last = *rt;
+  last_d = d;
+  last_base = base;
 }
 
 iha_status premix_fwd_tc_multi(int ntens, const void* const* x, const float* const* w,
