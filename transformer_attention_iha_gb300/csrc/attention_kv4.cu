@@ -387,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in the warp, for the compiler too
   volatile int* abort_flag = &sm.abort;
+  const int vl = kv4_v_lane(g, t);
   // FEW: of operand s, columns 2 t, 2 t + 1 are columns tc, tc + 1 scaled for group GC s + tg
   const int tg = FEW ? 2 * t / REAL : 0, tc = FEW ? 2 * t % REAL : 2 * t;
 
@@ -707,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
               uint32_t kw[2][NG], ks[NG];
               load_words<NG>(blk_s + b * BYTES + lane * 4 * NG, kw[0]);
               load_words<NG>(blk_s + b * BYTES + (32 + lane) * 4 * NG, kw[1]);
-              load_words<NG>(blk_s + b * BYTES + kv4_k_scales(NG) + g * 4 * NG, ks);
+              load_words<NG>(blk_s + b * BYTES + kv4_scales(NG) + g * 8 * NG, ks);
 #pragma unroll
               for (int j = 0; j < NG; ++j) {
                 uint32_t a[4], c8[4];  // rows g and g + 8
@@ -819,9 +820,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
                 for (int b = 0; b < NB; ++b) {
                   float f0 = 0.f, f1 = 0.f;  // scales of tokens g, g + 8 in this lane's group
                   if (GC * (s + 1) <= NG || GC * s + tg < NG) {
-                    const uint16_t* sp = reinterpret_cast<const uint16_t*>(blk_s + b * BYTES +
-                                                                           kv4_v_scales(NG)) +
-                                         g * 2 * NG + GC * s + tg;
+                    const uint16_t* sp = reinterpret_cast<const uint16_t*>(
+                        blk_s + b * BYTES + kv4_scales(NG) + g * 8 * NG + 4 * NG) + GC * s + tg;
                     f0 = __uint_as_float((uint32_t)sp[0] << 16);
                     f1 = __uint_as_float((uint32_t)sp[NG] << 16);
                   }
@@ -874,8 +874,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
 #pragma unroll
               for (int b = 0; b < NB; ++b) {
                 uint32_t vw[2][NG];
-                load_words<NG>(blk_s + b * BYTES + kv4_v_codes(NG) + lane * 4 * NG, vw[0]);
-                load_words<NG>(blk_s + b * BYTES + kv4_v_codes(NG) + (32 + lane) * 4 * NG, vw[1]);
+                load_words<NG>(blk_s + b * BYTES + kv4_v_codes(NG) + vl * 4 * NG, vw[0]);
+                load_words<NG>(blk_s + b * BYTES + kv4_v_codes(NG) + (32 + vl) * 4 * NG, vw[1]);
 #pragma unroll
                 for (int s = 0; s < SH; ++s) {
                   const uint32_t b0 =
@@ -900,9 +900,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
 #pragma unroll
               for (int b = 0; b < NB; ++b) {
                 uint32_t vw[2][NG], vs[NG];
-                load_words<NG>(blk_s + b * BYTES + kv4_v_codes(NG) + lane * 4 * NG, vw[0]);
-                load_words<NG>(blk_s + b * BYTES + kv4_v_codes(NG) + (32 + lane) * 4 * NG, vw[1]);
-                load_words<NG>(blk_s + b * BYTES + kv4_v_scales(NG) + g * 4 * NG, vs);
+                load_words<NG>(blk_s + b * BYTES + kv4_v_codes(NG) + vl * 4 * NG, vw[0]);
+                load_words<NG>(blk_s + b * BYTES + kv4_v_codes(NG) + (32 + vl) * 4 * NG, vw[1]);
+                load_words<NG>(blk_s + b * BYTES + kv4_scales(NG) + g * 8 * NG + 4 * NG, vs);
 #pragma unroll
                 for (int j = 0; j < NG; ++j) {
                   const float v0 = scale_of<NG>(vs, 0, j), v1 = scale_of<NG>(vs, 1, j);

@@ -14,11 +14,15 @@
 //             feature 32 j + 8 t + e.  Lane (g, t) owns token rows g and g + 8
 //             of the A operand; (w >> 4 i) & 0x000F000F is the feature pair
 //             (i, i + 4), and Q's B operand pairs its features the same way.
-//   V codes   [token / 8][g][t = token % 8 / 2][j]  32-bit words: the low half
-//             is token 2 t, the high half token 2 t + 1; nibble i of a half is
-//             feature 32 j + 4 g + i.  (w >> 4 i) & 0x000F000F is the token
-//             pair the transposed A operand (features x tokens) wants.
-//   K scales, V scales   [g = token % 8][token / 8][j] bf16.
+//   V codes   [token / 8][t = token % 8 / 2][g ^ 2 t][j]  32-bit words: the low
+//             half is token 2 t, the high half token 2 t + 1; nibble i of a half
+//             is feature 32 j + 4 g + i.  (w >> 4 i) & 0x000F000F is the token
+//             pair the transposed A operand (features x tokens) wants.  A pair of
+//             tokens is 32 NG contiguous bytes (a row read alone moves twice its
+//             bytes, not four times as with t innermost); the XOR keeps the
+//             attention's reads from shared memory free of bank conflicts.
+//   scales    [g = token % 8][K, V][token / 8][j] bf16: both rows of a token in
+//             one 32-byte sector.
 #pragma once
 
 #include "common.cuh"
@@ -38,21 +42,22 @@ constexpr float kKv4Tiny = 7.8886090522101181e-31f;  // 2^-100
 // Bytes of the whole block and of its planes, for NG groups.
 __host__ __device__ constexpr int kv4_block_bytes(int ng) { return 576 * ng; }
 __host__ __device__ constexpr int kv4_v_codes(int ng) { return 256 * ng; }
-__host__ __device__ constexpr int kv4_k_scales(int ng) { return 512 * ng; }
-__host__ __device__ constexpr int kv4_v_scales(int ng) { return 544 * ng; }
+__host__ __device__ constexpr int kv4_scales(int ng) { return 512 * ng; }
 
 // Byte offset inside a block of the K word of token tok (0..15), octet t, group j.
 __host__ __device__ constexpr int kv4_k_word(int ng, int tok, int t, int j) {
   return (((tok >> 3) * 32 + (tok & 7) * 4 + t) * ng + j) * 4;
 }
+// Place of lane (g, t) among the 32 of a half's V words.
+__host__ __device__ constexpr int kv4_v_lane(int g, int t) { return t * 8 + (g ^ (2 * t)); }
 // ... of the V half-word (4 features 32 j + 4 g ..) of token tok.
 __host__ __device__ constexpr int kv4_v_half(int ng, int tok, int g, int j) {
-  return kv4_v_codes(ng) + (((tok >> 3) * 32 + g * 4 + ((tok & 7) >> 1)) * ng + j) * 4 +
-         (tok & 1) * 2;
+  return kv4_v_codes(ng) +
+         (((tok >> 3) * 32 + kv4_v_lane(g, (tok & 7) >> 1)) * ng + j) * 4 + (tok & 1) * 2;
 }
-// ... of the scale of token tok, group j, from the plane's start.
-__host__ __device__ constexpr int kv4_scale(int ng, int tok, int j) {
-  return (((tok & 7) * 2 + (tok >> 3)) * ng + j) * 2;
+// ... of the scale of token tok, group j, of K (v = 0) or V (v = 1).
+__host__ __device__ constexpr int kv4_scale(int ng, int v, int tok, int j) {
+  return kv4_scales(ng) + ((((tok & 7) * 2 + v) * 2 + (tok >> 3)) * ng + j) * 2;
 }
 
 #if defined(__CUDACC__)

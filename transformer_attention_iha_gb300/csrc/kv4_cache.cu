@@ -3,18 +3,28 @@
 //
 // Both are byte movers.  Writing a token and head of d features reads 2 d
 // values (4 d bytes of bf16) and writes d + d / 8 bytes; reading back moves
-// the same bytes the other way.  A thread owns 8 neighbouring features, the
-// four threads of a group of 32 find its maximum with two shuffles.
+// the same bytes the other way.
+//
+// Store: a thread owns 8 neighbouring features of K and of V (the four threads
+// of a group of 32 find its maximum with two shuffles), a half-warp a token, a
+// warp two tokens of the call next to each other.  Where these go to an even
+// slot and the next (a prompt), the halves exchange their V codes, so that V is
+// written in whole words like K.
 //
 // Rounding x / s without a division per value: y = x * (1 / s) is off by at
-// most 2^-21 (|y| < 7.1, one rounding of the reciprocal), and x / s of a bf16
-// x and a bf16 s is either exactly half-way between two codes or at least
-// 1 / 512 away from it (2 x and (2 k + 1) s are 8-bit integers times powers of
-// two, so they differ by at least the smaller unit or not at all).  So y is
-// first rounded to a multiple of 2^-14 by adding 776 in the same FMA (776 =
-// 768 + 8 also shifts the code to its nibble), which puts half-way cases
-// exactly half-way, and then to an integer, ties to even, by adding
-// 1.5 * 2^23.
+// most 2^-19 (|y| < 7.1, a reciprocal good to an ulp), and x / s of a bf16 x
+// and a bf16 s is either exactly half-way between two codes or at least 1 / 512
+// away from it (2 x and (2 k + 1) s are 8-bit integers times powers of two, so
+// they differ by at least the smaller unit or not at all).  So y is first
+// rounded to a multiple of 2^-14 by adding 776 in the same FMA (776 = 768 + 8
+// also shifts the code to its nibble), which puts half-way cases exactly
+// half-way, and then to an integer, ties to even, by adding 1.5 * 2^23; the low
+// byte of the sum is the nibble.  Likewise bf16(top / 7) is bf16(top * fl(1/7)):
+// top / 7 of an 8-bit mantissa stays 2^-12 away from every bf16 tie.
+//
+// Load: eight threads a row, each with half of a K octet's words (whole lines
+// over the row) and one g of V.  bf16 output: codes as bf16 (128 + n) - 136,
+// exact, times s in one rounding multiply; f32: s * c, exact.
 #include "kv4.cuh"
 
 namespace iha {
@@ -22,12 +32,31 @@ namespace {
 
 IHA_DEVICE_ERROR_WORD(kv4_cache)
 
-struct Kv4Geom {
-  int N, H, page, blocks_per_page;  // tokens of a batch row, heads
-  int n_slots;                      // n_pages * page
-  int64_t rows;                     // B_outer * B_inner * N * H
-  int Bi;
+// n / d for 0 <= n < 2^31 by multiplication: inv = ceil(2^64 / d) is too large
+// by less than d / 2^64 of itself, so the product by less than 1 / d.
+struct FastDiv {
+  uint64_t inv;
+  int d;
+  __host__ void set(int x) {
+    d = x;
+    inv = x > 1 ? ~0ull / (unsigned)x + 1 : 0;
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return d == 1 ? n : (int)__umul64hi((uint64_t)(unsigned)n, inv);
+  }
 };
+
+struct Kv4Geom {
+  FastDiv N, Bi, page, units;  // tokens of a batch row; inner batch; page; head units of a warp
+  int toks, H, n_units, blocks_per_page;
+  int n_slots;  // n_pages * page
+};
+
+// Where token i of the call lies in a strided view.
+__device__ __forceinline__ int64_t view_of(const Kv4Geom& g, const iha_strides& s, int i) {
+  const int b = g.N.div(i), n = i - b * g.N.d, bo = g.Bi.div(b), bi = b - bo * g.Bi.d;
+  return bo * s.b_outer + bi * s.b_inner + n * s.seq;
+}
 
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, uint32_t (&v)[4]);  // 8 values as bf16 pairs
@@ -60,127 +89,178 @@ __device__ __forceinline__ uint32_t quantise8(const uint32_t (&v)[4], uint32_t& 
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   const float top = __uint_as_float(m << 16);
-  uint32_t word = 0x88888888u;
-  scale_bits = 0;
-  if (m >= 0x7F80u) {
-    scale_bits = 0x7FC0u;
-  } else if (top >= kKv4Tiny) {
-    const float s = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(top, 7.f)));
-    scale_bits = __float_as_uint(s) >> 16;
-    const float inv = __frcp_rn(s);
-    word = 0;
+  const float s = __bfloat162float(__float2bfloat16_rn(top * (1.f / 7.f)));
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  uint32_t r[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x = (e & 1) ? bf16hi_to_f32(v[e >> 1]) : bf16lo_to_f32(v[e >> 1]);
-      const float r = fmaf(x, inv, 776.f) + 12582912.f;
-      word |= (__float_as_uint(r) & 15u) << (4 * e);
-    }
+  for (int i = 0; i < 4; ++i) {
+    float2 x = make_float2(bf16lo_to_f32(v[i]), bf16hi_to_f32(v[i]));
+    x = __ffma2_rn(x, make_float2(inv, inv), make_float2(776.f, 776.f));
+    x = __fadd2_rn(x, make_float2(12582912.f, 12582912.f));
+    r[2 * i] = __float_as_uint(x.x);
+    r[2 * i + 1] = __float_as_uint(x.y);
+  }
+  const uint32_t even = __byte_perm(__byte_perm(r[0], r[2], 0x0040),
+                                    __byte_perm(r[4], r[6], 0x0040), 0x5410);
+  const uint32_t odd = __byte_perm(__byte_perm(r[1], r[3], 0x0040),
+                                   __byte_perm(r[5], r[7], 0x0040), 0x5410);
+  uint32_t word = even | (odd << 4);
+  scale_bits = __float_as_uint(s) >> 16;
+  if (m >= 0x7F80u || top < kKv4Tiny) {  // the same in the group's lanes
+    word = 0x88888888u;
+    scale_bits = m >= 0x7F80u ? 0x7FC0u : 0u;
   }
   return word;
 }
 
-// One thread per 8 features of a row; a row is (batch, token, head).
+// A warp: two tokens, 16 / (lanes of a row) heads each.
 template <typename T, int NG>
 __global__ void __launch_bounds__(256)
     kv4_store_kernel(const T* __restrict__ k, const T* __restrict__ v,
                      const int32_t* __restrict__ slots, uint8_t* __restrict__ cache, Kv4Geom g,
                      iha_strides sk, iha_strides sv) {
-  constexpr int TPR = 4 * NG;  // threads per row
-  const int64_t gi = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = gi / TPR;
-  const int o = (int)(gi - row * TPR);  // octet of the row
-  const bool live = row < g.rows;
-  const int64_t r = live ? row : 0;
-  const int64_t tok = r / g.H;
-  const int head = (int)(r - tok * g.H);
-  const int64_t b = tok / g.N;
-  const int n = (int)(tok - b * g.N);
-  const int64_t bo = b / g.Bi, bi = b - bo * g.Bi;
-  const int slot = __ldg(slots + tok);
+  constexpr int LPR = NG == 3 ? 16 : 4 * NG, HPW = 16 / LPR;  // lanes of a row, heads of a warp
+  const int lane = threadIdx.x & 31;
+  const int id = blockIdx.x * 8 + (threadIdx.x >> 5);  // (token pair, head unit)
+  const int pair = g.units.div(id), unit = id - pair * g.n_units;
+  const int tok = 2 * pair + (lane >> 4), head = unit * HPW + (lane & 15) / LPR;
+  const int o = (lane & 15) % LPR;  // octet of the row
+  const bool live = tok < g.toks && head < g.H && o < 4 * NG;
+  const int slot = live ? __ldg(slots + tok) : -1;
   const bool in = slot >= 0 && slot < g.n_slots;
-  if (live && !in && slot != -1) atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
-  const int pg = in ? slot / g.page : 0, off = in ? slot - pg * g.page : 0;
-  uint8_t* blk = cache + kv4_block_of(pg, off / kKv4Tok, head, g.H, g.blocks_per_page, NG);
-  const int tk = off % kKv4Tok;
-  const int j = o >> 2, t = o & 3;
-  uint32_t x[4], sc;
-  load8<T>(k + bo * sk.b_outer + bi * sk.b_inner + n * sk.seq + head * sk.head + o * 8, x);
-  const uint32_t kw = quantise8(x, sc);
-  if (live && in) {
-    *reinterpret_cast<uint32_t*>(blk + kv4_k_word(NG, tk, t, j)) = kw;
-    if (t == 0)
-      *reinterpret_cast<uint16_t*>(blk + kv4_k_scales(NG) + kv4_scale(NG, tk, j)) = (uint16_t)sc;
+  if (!in && slot != -1) atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
+  uint32_t xk[4] = {0, 0, 0, 0}, xv[4] = {0, 0, 0, 0};
+  if (in) {
+    load8<T>(k + view_of(g, sk, tok) + head * sk.head + o * 8, xk);
+    load8<T>(v + view_of(g, sv, tok) + head * sv.head + o * 8, xv);
   }
-  load8<T>(v + bo * sv.b_outer + bi * sv.b_inner + n * sv.seq + head * sv.head + o * 8, x);
-  const uint32_t vw = quantise8(x, sc);
-  if (live && in) {
+  uint32_t ks, vs;
+  const uint32_t kw = quantise8(xk, ks), vw = quantise8(xv, vs);
+  // the partner's token lies in the other half of this token's words?
+  const int other = __shfl_xor_sync(0xffffffffu, slot, 16);
+  const bool paired = in && other == (slot ^ 1);
+  const bool odd = slot & 1;
+  // of the words of features 4 (2 t) .. and 4 (2 t + 1) .., the even slot's lane
+  // writes the first, the odd slot's the second
+  const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? vw : vw >> 16, 16);
+  if (!in) return;
+  const int pg = g.page.div(slot), off = slot - pg * g.page.d, tk = off % kKv4Tok;
+  uint8_t* blk = cache + kv4_block_of(pg, off / kKv4Tok, head, g.H, g.blocks_per_page, NG);
+  const int j = o >> 2, t = o & 3;
+  *reinterpret_cast<uint32_t*>(blk + kv4_k_word(NG, tk, t, j)) = kw;
+  if (paired) {
+    const uint32_t w = odd ? __byte_perm(got, vw, 0x7610) : __byte_perm(vw, got, 0x5410);
+    *reinterpret_cast<uint32_t*>(blk + kv4_v_half(NG, tk & ~1, 2 * t + (odd ? 1 : 0), j)) = w;
+  } else {
     *reinterpret_cast<uint16_t*>(blk + kv4_v_half(NG, tk, 2 * t, j)) = (uint16_t)vw;
     *reinterpret_cast<uint16_t*>(blk + kv4_v_half(NG, tk, 2 * t + 1, j)) = (uint16_t)(vw >> 16);
-    if (t == 0)
-      *reinterpret_cast<uint16_t*>(blk + kv4_v_scales(NG) + kv4_scale(NG, tk, j)) = (uint16_t)sc;
   }
+  if (t < 2)
+    *reinterpret_cast<uint16_t*>(blk + kv4_scale(NG, t, tk, j)) = (uint16_t)(t == 0 ? ks : vs);
 }
 
-// Code word and scale -> 8 values, written as T (s * c is exact in fp32; the
-// bf16 form rounds once, to nearest even).
-template <typename T>
-__device__ __forceinline__ void write8(T* p, uint32_t word, float s);
-template <>
-__device__ __forceinline__ void write8<__nv_bfloat16>(__nv_bfloat16* p, uint32_t word, float s) {
-  uint32_t u[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    u[i] = pack_bf16x2(s * (float)((int)((word >> (8 * i)) & 15u) - 8),
-                       s * (float)((int)((word >> (8 * i + 4)) & 15u) - 8));
-  *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+// Nibbles 0, 1 (low, high half) of 4-bit fields in the low halves' order -> values.
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t nib, uint32_t s2) {
+  uint32_t x = nib | 0x43004300u;  // bf16 128 + n, exact
+  const uint32_t o = 0x43084308u;  // 136
+  __nv_bfloat162 v = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&x),
+                             *reinterpret_cast<const __nv_bfloat162*>(&o));
+  v = __hmul2(v, *reinterpret_cast<__nv_bfloat162*>(&s2));
+  return *reinterpret_cast<uint32_t*>(&v);
 }
-template <>
-__device__ __forceinline__ void write8<float>(float* p, uint32_t word, float s) {
-  float f[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = s * (float)((int)((word >> (4 * e)) & 15u) - 8);
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+__device__ __forceinline__ float scaled(uint32_t nib, float s) {
+  return s * (__uint_as_float(nib | 0x4B000000u) - 8388616.f);  // 2^23 + n - (2^23 + 8)
 }
 
+// 8 features of a K word, 4 of a V half-word (low 16 bits), times the scale.
+__device__ __forceinline__ void write_k(__nv_bfloat16* p, uint32_t w, uint32_t sc) {
+  const uint32_t s2 = sc | (sc << 16);
+  uint32_t v[4];  // features (i, i + 4)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = scaled_pair((w >> (4 * i)) & 0x000F000Fu, s2);
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                 __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+}
+__device__ __forceinline__ void write_v(__nv_bfloat16* p, uint32_t h, uint32_t sc) {
+  const uint32_t s2 = sc | (sc << 16), hi = h >> 8;
+  *reinterpret_cast<uint2*>(p) = make_uint2(scaled_pair((h | (h << 12)) & 0x000F000Fu, s2),
+                                            scaled_pair((hi | (hi << 12)) & 0x000F000Fu, s2));
+}
+__device__ __forceinline__ void write_k(float* p, uint32_t w, uint32_t sc) {
+  const float s = __uint_as_float(sc << 16);
+#pragma unroll
+  for (int q = 0; q < 2; ++q, w >>= 16)
+    reinterpret_cast<float4*>(p)[q] =
+        make_float4(scaled(w & 15u, s), scaled((w >> 4) & 15u, s), scaled((w >> 8) & 15u, s),
+                    scaled((w >> 12) & 15u, s));
+}
+__device__ __forceinline__ void write_v(float* p, uint32_t h, uint32_t sc) {
+  const float s = __uint_as_float(sc << 16);
+  *reinterpret_cast<float4*>(p) =
+      make_float4(scaled(h & 15u, s), scaled((h >> 4) & 15u, s), scaled((h >> 8) & 15u, s),
+                  scaled((h >> 12) & 15u, s));
+}
+
+// Eight threads a row of a token and head.
 template <typename T, int NG>
 __global__ void __launch_bounds__(256)
     kv4_load_kernel(const uint8_t* __restrict__ cache, const int32_t* __restrict__ slots,
                     T* __restrict__ k, T* __restrict__ v, Kv4Geom g, iha_strides sk,
                     iha_strides sv) {
-  constexpr int TPR = 4 * NG;
-  const int64_t gi = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = gi / TPR;
-  if (row >= g.rows) return;
-  const int o = (int)(gi - row * TPR);
-  const int64_t tok = row / g.H;
-  const int head = (int)(row - tok * g.H);
-  const int64_t b = tok / g.N;
-  const int n = (int)(tok - b * g.N);
-  const int64_t bo = b / g.Bi, bi = b - bo * g.Bi;
+  constexpr int HALF = (NG + 1) / 2;  // K words of a thread
+  const int64_t row64 = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
+  if (row64 >= (int64_t)g.toks * g.H) return;
+  const int row = (int)row64, i = threadIdx.x & 7;
+  const int tok = g.units.div(row), head = row - tok * g.H;
   const int slot = __ldg(slots + tok);
   const bool in = slot >= 0 && slot < g.n_slots;
   if (!in && slot != -1) atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
-  const int j = o >> 2, t = o & 3;
-  uint32_t kw = 0x88888888u, vw = 0x88888888u;
-  float ks = 0.f, vs = 0.f;
+  const int t = i >> 1, j0 = (i & 1) * HALF;
+  uint32_t kw[HALF], vh[NG], ks[HALF], vs[NG];
+#pragma unroll
+  for (int q = 0; q < HALF; ++q) kw[q] = ks[q] = 0;
+#pragma unroll
+  for (int j = 0; j < NG; ++j) vh[j] = vs[j] = 0;
   if (in) {
-    const int pg = slot / g.page, off = slot - pg * g.page, tk = off % kKv4Tok;
+    const int pg = g.page.div(slot), off = slot - pg * g.page.d, tk = off % kKv4Tok;
     const uint8_t* blk =
         cache + kv4_block_of(pg, off / kKv4Tok, head, g.H, g.blocks_per_page, NG);
-    kw = *reinterpret_cast<const uint32_t*>(blk + kv4_k_word(NG, tk, t, j));
-    vw = *reinterpret_cast<const uint16_t*>(blk + kv4_v_half(NG, tk, 2 * t, j)) |
-         ((uint32_t)*reinterpret_cast<const uint16_t*>(blk + kv4_v_half(NG, tk, 2 * t + 1, j))
-          << 16);
-    ks = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(
-                             blk + kv4_k_scales(NG) + kv4_scale(NG, tk, j))
-                         << 16);
-    vs = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(
-                             blk + kv4_v_scales(NG) + kv4_scale(NG, tk, j))
-                         << 16);
+    const uint8_t* vp = blk + kv4_v_half(NG, tk & ~1, i, 0);  // words of the token and its partner
+    const int sh = (tk & 1) * 16;
+    if constexpr (NG == 4) {
+      const uint2 a = *reinterpret_cast<const uint2*>(blk + kv4_k_word(NG, tk, t, j0));
+      const uint4 b = *reinterpret_cast<const uint4*>(vp);
+      const uint32_t c = *reinterpret_cast<const uint32_t*>(blk + kv4_scale(NG, 0, tk, j0));
+      const uint2 e = *reinterpret_cast<const uint2*>(blk + kv4_scale(NG, 1, tk, 0));
+      kw[0] = a.x, kw[1] = a.y;
+      vh[0] = b.x, vh[1] = b.y, vh[2] = b.z, vh[3] = b.w;
+      ks[0] = c & 0xFFFFu, ks[1] = c >> 16;
+      vs[0] = e.x & 0xFFFFu, vs[1] = e.x >> 16, vs[2] = e.y & 0xFFFFu, vs[3] = e.y >> 16;
+    } else {
+#pragma unroll
+      for (int q = 0; q < HALF; ++q)
+        if (j0 + q < NG) {
+          kw[q] = *reinterpret_cast<const uint32_t*>(blk + kv4_k_word(NG, tk, t, j0 + q));
+          ks[q] = *reinterpret_cast<const uint16_t*>(blk + kv4_scale(NG, 0, tk, j0 + q));
+        }
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        vh[j] = reinterpret_cast<const uint32_t*>(vp)[j];
+        vs[j] = *reinterpret_cast<const uint16_t*>(blk + kv4_scale(NG, 1, tk, j));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NG; ++j) vh[j] = (vh[j] >> sh) & 0xFFFFu;
   }
-  write8<T>(k + bo * sk.b_outer + bi * sk.b_inner + n * sk.seq + head * sk.head + o * 8, kw, ks);
-  write8<T>(v + bo * sv.b_outer + bi * sv.b_inner + n * sv.seq + head * sv.head + o * 8, vw, vs);
+  T* pk = k + view_of(g, sk, tok) + head * sk.head;
+  T* pv = v + view_of(g, sv, tok) + head * sv.head;
+#pragma unroll
+  for (int q = 0; q < HALF; ++q)
+    if (j0 + q < NG) write_k(pk + 32 * (j0 + q) + 8 * t, kw[q], ks[q]);
+#pragma unroll
+  for (int j = 0; j < NG; ++j) write_v(pv + 32 * j + 4 * i, vh[j], vs[j]);
 }
 
 bool strides_ok(const iha_strides& s, int es) {
@@ -232,7 +312,7 @@ iha_status move(const char* name, bool store, const void* k, const void* v, cons
   if (!strides_ok(sk, es) || !strides_ok(sv, es))
     return fail(IHA_ERR_ALIGNMENT, "%s: strides must be multiples of 16 bytes", name);
   const int64_t toks = (int64_t)B_outer * B_inner * N, rows = toks * Hkv;
-  if (toks > INT32_MAX || rows > INT32_MAX)
+  if (toks > INT32_MAX - 1 || rows > INT32_MAX)
     return fail(IHA_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 rows in one call", name);
   bool nk, nv;
   const int64_t bk = view_bytes(sk, B_outer, B_inner, N, Hkv, d, es, &nk);
@@ -250,16 +330,20 @@ iha_status move(const char* name, bool store, const void* k, const void* v, cons
           (N > 1 && t->seq == 0) || (Hkv > 1 && t->head == 0))
         return fail(IHA_ERR_INVALID_ARG, "%s: an output repeats rows (stride 0)", name);
   }
+  const int ng = d / kKv4Group;
+  const int heads_of_warp = ng == 3 ? 1 : 4 / ng;
   Kv4Geom g;
-  g.N = N;
+  g.N.set(N);
+  g.Bi.set(B_inner);
+  g.page.set(page);
+  g.toks = (int)toks;
   g.H = Hkv;
-  g.page = page;
   g.blocks_per_page = page / kKv4Tok;
   g.n_slots = n_pages * page;
-  g.rows = rows;
-  g.Bi = B_inner;
-  const int ng = d / kKv4Group;
-  const int64_t blocks = (rows * 4 * ng + 255) / 256;
+  g.n_units = store ? (Hkv + heads_of_warp - 1) / heads_of_warp : Hkv;
+  g.units.set(g.n_units);
+  // store: 8 warps a CTA, a warp per token pair and head unit; load: 32 rows a CTA
+  const int64_t blocks = store ? ((toks + 1) / 2 * g.n_units + 7) / 8 : (rows + 31) / 32;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* c = static_cast<uint8_t*>(const_cast<void*>(cache));
   IHA_NG_SWITCH(ng, {
