@@ -90,6 +90,26 @@ def test_round_trip_is_exact(T, dtype, B, N, H, d, page):
     assert T.device_error() == 0
 
 
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+@pytest.mark.parametrize("first", [0, 1])
+def test_many_rows_in_order(T, d, first):
+    """A prompt's worth of rows (the store's form of several heads a warp), slots
+    in order from an even and an odd one, heads that leave a unit part empty."""
+    import torch
+    N, H, page = 3301, 10, 16
+    k, v = S.normal((1, N, H, d), 14, 0), S.normal((1, N, H, d), 14, 1)
+    cache = cache_of(T, -(-N // page) + 1, page, H, d)
+    slots = np.arange(first, first + N, dtype=np.int32)[None]
+    slots[0, 100:103] = -1
+    T.kv4_store(to_dev(k), to_dev(v), to_dev(slots), cache, page)
+    gk, gv = T.kv4_load(cache, to_dev(slots), H, d, page, dtype=torch.float32)
+    for got, x in ((gk, k), (gv, v)):
+        r = O.kv4_values(x)
+        r[0, 100:103] = 0.0
+        np.testing.assert_array_equal(to_f64(got), r)
+    assert T.device_error() == 0
+
+
 def test_only_named_slots_change_and_load_takes_any_slots(T):
     import torch
     H, d, page = 3, 64, 16

@@ -114,50 +114,68 @@ __device__ __forceinline__ uint32_t quantise8(const uint32_t (&v)[4], uint32_t& 
   return word;
 }
 
-// A warp: two tokens, 16 / (lanes of a row) heads each.
-template <typename T, int NG>
+// A warp: two tokens, UN head units of 16 / (lanes of a row) heads each.  All
+// rows of a thread are on their way before the first is quantised.
+template <typename T, int NG, int UN>
 __global__ void __launch_bounds__(256)
     kv4_store_kernel(const T* __restrict__ k, const T* __restrict__ v,
                      const int32_t* __restrict__ slots, uint8_t* __restrict__ cache, Kv4Geom g,
                      iha_strides sk, iha_strides sv) {
-  constexpr int LPR = NG == 3 ? 16 : 4 * NG, HPW = 16 / LPR;  // lanes of a row, heads of a warp
+  constexpr int LPR = NG == 3 ? 16 : 4 * NG, HPW = 16 / LPR;  // lanes of a row, heads of a unit
   const int lane = threadIdx.x & 31;
-  const int id = blockIdx.x * 8 + (threadIdx.x >> 5);  // (token pair, head unit)
+  const int id = blockIdx.x * 8 + (threadIdx.x >> 5);  // (token pair, head units)
   const int pair = g.units.div(id), unit = id - pair * g.n_units;
-  const int tok = 2 * pair + (lane >> 4), head = unit * HPW + (lane & 15) / LPR;
+  const int tok = 2 * pair + (lane >> 4), head0 = unit * UN * HPW + (lane & 15) / LPR;
   const int o = (lane & 15) % LPR;  // octet of the row
-  const bool live = tok < g.toks && head < g.H && o < 4 * NG;
+  const bool live = tok < g.toks && o < 4 * NG;
   const int slot = live ? __ldg(slots + tok) : -1;
   const bool in = slot >= 0 && slot < g.n_slots;
   if (!in && slot != -1) atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
-  uint32_t xk[4] = {0, 0, 0, 0}, xv[4] = {0, 0, 0, 0};
-  if (in) {
-    load8<T>(k + view_of(g, sk, tok) + head * sk.head + o * 8, xk);
-    load8<T>(v + view_of(g, sv, tok) + head * sv.head + o * 8, xv);
+  uint32_t xk[UN][4], xv[UN][4];
+  {
+    const int b = g.N.div(tok), n = tok - b * g.N.d, bo = g.Bi.div(b), bi = b - bo * g.Bi.d;
+    const T* pk = k + bo * sk.b_outer + bi * sk.b_inner + n * sk.seq + head0 * sk.head + o * 8;
+    const T* pv = v + bo * sv.b_outer + bi * sv.b_inner + n * sv.seq + head0 * sv.head + o * 8;
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xk[u][i] = xv[u][i] = 0;
+      if (in && head0 + u * HPW < g.H) {
+        load8<T>(pk, xk[u]);
+        load8<T>(pv, xv[u]);
+      }
+      pk += HPW * sk.head;
+      pv += HPW * sv.head;
+    }
   }
-  uint32_t ks, vs;
-  const uint32_t kw = quantise8(xk, ks), vw = quantise8(xv, vs);
   // the partner's token lies in the other half of this token's words?
   const int other = __shfl_xor_sync(0xffffffffu, slot, 16);
   const bool paired = in && other == (slot ^ 1);
   const bool odd = slot & 1;
-  // of the words of features 4 (2 t) .. and 4 (2 t + 1) .., the even slot's lane
-  // writes the first, the odd slot's the second
-  const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? vw : vw >> 16, 16);
-  if (!in) return;
-  const int pg = g.page.div(slot), off = slot - pg * g.page.d, tk = off % kKv4Tok;
-  uint8_t* blk = cache + kv4_block_of(pg, off / kKv4Tok, head, g.H, g.blocks_per_page, NG);
-  const int j = o >> 2, t = o & 3;
-  *reinterpret_cast<uint32_t*>(blk + kv4_k_word(NG, tk, t, j)) = kw;
-  if (paired) {
-    const uint32_t w = odd ? __byte_perm(got, vw, 0x7610) : __byte_perm(vw, got, 0x5410);
-    *reinterpret_cast<uint32_t*>(blk + kv4_v_half(NG, tk & ~1, 2 * t + (odd ? 1 : 0), j)) = w;
-  } else {
-    *reinterpret_cast<uint16_t*>(blk + kv4_v_half(NG, tk, 2 * t, j)) = (uint16_t)vw;
-    *reinterpret_cast<uint16_t*>(blk + kv4_v_half(NG, tk, 2 * t + 1, j)) = (uint16_t)(vw >> 16);
+  const int pg = in ? g.page.div(slot) : 0, off = in ? slot - pg * g.page.d : 0;
+  const int tk = off % kKv4Tok, j = o >> 2, t = o & 3;
+  uint8_t* blk = cache + kv4_block_of(pg, off / kKv4Tok, head0, g.H, g.blocks_per_page, NG);
+  const int64_t next = (int64_t)HPW * g.blocks_per_page * kv4_block_bytes(NG);
+#pragma unroll
+  for (int u = 0; u < UN; ++u, blk += next) {
+    uint32_t ks, vs;
+    const uint32_t kw = quantise8(xk[u], ks), vw = quantise8(xv[u], vs);
+    // of the words of features 4 (2 t) .. and 4 (2 t + 1) .., the even slot's lane
+    // writes the first, the odd slot's the second
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? vw : vw >> 16, 16);
+    if (in && head0 + u * HPW < g.H) {
+      *reinterpret_cast<uint32_t*>(blk + kv4_k_word(NG, tk, t, j)) = kw;
+      if (paired) {
+        const uint32_t w = odd ? __byte_perm(got, vw, 0x7610) : __byte_perm(vw, got, 0x5410);
+        *reinterpret_cast<uint32_t*>(blk + kv4_v_half(NG, tk & ~1, 2 * t + (odd ? 1 : 0), j)) = w;
+      } else {
+        *reinterpret_cast<uint16_t*>(blk + kv4_v_half(NG, tk, 2 * t, j)) = (uint16_t)vw;
+        *reinterpret_cast<uint16_t*>(blk + kv4_v_half(NG, tk, 2 * t + 1, j)) = (uint16_t)(vw >> 16);
+      }
+      if (t < 2)
+        *reinterpret_cast<uint16_t*>(blk + kv4_scale(NG, t, tk, j)) = (uint16_t)(t == 0 ? ks : vs);
+    }
   }
-  if (t < 2)
-    *reinterpret_cast<uint16_t*>(blk + kv4_scale(NG, t, tk, j)) = (uint16_t)(t == 0 ? ks : vs);
 }
 
 // Nibbles 0, 1 (low, high half) of 4-bit fields in the low halves' order -> values.
@@ -289,6 +307,28 @@ bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
     default: { constexpr int kNG = 4; __VA_ARGS__; } break;     \
   }
 
+// Head units of a warp.  Few rows: one, for the most warps.  Many bf16 rows: four,
+// which spreads the address arithmetic over them (8192 tokens x 80 heads of 128:
+// 72 against 101 us, 5.96 TB/s).  f32 rows carry twice the bytes a value and are
+// bound by them with one (8192 x 40: 60 us, 6.3 TB/s, against 70 with four).
+constexpr int kStoreUnits = 4;
+constexpr int64_t kStoreMany = 32768;  // rows (a token and head)
+
+template <typename T, int NG>
+void launch_store(int un, unsigned blocks, cudaStream_t s, const void* k, const void* v,
+                  const int32_t* slots, uint8_t* cache, const Kv4Geom& g, iha_strides sk,
+                  iha_strides sv) {
+  const T* tk = static_cast<const T*>(k);
+  const T* tv = static_cast<const T*>(v);
+  if constexpr (sizeof(T) == 2) {
+    if (un > 1) {
+      kv4_store_kernel<T, NG, kStoreUnits><<<blocks, 256, 0, s>>>(tk, tv, slots, cache, g, sk, sv);
+      return;
+    }
+  }
+  kv4_store_kernel<T, NG, 1><<<blocks, 256, 0, s>>>(tk, tv, slots, cache, g, sk, sv);
+}
+
 iha_status move(const char* name, bool store, const void* k, const void* v, const int32_t* slots,
                 const void* cache, int B_outer, int B_inner, int N, int n_pages, int page, int Hkv,
                 int d, iha_strides sk, iha_strides sv, iha_dtype dt, void* stream) {
@@ -340,7 +380,8 @@ iha_status move(const char* name, bool store, const void* k, const void* v, cons
   g.H = Hkv;
   g.blocks_per_page = page / kKv4Tok;
   g.n_slots = n_pages * page;
-  g.n_units = store ? (Hkv + heads_of_warp - 1) / heads_of_warp : Hkv;
+  const int un = store && dt == IHA_BF16 && rows >= kStoreMany ? kStoreUnits : 1;
+  g.n_units = store ? (Hkv + heads_of_warp * un - 1) / (heads_of_warp * un) : Hkv;
   g.units.set(g.n_units);
   // store: 8 warps a CTA, a warp per token pair and head unit; load: 32 rows a CTA
   const int64_t blocks = store ? ((toks + 1) / 2 * g.n_units + 7) / 8 : (rows + 31) / 32;
@@ -349,12 +390,9 @@ iha_status move(const char* name, bool store, const void* k, const void* v, cons
   IHA_NG_SWITCH(ng, {
     if (store) {
       if (dt == IHA_BF16)
-        kv4_store_kernel<__nv_bfloat16, kNG><<<(unsigned)blocks, 256, 0, s>>>(
-            static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), slots, c,
-            g, sk, sv);
+        launch_store<__nv_bfloat16, kNG>(un, (unsigned)blocks, s, k, v, slots, c, g, sk, sv);
       else
-        kv4_store_kernel<float, kNG><<<(unsigned)blocks, 256, 0, s>>>(
-            static_cast<const float*>(k), static_cast<const float*>(v), slots, c, g, sk, sv);
+        launch_store<float, kNG>(un, (unsigned)blocks, s, k, v, slots, c, g, sk, sv);
     } else {
       if (dt == IHA_BF16)
         kv4_load_kernel<__nv_bfloat16, kNG><<<(unsigned)blocks, 256, 0, s>>>(
