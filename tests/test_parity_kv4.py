@@ -459,7 +459,8 @@ def test_streams(T):
 @pytest.mark.parametrize("B,N,H,P,d,dtype", [
     (1, 1, 20, 4, 128, "bf16"), (3, 5, 20, 4, 128, "bf16"), (7, 1, 4, 2, 64, "bf16"),
     (2, 3, 32, 4, 64, "bf16"), (1, 9, 8, 1, 32, "bf16"), (2, 4, 4, 2, 32, "f32"),
-    (1, 3, 20, 4, 128, "f32")])
+    (1, 3, 20, 4, 128, "f32"), (64, 1, 5, 3, 128, "bf16"), (13, 5, 5, 3, 128, "bf16"),
+    (2, 32, 1, 1, 64, "bf16"), (5, 13, 32, 4, 64, "bf16")])
 def test_premix_at_positions(T, B, N, H, P, d, dtype):
     xs = [S.normal((B, N, H, d), 140, t, dtype=dtype) for t in range(3)]
     ws = [S.premix_weight(H, P, 141, t) for t in range(3)]

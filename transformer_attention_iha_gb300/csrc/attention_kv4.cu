@@ -51,13 +51,13 @@ IHA_DEVICE_ERROR_WORD(attention_kv4)
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-// A warp's ring: stages of up to run_of(NT) blocks.  Longer stages spread the
+// A warp's ring: stages of up to kRun blocks.  Longer stages spread the
 // cost of a wait and a refill; 12 warps of 2 x 4 blocks measured better than 16
 // of 2 x 2 (131071 keys x 80 heads: 241 against 260 us; 8 warps: 256).
 constexpr int kStages = 2;
-__host__ __device__ constexpr int run_of(int nt) { return nt == 1 ? 4 : 2; }
+constexpr int kRun = 4;
 // CTAs an SM holds at once (registers and shared memory allow that many).
-__host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 4 ? 2 : 3; }
+__host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
 // FEW: the codes' offset leaves O after this many blocks (256 tokens): it costs
 // 32 FMAs, and O has grown by 8 s per unit of probability until then.
 constexpr int kFlush = 16;
@@ -67,7 +67,9 @@ constexpr int kUnitCost = 6;  // positions a unit takes besides its blocks
 constexpr int kMinShare = 4;
 constexpr int kMaxCtas = 480;  // counters for 152 SMs x 3 CTAs and some
 constexpr int kCounterBytes = kMaxCtas * 4;
-constexpr int kCtaParts = 2 + 2 * kWarps;
+// Parts a CTA may leave in the workspace: of the unit it begins in and the one it
+// ends in; and of the unit each of its warps begins in, for the CTA itself.
+constexpr int kCtaParts = 2 + kWarps;
 
 struct Kv4AttnParams {
   const __nv_bfloat16* q;
@@ -77,8 +79,7 @@ struct Kv4AttnParams {
   __nv_bfloat16* o;
   float* lse;
   unsigned* counters;  // [kMaxCtas], zero between calls
-  float* parts;        // [CTAs][2 + 2 kWarps][part_stride]: units begun before the CTA and
-                       // in it; heads and tails of its warps that shared memory cannot hold
+  float* parts;        // [CTAs][kCtaParts][part_stride]
   int part_cols, part_stride;
   int B, Nq, Hq, Hkv, G, ncols, ncb;  // ncols = Nq * G columns of a key-value head, in ncb blocks
   unsigned long long inv_g;           // ceil(2^32 / G): col / G = col * inv_g >> 32
@@ -261,7 +262,7 @@ struct Part {
 template <int NG, int NT>
 struct Smem {
   // a warp's ring; when it has run out, the part of the unit its stretch ends in
-  uint8_t ring[kWarps][kStages][run_of(NT)][kv4_block_bytes(NG)];
+  uint8_t ring[kWarps][kStages][kRun][kv4_block_bytes(NG)];
   uint4 q[NT > 1 ? kWarps : 1][NT > 1 ? NT * NG * 32 : 1];
   // -8 2^-24 sum of a group's q of columns 2 t and 2 t + 1, twice: an accumulator's start
   float4 qc[kWarps][NT * NG][4];
@@ -274,8 +275,6 @@ struct Smem {
   int span[kWarps + 1][8];
   int last[2], of[2][2];  // unit at each end of the stretch: joined here, its CTAs
   int abort;
-  static constexpr bool kTailInRing =
-      sizeof(uint8_t[kStages][run_of(NT)][kv4_block_bytes(NG)]) >= sizeof(float) * Part<NG, NT>::FLOATS;
 };
 
 // Running join of softmax parts.
@@ -376,8 +375,7 @@ template <int NG, int NT, int GC, bool ONE>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
     attn_kv4_kernel(const Kv4AttnParams p) {
   constexpr int D = 32 * NG, COLS = 8 * NT, BYTES = kv4_block_bytes(NG);
-  constexpr int NB = NT == 1 ? 2 : 1;  // blocks computed together (registers allow)
-  constexpr int kRun = run_of(NT);
+  constexpr int NB = 2;            // blocks computed together
   constexpr int ES = ONE ? 2 : 1;      // step over the columns of a pair
   constexpr bool FEW = GC > 1;
   constexpr int REAL = FEW ? 8 / GC : 8;           // columns of a B operand that differ
@@ -455,13 +453,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
   // where a warp of this CTA leaves its part of a unit that ends in its stretch
   // after beginning before it, and of one that goes on after it
   float* const cta_parts = p.parts + (int64_t)blockIdx.x * kCtaParts * p.part_stride;
-  auto head_of = [&](int w) {
-    return cta_parts + (2 + w) * p.part_stride;
-  };
-  auto tail_of = [&](int w) {
-    return Smem<NG, NT>::kTailInRing ? reinterpret_cast<float*>(sm.ring[w])
-                                     : cta_parts + (2 + kWarps + w) * p.part_stride;
-  };
+  auto head_of = [&](int w) { return cta_parts + (2 + w) * p.part_stride; };
+  auto tail_of = [&](int w) { return reinterpret_cast<float*>(sm.ring[w]); };
   bool ok = true;
   if (stretch > 0) {
     Unit u;
@@ -700,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
 #pragma unroll 1
           for (int k0 = 0; k0 < kRun; k0 += NB) {
             const int rk = r + k0;
-            if (NB < kRun && rk >= r1) break;
+            if (rk >= r1) break;
             const uint8_t* blk_s = sm.ring[warp][stage][k0];
             float x[NT][NB][4];  // (token g, columns 2t, 2t+1), (token g + 8, ...)
 #pragma unroll
@@ -1091,9 +1084,11 @@ bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
   return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
 }
 
-// Column blocks of 8, 16 or 32: the fewest passes over the cache; a pass of 16
-// or 32 columns unpacks each code once for all of them.
-int pick_nt(int64_t ncols) { return ncols <= 8 ? 1 : (ncols <= 16 ? 2 : 4); }
+// Column blocks of 8 or 16: a pass of 16 columns unpacks each code once for both
+// halves.  (8 sequences of 16384 keys, 8 key heads of 128: 16 columns 70 us against
+// 81 in two passes of 8; 32 columns 116, against 141 in passes of 8 and 138 in one
+// of 32, whose accumulators leave too few warps and spill.)
+int pick_nt(int64_t ncols) { return ncols <= 8 ? 1 : 2; }
 
 int part_cols(int64_t ncols) {
   const int64_t cols = 8 * pick_nt(ncols);
@@ -1108,6 +1103,8 @@ iha_status launch_nt(const Kv4AttnParams& p, int grid, cudaStream_t s) {
   static_assert((sizeof(Smem<NG, NT>) + 1024) * ctas_per_sm(NT) <= 228 * 1024,
                 "4-bit attention: the CTAs of an SM do not fit its shared memory");
   static_assert(sizeof(Smem<NG, NT>::ring) >= kThreads * 6 * sizeof(float), "scratch of the join");
+  static_assert(sizeof(Smem<NG, NT>::ring) / kWarps >= Part<NG, NT>::FLOATS * sizeof(float),
+                "a warp's part of a unit goes into its ring");
   static SmemLimit limit;
   const cudaError_t e = limit.ensure(attn_kv4_kernel<NG, NT, GC, ONE>, (int)sizeof(Smem<NG, NT>));
   if (e != cudaSuccess)
@@ -1120,8 +1117,7 @@ iha_status launch(const Kv4AttnParams& p, int nt, int grid, cudaStream_t s) {
   if (p.ncols == 1) return launch_nt<NG, 1, 4, true>(p, grid, s);
   if (p.ncols == 2) return launch_nt<NG, 1, 4, false>(p, grid, s);
   if (p.ncols <= 4) return launch_nt<NG, 1, 2, false>(p, grid, s);
-  if (nt == 1) return launch_nt<NG, 1, 1, false>(p, grid, s);
-  return nt == 2 ? launch_nt<NG, 2, 1, false>(p, grid, s) : launch_nt<NG, 4, 1, false>(p, grid, s);
+  return nt == 1 ? launch_nt<NG, 1, 1, false>(p, grid, s) : launch_nt<NG, 2, 1, false>(p, grid, s);
 }
 
 }  // namespace

@@ -93,6 +93,73 @@ __device__ __forceinline__ float2 rope_inv_freq(const RopeTable& rt, int i) {
   return r;
 }
 
+// Few tokens (a decode step): Q, K and V of a handful of tokens at their
+// positions, on the CUDA cores.  The tensor-core kernel is built to stream
+// tokens: its CTAs stage the whole W as bf16 hi | lo and start a TMA pipeline
+// before the first token.  Here a CTA takes 16 pseudo-heads of one token of one
+// tensor: W's 16 rows and the token's X go to shared memory (fp32), a thread
+// holds features i and i + d/2 (RoPE partners) of 8 (d = 128) or 4 rows, and
+// loops over the source heads.  Latency-bound: one load, one barrier, H steps.
+// H = 20, P = 4, d = 128: 1 token 3.8 us (7.9 on the tensor-core kernel), 16
+// tokens 4.5 (8.7), 64 tokens 6.8 (8.9), 96 tokens 8.4 (9.0), 128 tokens 10.7 (9.7):
+// kFewTokens lies where both are close.
+constexpr int kFewRows = 16, kFewThreads = 128;
+
+struct FewParams {
+  const __nv_bfloat16* x[3];
+  const float* w[3];
+  __nv_bfloat16* y[3];
+  const int32_t* pos;
+  int H, HP;
+  RopeTable rt;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kFewThreads) premix_few_kernel(const __grid_constant__ FewParams p) {
+  constexpr int HALF = D / 2, R = kFewRows * HALF / kFewThreads;  // rows of a thread
+  __shared__ __align__(16) float xs[32][D];
+  __shared__ __align__(16) float ws[32][kFewRows];
+  const int tid = threadIdx.x, tok = blockIdx.x, tns = blockIdx.z, row0 = blockIdx.y * kFewRows;
+  const float* __restrict__ w = p.w[tns];
+  const __nv_bfloat16* __restrict__ x = p.x[tns] + (int64_t)tok * p.H * D;
+  for (int i = tid; i < p.H * D / 8; i += kFewThreads) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(x) + i);
+    float4* d = reinterpret_cast<float4*>(&xs[0][0] + 8 * i);
+    d[0] = make_float4(bf16lo_to_f32(u.x), bf16hi_to_f32(u.x), bf16lo_to_f32(u.y), bf16hi_to_f32(u.y));
+    d[1] = make_float4(bf16lo_to_f32(u.z), bf16hi_to_f32(u.z), bf16lo_to_f32(u.w), bf16hi_to_f32(u.w));
+  }
+  for (int i = tid; i < kFewRows * p.H; i += kFewThreads) {
+    const int r = i / p.H, s = i - r * p.H;
+    ws[s][r] = row0 + r < p.HP ? __ldg(w + (row0 + r) * p.H + s) : 0.f;
+  }
+  const int i = tid % HALF, r0 = tid / HALF * R;
+  float c = 1.f, sn = 0.f;
+  if (tns < 2) rope_cos_sin(__ldg(p.pos + tok), p.rt.hi[i], p.rt.lo[i], c, sn);
+  __syncthreads();
+  float a[R], b[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) a[r] = b[r] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < p.H; ++s) {
+    const float xa = xs[s][i], xb = xs[s][i + HALF];
+#pragma unroll
+    for (int r = 0; r < R; r += 4) {
+      const float4 w4 = *reinterpret_cast<const float4*>(&ws[s][r0 + r]);
+      a[r] = fmaf(w4.x, xa, a[r]), b[r] = fmaf(w4.x, xb, b[r]);
+      a[r + 1] = fmaf(w4.y, xa, a[r + 1]), b[r + 1] = fmaf(w4.y, xb, b[r + 1]);
+      a[r + 2] = fmaf(w4.z, xa, a[r + 2]), b[r + 2] = fmaf(w4.z, xb, b[r + 2]);
+      a[r + 3] = fmaf(w4.w, xa, a[r + 3]), b[r + 3] = fmaf(w4.w, xb, b[r + 3]);
+    }
+  }
+  __nv_bfloat16* y = p.y[tns] + ((int64_t)tok * p.HP + row0 + r0) * D + i;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (row0 + r0 + r < p.HP) {
+      y[r * D] = __float2bfloat16_rn(fmaf(a[r], c, -b[r] * sn));
+      y[r * D + HALF] = __float2bfloat16_rn(fmaf(b[r], c, a[r] * sn));
+    }
+}
+
 __device__ __forceinline__ void raise_error(volatile int* abort_flag) {
   *abort_flag = 1;
   atomicOr(&g_dev_error, DEV_ERR_WAIT_TIMEOUT);
@@ -448,6 +515,31 @@ iha_status premix_fwd_tc_multi(int ntens, const void* const* x, const float* con
   if (grid > ntens * p.n_stages) grid = ntens * p.n_stages;
   kern<<<grid, kThreads, smem, stream>>>(maps, p);
   return check_launch("premix forward");
+}
+
+bool premix_few_supported(int ntok, int H, int P, int d) {
+  return ntok <= kFewTokens && premix_tc_supported(H, P, d);
+}
+
+iha_status premix_few_at(const void* const* x, const float* const* w, void* const* y,
+                         const int32_t* pos, int ntok, int H, int P, int d, float rope_base,
+                         cudaStream_t stream) {
+  FewParams p;
+  for (int t = 0; t < 3; ++t) {
+    p.x[t] = static_cast<const __nv_bfloat16*>(x[t]);
+    p.w[t] = w[t];
+    p.y[t] = static_cast<__nv_bfloat16*>(y[t]);
+  }
+  p.pos = pos;
+  p.H = H;
+  p.HP = H * P;
+  make_rope_table(&p.rt, d, rope_base);
+  const dim3 grid(ntok, (p.HP + kFewRows - 1) / kFewRows, 3);
+  if (d == 128)
+    premix_few_kernel<128><<<grid, kFewThreads, 0, stream>>>(p);
+  else
+    premix_few_kernel<64><<<grid, kFewThreads, 0, stream>>>(p);
+  return check_launch("iha_premix_fwd_qkv_at");
 }
 
 iha_status premix_fwd_tc(const void* x, const float* w, void* y, int B, int N, int H, int P,
