@@ -169,6 +169,7 @@ OP_INPUTS = {
     "long_premix_fwd_qkv": [f"l{a}_{t}" for t in "qkv" for a in "xw"],
     "long_attention_causal": [f"l{a}_{t}" for t in "qkv" for a in "xw"],
     "mu_attention_qpool": [],   # generated on the device (see qpool_case)
+    "kv4_store": [], "kv4_load": [], "kv4_decode": [],   # likewise (see kv4_case)
 }
 
 
@@ -283,6 +284,40 @@ def qpool_case(T, torch, device):
     nbytes = units * (3 * hq.T + hq.Tq) * hq.head_dim * 2
     flops = 4 * hq.head_dim * hq.Tq * hq.T * units
     return run, nbytes, flops
+
+
+def kv4_case(T, torch, device, name):
+    """The 4-bit cache at the LLaMA layer's 80 pseudo-heads of 128: (enqueue
+    function, algorithmic bytes, flops) of writing or reading back a prompt of
+    8192 tokens in order, or of one new token attending over 32768 keys in pages
+    of 64 in shuffled order.  Seeded, on the device; inputs larger than L2."""
+    pm, page = S.LLAMA_PREMIX, 64
+    H, d, n = pm.HP, pm.d, 32768 if name == "kv4_decode" else pm.N
+    gen = torch.Generator(device=device)
+    gen.manual_seed(11)
+    e = lambda *s: torch.randn(s, generator=gen, device=device).to(torch.bfloat16)
+    k, v = e(1, n, H, d), e(1, n, H, d)
+    pages = torch.randperm(n // page, generator=gen, device=device).to(torch.int32)
+    if name != "kv4_decode":
+        pages = pages.sort().values
+    slots = (pages[:, None] * page + torch.arange(page, device=device)).to(torch.int32).view(1, n)
+    cache = torch.empty((n // page, T.kv4_page_bytes(page, H, d)), dtype=torch.uint8, device=device)
+    store = lambda: T.kv4_store(k, v, slots, cache, page)
+    row4 = 2 * (d // 2 + d // 32 * 2)
+    moved = n * H * (4 * d + row4) + 4 * n
+    if name == "kv4_store":
+        return store, moved, 0
+    store()
+    if name == "kv4_load":
+        out = (torch.empty_like(k), torch.empty_like(v))
+        return lambda: T.kv4_load(cache, slots, H, d, page, out=out), moved, 0
+    q = e(1, 1, H, d)
+    lens = torch.tensor([n], dtype=torch.int32, device=device)
+    o, lse = torch.empty_like(q), torch.empty((1, H, 1), device=device)
+    ws = torch.zeros(T.mha_fwd_kv4_workspace_bytes(1, 1, H, H, d), dtype=torch.uint8,
+                     device=device)
+    return (lambda: T.mha_fwd_kv4(q, cache, pages[None], lens, H, page, out=o, lse=lse,
+                                  workspace=ws), n * H * row4 + 4 * H * d, 4 * d * n * H)
 
 
 def extra_ops(T, torch, dev, step, device, iters: int, hbm: float, tc: float):
@@ -796,6 +831,8 @@ def single_op(T, torch, name, dev, device):
                                             mu.mu_h, mu.mu_w)
     if kind == "mu_attention_qpool":
         return qpool_case(T, torch, device)[0]
+    if kind.startswith("kv4_"):
+        return kv4_case(T, torch, device, kind)[0]
     if kind.startswith("mu_"):
         g, ou = e((mu.B, mu.n_keep, mu.unit_tokens, mu.C)), e((mu.B, mu.n_keep, mu.unit_tokens, mu.C))
         dec = torch.zeros((mu.B, mu.grid_h * mu.grid_w, mu.C), dtype=torch.bfloat16, device=device)
@@ -854,6 +891,8 @@ def single_op_arm(args):
     units = hq.B * hq.n_units * hq.heads
     table["mu_attention_qpool"] = (units * (3 * hq.T + hq.Tq) * hq.head_dim * 2,
                                    4 * hq.head_dim * hq.Tq * hq.T * units)
+    if args.only.startswith("kv4_"):
+        table[args.only] = kv4_case(T, torch, device, args.only)[1:]
     nbytes, flops = table[args.only]
     ms = e0.elapsed_time(e1) / args.steps
     out = {"op": args.only, "ms": round(ms, 5), "GB/s": round(nbytes / ms / 1e6, 1),
@@ -879,7 +918,8 @@ def make_parser() -> argparse.ArgumentParser:
                     help="oracle samples behind the cpu_baseline of the GPU arm")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--only", choices=sorted(OP_INPUTS),
-                    help="time one op of the step alone on one GPU (profiling case)")
+                    help="time one op of the step, or a serving op, alone on one GPU "
+                         "(profiling case)")
     return ap
 
 
