@@ -357,7 +357,8 @@ iha_status kv4_load(const void* cache, const int32_t* slots, void* k, void* v, i
  * A row without visible keys (an empty sequence, i < 0) gives o = 0 and
  * lse = -inf.  What hidden keys hold, NaN too, has no influence.
  *   q, o         bf16 [B, Nq, Hq, d] views, element strides sq, so (b_outer,
- *                seq, head; b_inner unused), >= 0, multiples of 8
+ *                seq, head; b_inner unused), >= 0, multiples of 8; those of o
+ *                not 0
  *   cache        as kv4_store; block_table int32 [B, table_width] dense, only
  *                entries of pages with visible keys are read; seq_lens int32
  *                [B].  A page id outside the cache counts as hidden keys, a
@@ -370,8 +371,9 @@ iha_status kv4_load(const void* cache, const int32_t* slots, void* k, void* v, i
  *                next, of any shape that fits it.  Calls that may run at the
  *                same time (other streams, graphs replayed together) need a
  *                workspace each.
- *   scale <= 0 selects 1/sqrt(d)
- * Hq a multiple of Hkv, d in {32, 64, 96, 128}, bf16.  No length is read on
+ *   scale <= 0 selects 1/sqrt(d); at most 1e30
+ * Hq a multiple of Hkv (at most 2048 times), Nq * Hq / Hkv <= 2^20, d in {32,
+ * 64, 96, 128}, bf16.  No length is read on
  * the host, so a captured call replays with new seq_lens and block_table.  The
  * result does not depend on timing (no atomics on values).
  */

@@ -152,7 +152,14 @@ def test_attention_refusals(L):
     assert call(o=_p(1)) == 1 and call(o=_p(2)) == 1 and call(lse=_p(5)) == 1
     assert call(ws=_p(5)) == 1 and call(ws=_p(2)) == 1
     assert "overlap" in L.iha_last_error().decode()
+    assert call(so=_st(0, 0, 256, 64)) == 1 and call(so=_st(768, 0, 256, 0)) == 1
+    assert "stride 0" in L.iha_last_error().decode()
+    assert L.mha_fwd_kv4(*[_p(i) for i in (1, 2, 3, 4, 5)], None, _p(6), 1 << 40, 1, 1, 1, 1, 64, 4,
+                         16, 4, _st(64, 0, 64, 64), _st(64, 0, 64, 64), 2e30, 1, 0, T.BF16,
+                         None) == 1
+    assert call(Nq=1, Hq=4096 * 2, Hkv=2) == 2           # 4096 query heads a key head
     assert L.mha_fwd_kv4_workspace_bytes(2, 3, 4, 2, 64) > 0
+    assert L.mha_fwd_kv4_workspace_bytes(2, 3, 5, 2, 64) == 0
 
 
 def test_premix_at_refusals(L):

@@ -296,6 +296,15 @@ def test_several_tokens_and_shared_heads(T, Nq, Hq, Hkv, mask, window):
     run_case(T, [0, 1, 5, 16, 40, 130], Nq, Hq, Hkv, 64, 32, mask, window)
 
 
+@pytest.mark.parametrize("d", [32, 96, 128])
+@pytest.mark.parametrize("Nq,Hq,Hkv", [(2, 2, 2), (1, 3, 1), (4, 2, 2), (1, 7, 1), (3, 4, 1),
+                                       (1, 16, 1), (5, 5, 1)])
+def test_column_forms(T, d, Nq, Hq, Hkv):
+    """Each number of columns (new token x query head of a key head) that takes a
+    form of its own: 1, 2, 3-4, 5-8, 9-16, more; every d."""
+    run_case(T, [3, 75, 260], Nq, Hq, Hkv, d, 16, T.MASK_CAUSAL, 0)
+
+
 @pytest.mark.parametrize("Nq,Hq,Hkv,d", [(1, 8, 8, 128), (4, 8, 2, 128), (1, 2, 1, 64),
                                          (16, 2, 1, 96), (2, 16, 1, 32)])
 @pytest.mark.parametrize("page", [16, 48, 128])
@@ -316,6 +325,54 @@ def test_many_short_sequences(T):
 def test_scale_argument_and_large_scores(T):
     run_case(T, [100, 300], 1, 2, 2, 64, 16, T.MASK_CAUSAL, 0, scale=2.5)
     run_case(T, [100, 300], 1, 2, 2, 64, 16, T.MASK_CAUSAL, 0, scale=1e-4)
+
+
+@pytest.mark.parametrize("Hq", [1, 2, 4, 8, 16])
+@pytest.mark.parametrize("kind", ["v_huge_hidden_by_softmax", "v_groups", "v_zero", "v_top",
+                                  "q_large", "q_small", "mixed_tokens"])
+def test_extreme_ranges(T, kind, Hq):
+    """Scales far apart within a head: what a token that gets no weight holds, or
+    another group, must not cost the others their digits."""
+    import torch
+    n, d, page = 150, 128, 16
+    k = S.normal((n, 1, d), 180, 0, dtype="f32")
+    v = S.normal((n, 1, d), 180, 1, dtype="f32")
+    q = S.normal((1, Hq, d), 180, 2, dtype="f32")
+    if kind == "v_huge_hidden_by_softmax":
+        k[5] = -40.0 * q[0, 0] / np.abs(q[0, 0]).max()   # gets p ~ 0 from query 0
+        q[0, 1:] = q[0, :1] * np.float32(1.25)
+        v[5] *= np.float32(1e30)
+        k[5] *= np.float32(8.0)                          # p underflows to 0 exactly
+    elif kind == "v_groups":
+        v *= np.repeat(np.float32([1e-20, 1.0, 1e20, 1e-3]), 32)
+    elif kind == "v_zero":
+        v[:, :, 32:64] = 0.0
+        v[:100, :, 64:96] = 0.0
+    elif kind == "v_top":
+        v *= np.float32(8e36)                            # just below the largest bf16 scale
+    elif kind == "q_large":
+        q *= np.float32(1e20)
+        k *= np.float32(1e-20)
+    elif kind == "q_small":
+        q *= np.float32(1e-30)
+        k *= np.float32(1e30)
+    else:
+        v *= np.float32(10.0) ** S.rng(3).integers(-12, 12, (n, 1, 1)).astype(np.float32)
+        k *= np.float32(0.2)
+    kb, vb, qb = (S.f32_to_bf16_bits(x) for x in (k, v, q))
+    cache = cache_of(T, 10, page, 1, d)
+    T.kv4_store(to_dev(kb[None]), to_dev(vb[None]), to_dev(np.arange(n, dtype=np.int32)[None]),
+                cache, page)
+    table = torch.arange(10, dtype=torch.int32, device="cuda")[None]
+    o, lse = T.mha_fwd_kv4(to_dev(qb[None]), cache, table,
+                           torch.tensor([n], dtype=torch.int32, device="cuda"), 1, page,
+                           return_lse=True)
+    kv, vv = O.kv4_values(kb), O.kv4_values(vb)
+    if kind != "v_huge_hidden_by_softmax":
+        check_rows(T, o[0], lse[0], qb, kv, vv, T.MASK_CAUSAL, 0)
+        return
+    keep = np.r_[0:5, 6:n]                               # token 5 has weight 0
+    check_rows(T, o[0], lse[0], qb, kv[keep], vv[keep], T.MASK_NONE, 0)
 
 
 def test_strided_query_and_output(T):

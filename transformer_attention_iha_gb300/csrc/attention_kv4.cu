@@ -24,8 +24,8 @@
 //     more columns: P s in bf16 (2^-8 a term, as P has in the bf16 attention),
 //       the codes as bf16 (128 + n) - 136, exact.
 //     P^T turns from accumulator to B operand by movmatrix.
-//   Softmax in the log2 domain, fp32; a column's reference maximum moves only
-//   when a score exceeds it by more than 8, then O and the sum are rescaled.
+//   Softmax in the log2 domain, fp32; a column's reference moves only when a
+//   score exceeds it, to 8 above that score; then O and the sum are rescaled.
 // Codes are never expanded in memory: 36 NG bytes per token and head are read
 // once, by bulk copies of whole blocks into a ring that each warp owns, and unpacked in the registers of the lanes that use them.
 //
@@ -296,6 +296,27 @@ struct Joined {
     o.z = fmaf(o.z, a, po.z * c);
     o.w = fmaf(o.w, a, po.w * c);
   }
+  // U parts at once: one rescale for all of them.
+  template <int U>
+  __device__ __forceinline__ void add(const float (&pm)[U], const float (&pl)[U],
+                                      const float4 (&po)[U]) {
+    float n = m;
+#pragma unroll
+    for (int k = 0; k < U; ++k) n = fmaxf(n, pm[k]);
+    const float ref = n == -INFINITY ? 0.f : n, a = exp2f(m - ref);
+    m = n;
+    l *= a;
+    o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const float c = exp2f(pm[k] - ref);
+      l = fmaf(pl[k], c, l);
+      o.x = fmaf(po[k].x, c, o.x);
+      o.y = fmaf(po[k].y, c, o.y);
+      o.z = fmaf(po[k].z, c, o.z);
+      o.w = fmaf(po[k].w, c, o.w);
+    }
+  }
   __device__ __forceinline__ void write(const Kv4AttnParams& p, const int* span, int col,
                                         int f) const {
     write_out(p, span[0], span[1], col, f, o, m == -INFINITY ? 0.f : m, l);
@@ -337,8 +358,7 @@ __device__ __forceinline__ void join_ctas(const Kv4AttnParams& p, const int* spa
             po[k] = __ldcg(reinterpret_cast<const float4*>(pp + cc * D + f));
           }
         }
-#pragma unroll
-        for (int k = 0; k < U; ++k) a.add(pm[k], pl[k], po[k]);
+        a.add(pm, pl, po);
       }
     }
     if (groups > 1) {
@@ -482,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
           const int qi = token_of(p, col), qh = n.hk * p.G + col - qi * p.G;
           const __nv_bfloat16* qp =
               p.q + n.b * p.sq.b_outer + qi * p.sq.seq + qh * p.sq.head + 64 * t;
-          asm volatile("prefetch.global.L1 [%0];" ::"l"(qp));
+          asm volatile("prefetch.L1 [%0];" ::"l"(qp));
         }
       }
     };
@@ -638,8 +658,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
           if (u.at + u.n + kUnitCost < stretch && next_unit<COLS>(p, n)) prefetch_q(n);
         }
 
-        // running maximum m of a column: mlim = m + 8, mref = m, or 0 while no key
-        // has been seen (m = -inf)
+        // a column's reference: 8 above the maximum when it was last set, so that
+        // p = 2^(x - mref) stays below 1 (p times a scale then cannot overflow);
+        // mlim is the same, or -inf while no key has been seen (mref = 0)
         float mlim[NT][2], mref[NT][2], l[NT][2];
         float off[SH][4];        // FEW: -8 2^-24 sum P since the last flush
         float F[SH][2], F_lim[SH][2];  // FEW: see below; lanes without a group never ask
@@ -772,10 +793,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
                   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                  if (mlim[nt][e] != -INFINITY) v = fmaxf(v, mref[nt][e]);
+                  // a column below its limit keeps its reference
+                  v = v > mlim[nt][e] ? v + 8.f : mlim[nt][e];
                   const float ref = v == -INFINITY ? 0.f : v;
                   const float f = mlim[nt][e] == -INFINITY ? 0.f : exp2f(mref[nt][e] - ref);
-                  mlim[nt][e] = v + 8.f;
+                  mlim[nt][e] = v;
                   mref[nt][e] = ref;
                   l[nt][e] *= f;
                   if constexpr (FEW) {
@@ -949,7 +971,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
           } else {
             *reinterpret_cast<float4*>(part + cc * D + 32 * j + 4 * g) = o;
             if (j == 0 && g == 0) {
-              part[p.part_cols * D + cc] = lim == -INFINITY ? lim : ref;
+              part[p.part_cols * D + cc] = lim;
               part[p.part_cols * D + p.part_cols + cc] = ll;
             }
           }
@@ -968,10 +990,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
                   o[k] = __uint_as_float(sel_u32(GC * s + tg == j,
                                                  __float_as_uint(acc[0][j][k >> 1][2 * (k & 1) + e]),
                                                  __float_as_uint(o[k])));
-              // F = 0: every w was 0 (or NaN, and O is NaN)
-              const float f = F[s][e] == 0.f ? 1.f : 16777216.f / F[s][e], h = f * 0.0625f;
+              // F = 0: every w was 0 (or NaN, and O is NaN).  2^24 / F as two factors:
+              // together they can leave the range of fp32
+              const float f = F[s][e] == 0.f ? 1.f : 1.f / F[s][e];
               if (GC * s + tg < NG && tc + e < ncolv)
-                put(tc + e, GC * s + tg, make_float4(o[0] * f, o[1] * h, o[2] * f, o[3] * h),
+                put(tc + e, GC * s + tg,
+                    make_float4(o[0] * 16777216.f * f, o[1] * 1048576.f * f,
+                                o[2] * 16777216.f * f, o[3] * 1048576.f * f),
                     mlim[0][e], mref[0][e], l[0][e]);
             }
         } else {
@@ -1162,7 +1187,7 @@ iha_status mha_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
   const int nt = pick_nt(ncols);
   const int64_t ncb = (ncols + 8 * nt - 1) / (8 * nt);
   if (ncols > (1 << 20) || G > 2048 || ncb * ((int64_t)table_width * page / kKv4Tok + kUnitCost) > INT32_MAX)
-    return fail(IHA_ERR_UNSUPPORTED, "%s: too many new tokens or keys for one launch", name);
+    return fail(IHA_ERR_UNSUPPORTED, "%s: more than 2^20 new rows or 2048 query heads of a key head", name);
   if (!aligned16(q) || !aligned16(o))
     return fail(IHA_ERR_ALIGNMENT, "%s: q and o must be 16-byte aligned", name);
   if ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(seq_lens) |
@@ -1174,6 +1199,8 @@ iha_status mha_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
   if (Hq == 1) sq.head = so.head = 0;
   if (sq.b_outer < 0 || sq.seq < 0 || sq.head < 0 || so.b_outer < 0 || so.seq < 0 || so.head < 0)
     return fail(IHA_ERR_INVALID_ARG, "%s: negative stride", name);
+  if ((B > 1 && so.b_outer == 0) || (Nq > 1 && so.seq == 0) || (Hq > 1 && so.head == 0))
+    return fail(IHA_ERR_INVALID_ARG, "%s: the output repeats rows (stride 0)", name);
   if ((sq.b_outer | sq.seq | sq.head | so.b_outer | so.seq | so.head) & 7)
     return fail(IHA_ERR_ALIGNMENT, "%s: strides must be multiples of 8 elements", name);
   if (reinterpret_cast<uintptr_t>(workspace) & 255)
@@ -1225,6 +1252,7 @@ iha_status mha_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
   p.mask = mask_mode;
   p.window = window;
   if (!(scale > 0.f)) scale = 1.f / sqrtf((float)d);
+  if (scale > 1e30f) return fail(IHA_ERR_INVALID_ARG, "%s: scale above 1e30", name);
   p.scale_log2 = scale * 1.4426950408889634f;
   p.sq = sq;
   p.so = so;
