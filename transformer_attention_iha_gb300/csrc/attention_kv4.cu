@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
             }
 
             const bool edge = (unsigned)(rk - rf0) >= rf_n || (unsigned)(rk + NB - 1 - rf0) >= rf_n ||
-                              gone != 0;
+                              ((gone >> k0) & ((1u << NB) - 1u)) != 0;
             uint32_t hidden = 0;  // bit 4 (nt NB + b) + e
             if (edge) {
               const int key = (u.b0 + rk) * kKv4Tok + g;
