@@ -512,6 +512,84 @@ def test_streams(T):
     np.testing.assert_array_equal(to_f64(got[0])[0], ks[0][:16])
 
 
+def test_two_calls_at_once(T):
+    """Two streams, a workspace each, calls of different shapes in flight together."""
+    import torch
+    page = 16
+    shapes = [([20000, 300], 1, 8, 8, 128), ([3000] * 9, 2, 8, 2, 64)]
+    cases = []
+    for i, (lens, Nq, Hq, Hkv, d) in enumerate(shapes):
+        cache, table, sl, ks, vs = build(T, lens, Hkv, d, page, 190 + 20 * i)
+        q = S.normal((len(lens), Nq, Hq, d), 190 + i, 9)
+        ws = torch.zeros(T.mha_fwd_kv4_workspace_bytes(len(lens), Nq, Hq, Hkv, d),
+                         dtype=torch.uint8, device="cuda")
+        qd = to_dev(q)
+        ref = T.mha_fwd_kv4(qd, cache, table, sl, Hkv, page, workspace=ws)
+        cases.append((qd, cache, table, sl, Hkv, ws, torch.cuda.Stream(), ref, q, ks, vs))
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(30):
+        for o, (qd, cache, table, sl, Hkv, ws, st, *_r) in zip(outs, cases):
+            o.append(T.mha_fwd_kv4(qd, cache, table, sl, Hkv, page, workspace=ws, stream=st))
+    torch.cuda.synchronize()
+    for o, c in zip(outs, cases):
+        assert all(torch.equal(x, c[7]) for x in o)
+        for b in range(len(c[9])):
+            check_rows(T, c[7][b], None, c[8][b], c[9][b], c[10][b], T.MASK_CAUSAL, 0)
+    assert T.device_error() == 0
+
+
+def test_captured_decode_step(T):
+    """One graph of premix, store and attention; positions, slots and lengths move
+    on between replays, and each replay equals the calls made one by one."""
+    import torch
+    B, H, P, d, page, n0, steps = 3, 4, 2, 64, 16, 30, 5
+    HP = H * P
+    i32 = dict(dtype=torch.int32, device="cuda")
+    width = 4
+    table = torch.arange(B * width, **i32).flip(0).view(B, width).contiguous()
+    x = [to_dev(S.normal((steps, B, 1, H, d), 200, t)) for t in range(3)]
+    ws = [to_dev(S.premix_weight(H, P, 201, t)) for t in range(3)]
+    k0, v0 = (to_dev(S.normal((B, n0, HP, d), 202, t)) for t in range(2))
+    j = torch.arange(width * page, device="cuda")
+    every = (table[:, j // page] * page + j % page).to(torch.int32)
+    caches = [cache_of(T, B * width, page, HP, d) for _ in range(2)]
+    for c in caches:
+        T.kv4_store(k0, v0, every[:, :n0].contiguous(), c, page)
+    scratch = [torch.zeros(T.mha_fwd_kv4_workspace_bytes(B, 1, HP, HP, d), dtype=torch.uint8,
+                           device="cuda") for _ in range(2)]
+    xin = [t[0].clone() for t in x]
+    pos, slots, lens = torch.zeros((B, 1), **i32), torch.zeros((B, 1), **i32), torch.zeros(B, **i32)
+    y = [torch.empty((B, 1, HP, d), dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    o = torch.empty_like(y[0])
+
+    def step(xs, ys, out, cache, work):
+        T.premix_fwd_qkv_at(xs, ws, P, pos, out=ys)
+        T.kv4_store(ys[1], ys[2], slots, cache, page)
+        T.mha_fwd_kv4(ys[0], cache, table, lens, HP, page, out=out, workspace=work)
+
+    def move(i):
+        pos.fill_(n0 + i)
+        slots.copy_(every[:, n0 + i:n0 + i + 1])
+        lens.fill_(n0 + i + 1)
+        for a, b in zip(xin, x):
+            a.copy_(b[i])
+
+    move(0)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(xin, y, o, caches[0], scratch[0])
+    y2, o2 = [torch.empty_like(t) for t in y], torch.empty_like(o)
+    for i in range(steps):
+        move(i)
+        g.replay()
+        step(xin, y2, o2, caches[1], scratch[1])
+        assert all(torch.equal(a, b) for a, b in zip(y, y2)) and torch.equal(o, o2)
+        assert torch.isfinite(o.float()).all()
+    assert torch.equal(caches[0], caches[1])
+    assert T.device_error() == 0
+
+
 # ------------------------------------------------------------------ premix at positions
 @pytest.mark.parametrize("B,N,H,P,d,dtype", [
     (1, 1, 20, 4, 128, "bf16"), (3, 5, 20, 4, 128, "bf16"), (7, 1, 4, 2, 64, "bf16"),

@@ -25,6 +25,12 @@
 // Load: eight threads a row, each with half of a K octet's words (whole lines
 // over the row) and one g of V.  bf16 output: codes as bf16 (128 + n) - 136,
 // exact, times s in one rounding multiply; f32: s * c, exact.
+//
+// Both are bound by HBM.  8192 tokens x 80 heads of 128, bf16, in order, 430 MB:
+// store 72 us (6.0 TB/s; the quantiser's arithmetic keeps the issue slots 69 per
+// cent busy), load 66 us (6.6 TB/s).  16384 rows read in random order: 163 us, 5.3
+// TB/s of what is asked for and 6 of what moves (a V row alone moves its
+// partner's bytes too).
 #include "kv4.cuh"
 
 namespace iha {
