@@ -100,7 +100,9 @@ struct FwdTensors {
   T* y[3];
 };
 
-template <typename T, int HC, bool ROPE>
+// ROPE: 0 none, 1 at position token % N, 2 at positions g.pos (apart from 1, whose
+// calls the choice at run time costs 1 per cent).
+template <typename T, int HC, int ROPE>
 __global__ void __launch_bounds__(256) premix_fwd_kernel(const FwdTensors<T> ts, PremixGeom g) {
   extern __shared__ float4 smem_f4[];
   float* wsm = reinterpret_cast<float*>(smem_f4);
@@ -140,7 +142,7 @@ __global__ void __launch_bounds__(256) premix_fwd_kernel(const FwdTensors<T> ts,
     }
     float cs[4], sn[4];
     if (ROPE) {
-      const int n = g.pos ? __ldg(g.pos + tok) : (int)(tok % g.N);
+      const int n = ROPE == 2 ? __ldg(g.pos + tok) : (int)(tok % g.N);
 #pragma unroll
       for (int j = 0; j < 4; ++j) rope_cs(n, inv_freq[j], cs[j], sn[j]);
     }
@@ -518,10 +520,12 @@ void launch_fwd_n(const PremixGeom& g, int ntens, const void* const* x, const fl
   }
   const dim3 grid(blocks, ntens);
   IHA_HC_SWITCH(hc, {
-    if (rope)
-      premix_fwd_kernel<T, kHC, true><<<grid, threads, smem, s>>>(ts, g);
+    if (rope && g.pos)
+      premix_fwd_kernel<T, kHC, 2><<<grid, threads, smem, s>>>(ts, g);
+    else if (rope)
+      premix_fwd_kernel<T, kHC, 1><<<grid, threads, smem, s>>>(ts, g);
     else
-      premix_fwd_kernel<T, kHC, false><<<grid, threads, smem, s>>>(ts, g);
+      premix_fwd_kernel<T, kHC, 0><<<grid, threads, smem, s>>>(ts, g);
   })
 }
 
