@@ -371,7 +371,8 @@ iha_status kv4_load(const void* cache, const int32_t* slots, void* k, void* v, i
  *                next, of any shape that fits it.  Calls that may run at the
  *                same time (other streams, graphs replayed together) need a
  *                workspace each.
- *   scale <= 0 selects 1/sqrt(d); at most 1e30
+ *   scale <= 0 selects 1/sqrt(d); at most 1e30, and |q| * scale below 2^117 (beyond
+ *   it a score's factor leaves fp32)
  * Hq a multiple of Hkv (at most 2048 times), Nq * Hq / Hkv <= 2^20, d in {32,
  * 64, 96, 128}, bf16.  No length is read on
  * the host, so a captured call replays with new seq_lens and block_table.  The
