@@ -226,33 +226,45 @@ __global__ void __launch_bounds__(kThreads, 1)
   // there).  Rows of the last tile past H*P stay unwritten: they only reach
   // accumulator rows that are never read.
   if (tid < kEpiThreads) {
-    const int rows8 = (p.HP + 7) & ~7;
-    for (int idx = tid; idx < p.ntens * rows8 * 8; idx += kEpiThreads) {
-      const int tns = idx / (rows8 * 8), r = idx - tns * rows8 * 8;
-      const int row = r >> 3, j = r & 7;
-      // weight row of output row `row`: (h, p) = (row / P, row % P), or
-      // interleaved (row % H, row / H)
-      const int wrow = p.interleave ? (row % p.H) * (p.HP / p.H) + row / p.H : row;
-      const float* w = p.w[0];
-      if (tns == 1) w = p.w[1];
-      if (tns == 2) w = p.w[2];
-      uint32_t v[4];
+    // An item is 8 source heads of a row, hi and lo; a thread reads the weights of
+    // two items at once (the staging waits for L2, not for bandwidth).
+    const int rows8 = (p.HP + 7) & ~7, items = p.ntens * rows8 * 4;
+    for (int idx0 = tid; idx0 < items; idx0 += 2 * kEpiThreads) {
+      float wv[2][8];
+      uint32_t off[2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float part[2];
+      for (int u = 0; u < 2; ++u) {
+        const int idx = idx0 + u * kEpiThreads;
+        const int tns = idx / (rows8 * 4), r = idx - tns * rows8 * 4;
+        const int row = r >> 2, j = r & 3;
+        // weight row of output row `row`: (h, p) = (row / P, row % P), or
+        // interleaved (row % H, row / H)
+        const int wrow = p.interleave ? (row % p.H) * (p.HP / p.H) + row / p.H : row;
+        const float* w = p.w[0];
+        if (tns == 1) w = p.w[1];
+        if (tns == 2) w = p.w[2];
 #pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2) {
-          const int k = 8 * j + 2 * e + h2;  // 0..63
-          const int s = k & 31;
-          const float wv = (row < p.HP && s < p.H) ? __ldg(w + wrow * p.H + s) : 0.f;
-          const float hi = __bfloat162float(__float2bfloat16_rn(wv));
-          part[h2] = (k < 32) ? hi : (wv - hi);
-        }
-        v[e] = pack_bf16x2(part[0], part[1]);
+        for (int e = 0; e < 8; ++e)
+          wv[u][e] = idx < items && row < p.HP && 8 * j + e < p.H
+                         ? __ldg(w + wrow * p.H + 8 * j + e)
+                         : 0.f;
+        off[u] = (uint32_t)tns * p.w_spacing +
+                 (uint32_t)((row >> 3) * 1024 + (row & 7) * 128 + ((j ^ (row & 7)) << 4));
       }
-      const uint32_t off = (uint32_t)tns * p.w_spacing +
-                           (uint32_t)((row >> 3) * 1024 + (row & 7) * 128 + ((j ^ (row & 7)) << 4));
-      *reinterpret_cast<uint4*>(smem + off) = make_uint4(v[0], v[1], v[2], v[3]);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (idx0 + u * kEpiThreads >= items) break;
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float a = __bfloat162float(__float2bfloat16_rn(wv[u][2 * e]));
+          const float b = __bfloat162float(__float2bfloat16_rn(wv[u][2 * e + 1]));
+          hi[e] = pack_bf16x2(a, b);
+          lo[e] = pack_bf16x2(wv[u][2 * e] - a, wv[u][2 * e + 1] - b);
+        }
+        *reinterpret_cast<uint4*>(smem + off[u]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(smem + (off[u] ^ 64u)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
     }
     fence_proxy_async_smem();
   }
