@@ -206,7 +206,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  if (tid == 0) {
+  auto load_x = [&](int k, int G) {
+    const int tns = G / p.n_stages, g = G - tns * p.n_stages, xs = k % XS;
+    mbar_arrive_expect_tx(b_xfull(xs), p.stage_bytes);
+    tma_load_4d(sX + xs * p.stage_bytes, &maps.x[tns], b_xfull(xs), 0, 0, 0, g * kTok);
+  };
+  if (tid == kEpiThreads) {  // the producer; the ring's first loads fly while W is staged
     for (int s = 0; s < XS; ++s) {
       mbar_init(b_xfull(s), 1);
       mbar_init(b_xempty(s), 1);
@@ -218,6 +223,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(b_drain, 1);
     *abort_flag = 0;
     mbar_init_fence();
+    for (int k = 0, G = blockIdx.x; k < XS && G < total_stages; ++k, G += gridDim.x) load_x(k, G);
+  }
+  if (tid == kThreads - 1) {
 #pragma unroll
     for (int i = 0; i < 64; ++i) inv_tab[i] = make_float2(p.rt.hi[i], p.rt.lo[i]);
   }
@@ -280,17 +288,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      for (int t = 0; t < p.ntens; ++t) tma_prefetch_desc(&maps.x[t]);
       int k = 0;
       for (int G = blockIdx.x; G < total_stages; G += gridDim.x, ++k) {
-        const int tns = G / p.n_stages, g = G - tns * p.n_stages;
-        const int xs = k % XS;
-        if (!mbar_wait(b_xempty(xs), ((k / XS) & 1) ^ 1, abort_flag)) {
+        if (k < XS) continue;  // on their way since the start
+        if (!mbar_wait(b_xempty(k % XS), ((k / XS) & 1) ^ 1, abort_flag)) {
           raise_error(abort_flag);
           break;
         }
-        mbar_arrive_expect_tx(b_xfull(xs), p.stage_bytes);
-        tma_load_4d(sX + xs * p.stage_bytes, &maps.x[tns], b_xfull(xs), 0, 0, 0, g * kTok);
+        load_x(k, G);
       }
       // Whoever aborted, no copy may still be landing when the CTA exits
       // (in a normal run the last loads have completed and this returns at once).
