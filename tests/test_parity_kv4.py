@@ -610,6 +610,19 @@ def test_premix_at_positions(T, B, N, H, P, d, dtype):
             np.testing.assert_allclose(to_f64(ys[t]), r, atol=1e-5, rtol=0)
 
 
+@pytest.mark.parametrize("n,H,P,d", [(51, 20, 4, 128), (52, 20, 4, 128), (32, 32, 4, 64),
+                                     (33, 32, 4, 64), (256, 8, 2, 64), (257, 8, 2, 64)])
+def test_premix_at_where_the_kernels_change(T, n, H, P, d):
+    """The largest call of the kernel for few tokens, and the next."""
+    xs = [S.normal((n, 1, H, d), 145, t) for t in range(3)]
+    ws = [S.premix_weight(H, P, 146, t) for t in range(3)]
+    pos = S.rng(147).integers(0, 130000, (n, 1)).astype(np.int32)
+    ys = T.premix_fwd_qkv_at([to_dev(x) for x in xs], [to_dev(w) for w in ws], P, to_dev(pos))
+    for t in range(3):
+        r = O.premix_at(xs[t], ws[t], P, pos) if t < 2 else O.premix_fwd(xs[t], ws[t], P)
+        assert_bf16_close(to_f64(ys[t]), r, f"premix at {t}")
+
+
 def test_premix_at_consecutive_positions_is_the_premix(T):
     import torch
     B, N, H, P, d = 2, 37, 20, 4, 128

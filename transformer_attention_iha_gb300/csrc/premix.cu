@@ -620,7 +620,7 @@ iha_status premix_fwd_qkv(const char* name, const void* const* x, const float* c
     if (pos && overlaps(y[t], ny, pos, (size_t)g.ntok * 4))
       return fail(IHA_ERR_INVALID_ARG, "%s: an output overlaps the positions", name);
   }
-  if (pos && dt == IHA_BF16 && g.ntok <= kFewTokens && premix_few_supported((int)g.ntok, H, P, d))
+  if (pos && dt == IHA_BF16 && premix_few_supported(g.ntok, H, P, d))
     return premix_few_at(x, w, y, pos, (int)g.ntok, H, P, d, rope_base, s);
   if (dt == IHA_BF16 && premix_tc_supported(H, P, d))
     return premix_fwd_tc_multi(3, x, w, y, B, N, H, P, d, rope ? 3 : 0, rope_base, s, 0, pos);

@@ -100,10 +100,11 @@ __device__ __forceinline__ float2 rope_inv_freq(const RopeTable& rt, int i) {
 // tensor: W's 16 rows and the token's X go to shared memory (fp32), a thread
 // holds features i and i + d/2 (RoPE partners) of 8 (d = 128) or 4 rows, and
 // loops over the source heads.  Latency-bound: one load, one barrier, H steps.
-// H = 20, P = 4, d = 128: 1 token 3.8 us (7.9 on the tensor-core kernel), 16
-// tokens 4.5 (8.7), 64 tokens 6.8 (8.9), 96 tokens 8.4 (9.0), 128 tokens 10.7 (9.7):
-// kFewTokens lies where both are close.
-constexpr int kFewRows = 16, kFewThreads = 128;
+// H = 20, P = 4, d = 128: 1 token 3.8 us (5.2 on the tensor-core kernel), 16
+// tokens 4.2 (6.0), 48 tokens 5.9 (6.3), 64 tokens 6.7 (6.2); H = 32, P = 4: 32 tokens
+// 7.5 (7.9), 48 tokens 8.9 (7.8); H = 8, P = 2, d = 64: 128 tokens 3.0 (5.0).  They
+// cross at about five CTAs an SM.
+constexpr int kFewRows = 16, kFewThreads = 128, kFewCtas = 768;
 
 struct FewParams {
   const __nv_bfloat16* x[3];
@@ -347,17 +348,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = (uint32_t)(q * 32) << 16;
     const uint32_t wstage = sStage + (uint32_t)warp * kWarpStage;
     float4* tab = rope_tabs + warp * 32;
+    // AT: the position of this warp's token of stage G, read a stage ahead
+    // (the last pair of an odd token count has no second token)
+    auto pos_of = [&](int G) {
+      return G < total_stages ? __ldg(p.pos + min(G % p.n_stages * kTok + tt, p.ntok - 1)) : 0;
+    };
+    int n_next = AT ? pos_of(blockIdx.x) : 0;
     int k = 0;
     for (int G = blockIdx.x; G < total_stages; G += gridDim.x, ++k) {
       const int tns = G / p.n_stages, g = G - tns * p.n_stages;
       const bool rope = (p.rope_mask >> tns) & 1;
+      const int n_at = n_next;
+      if (AT) n_next = pos_of(G + gridDim.x);
       const int a = k & 1, sb = k & 1;
       const int t = g * kTok + tt;
       if (rope && warp_active && 2 * lane < HALF) {
         float c0, s0, c1, s1;
         const float4 inv = reinterpret_cast<const float4*>(inv_tab)[lane];  // pairs 2 lane, 2 lane + 1
-        // (the last pair of an odd token count has no second token)
-        const int n = AT ? __ldg(p.pos + min(t, p.ntok - 1)) : t % p.N;
+        const int n = AT ? n_at : t % p.N;
         rope_cos_sin(n, inv.x, inv.y, c0, s0);
         rope_cos_sin(n, inv.z, inv.w, c1, s1);
         tab[lane] = make_float4(c0, c1, s0, s1);
@@ -538,8 +546,8 @@ iha_status premix_fwd_tc_multi(int ntens, const void* const* x, const float* con
   return check_launch("premix forward");
 }
 
-bool premix_few_supported(int ntok, int H, int P, int d) {
-  return ntok <= kFewTokens && premix_tc_supported(H, P, d);
+bool premix_few_supported(int64_t ntok, int H, int P, int d) {
+  return premix_tc_supported(H, P, d) && ntok * 3 * ((H * P + kFewRows - 1) / kFewRows) <= kFewCtas;
 }
 
 iha_status premix_few_at(const void* const* x, const float* const* w, void* const* y,

@@ -51,10 +51,9 @@ iha_status premix_fwd_tc_multi(int ntens, const void* const* x, const float* con
                                float rope_base, cudaStream_t stream, int interleave = 0,
                                const int32_t* pos = nullptr);
 
-// Premix of Q, K and V of up to kFewTokens bf16 tokens (d in {64, 128}), Q and K
-// rotated at positions pos, without the tensor cores.
-constexpr int kFewTokens = 64;
-bool premix_few_supported(int ntok, int H, int P, int d);
+// Premix of Q, K and V of few bf16 tokens (d in {64, 128}), Q and K rotated at
+// positions pos, without the tensor cores.
+bool premix_few_supported(int64_t ntok, int H, int P, int d);
 iha_status premix_few_at(const void* const* x, const float* const* w, void* const* y,
                          const int32_t* pos, int ntok, int H, int P, int d, float rope_base,
                          cudaStream_t stream);
