@@ -18,14 +18,19 @@
 //       columns of the operand hold the 2 columns four times, once per group,
 //       each with its group's scale, so P is scaled, rounded and turned once
 //       instead of four times; up to 4 columns, twice, for two groups.  P s F in
-//       fp16 (2^-11 a term) with a power of two F per column and group that keeps
-//       it in range, codes as for K; -8 sum P comes from one more MMA with a
-//       constant A operand (the same rounded P) and leaves O every kFlush blocks.
+//       fp16 with a power of two F per column and group that keeps the largest of
+//       the sum so far between 2^5 and 2^15: F falls when a p s outgrows that, and
+//       rises with the softmax reference, so it follows what is left of a token
+//       that later ones overtake.  A term is off by 2^-11 of itself or, if it is
+//       below 2^-19 of the largest, 2^-30 of that.  Codes as for K; -8 sum P comes
+//       from one more MMA with a constant A operand (the same rounded P) and leaves
+//       O every kFlush blocks.
 //     more columns: P s in bf16 (2^-8 a term, as P has in the bf16 attention),
 //       the codes as bf16 (128 + n) - 136, exact.
 //     P^T turns from accumulator to B operand by movmatrix.
 //   Softmax in the log2 domain, fp32; a column's reference moves only when a
-//   score exceeds it, to 8 above that score; then O and the sum are rescaled.
+//   score exceeds it, to the next integer 8 above that score (so by a whole power
+//   of two, which F can take up exactly); then O and the sum are rescaled.
 // Codes are never expanded in memory: 36 NG bytes per token and head are read
 // once, by bulk copies of whole blocks into a ring that each warp owns, and
 // unpacked in the registers of the lanes that use them.
@@ -70,6 +75,9 @@ __host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; 
 // FEW: the codes' offset leaves O after this many blocks (256 tokens): it costs
 // 32 FMAs, and O has grown by 8 s per unit of probability until then.
 constexpr int kFlush = 16;
+// FEW: the largest F, 2^126 (its reciprocal is a normal number), and its exponent field.
+constexpr float kTopF = 8.5070591730234616e37f;
+constexpr int kTopFExp = 126 + 127;
 // Positions a unit takes besides its blocks: its Q, output and ramp.  Measured on
 // a ragged batch (16 sequences of 1 to 8192 keys, 8 key heads): 2 31 us, 4 23.6,
 // 6 23.1; on 131071 keys x 80 heads they differ by 1 per cent.
@@ -670,17 +678,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
           if (u.at + u.n + kUnitCost < stretch && next_unit<COLS>(p, n)) prefetch_q(n);
         }
 
-        // a column's reference: 8 above the maximum when it was last set, so that
-        // p = 2^(x - mref) stays below 1 (p times a scale then cannot overflow);
+        // a column's reference: 8 above the maximum (rounded up) when it was last set, so
+        // that p = 2^(x - mref) stays below 1 (p times a scale then cannot overflow);
         // mlim is the same, or -inf while no key has been seen (mref = 0)
         float mlim[NT][2], mref[NT][2], l[NT][2];
         float off[SH][4];        // FEW: -8 2^-24 sum P since the last flush
-        float F[SH][2], F_lim[SH][2];  // FEW: see below; lanes without a group never ask
+        float F[SH][2];          // FEW: the power of two of a column and group, see below
 #pragma unroll
         for (int s = 0; s < SH; ++s) {
           off[s][0] = off[s][1] = off[s][2] = off[s][3] = 0.f;
-          F[s][0] = F[s][1] = 0.f;
-          F_lim[s][0] = F_lim[s][1] = GC * s + tg < NG ? -1.f : INFINITY;
+          F[s][0] = F[s][1] = kTopF;
         }
         float acc[NT][NG][2][4];
 #pragma unroll
@@ -806,23 +813,34 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
                   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
                   // a column below its limit keeps its reference
-                  v = v > mlim[nt][e] ? v + 8.f : mlim[nt][e];
+                  v = v > mlim[nt][e] ? ceilf(v) + 8.f : mlim[nt][e];
                   const float ref = v == -INFINITY ? 0.f : v;
-                  const float f = mlim[nt][e] == -INFINITY ? 0.f : exp2f(mref[nt][e] - ref);
+                  // the move, a whole number; 0 from the first reference (nothing to rescale)
+                  const float up = mlim[nt][e] == -INFINITY ? 0.f : ref - mref[nt][e];
+                  const float f = exp2f(-up);
                   mlim[nt][e] = v;
                   mref[nt][e] = ref;
                   l[nt][e] *= f;
-                  if constexpr (FEW) {
 #pragma unroll
-                    for (int s = 0; s < SH; ++s) off[s][e] *= f;
-                  }
-#pragma unroll
-                  for (int j = 0; j < NG; ++j)
-#pragma unroll
-                    for (int a = 0; a < 2; ++a) {
-                      acc[nt][j][a][e] *= f;
-                      acc[nt][j][a][e + 2] *= f;
+                  for (int s = 0; s < SH; ++s) {
+                    // FEW: F rises by 2^up, and O stays as it is, as far as F's range goes
+                    float k = f;
+                    if constexpr (FEW) {
+                      const int ef = __float_as_uint(F[s][e]) >> 23;
+                      const int to = min(ef + (int)fminf(up, 512.f), kTopFExp);
+                      F[s][e] = __uint_as_float((uint32_t)to << 23);
+                      k = exp2f((float)(to - ef) - up);
+                      off[s][e] *= k;
                     }
+#pragma unroll
+                    for (int j = FEW ? GC * s : 0; j < (FEW && GC * (s + 1) < NG ? GC * (s + 1) : NG);
+                         ++j)
+#pragma unroll
+                      for (int a = 0; a < 2; ++a) {
+                        acc[nt][j][a][e] *= k;
+                        acc[nt][j][a][e + 2] *= k;
+                      }
+                  }
                 }
               }
 #pragma unroll
@@ -835,9 +853,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
               }
             }
             if constexpr (FEW) {
-              // w = p s of this lane's group; P = w F.  F is 0 until the first
-              // w > 0 of the column and group, then a power of two that keeps
-              // the largest w F so far between 1 and 2^15.
+              // w = p s of this lane's group; P = w F.  F starts at the top of its
+              // range; when a w F exceeds 2^15, F falls to where the largest of them is
+              // 2^5 (p grows by up to 2^9 until the reference moves, and with it F).
               float w[SH][NB][4];
               bool grow = false;
               float top[SH][2];
@@ -868,7 +886,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
 #pragma unroll
                   for (int b = 1; b < NB; ++b)
                     top[s][e] = fmax3f(top[s][e], w[s][b][e], w[s][b][e + 2]);
-                  grow |= top[s][e] * F[s][e] > F_lim[s][e];
+                  grow |= top[s][e] * F[s][e] > 32768.f;
                 }
               }
               if (__any_sync(0xffffffffu, grow)) {
@@ -880,13 +898,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                    // 2^-(exponent of v), from its bits; v is 0 or positive, infinite at most
-                    const int ex = max((int)(__float_as_uint(v) >> 23), 1);
-                    const float to = __uint_as_float((uint32_t)max(254 - ex, 1) << 23);
-                    if (v > 0.f && (F[s][e] == 0.f || to < F[s][e])) {
-                      const float f = F[s][e] == 0.f ? 0.f : to / F[s][e];
+                    // 2^(5 - exponent of v), from its bits; v is 0 or positive, infinite at most
+                    const int ex = __float_as_uint(v) >> 23;
+                    const float to = __uint_as_float((uint32_t)min(259 - ex, kTopFExp) << 23);
+                    if (to < F[s][e]) {
+                      const float f = to / F[s][e];
                       F[s][e] = to;
-                      F_lim[s][e] = 32768.f;
                       off[s][e] *= f;
 #pragma unroll
                       for (int j = GC * s; j < (GC * (s + 1) < NG ? GC * (s + 1) : NG); ++j)
@@ -1002,9 +1019,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
                   o[k] = __uint_as_float(sel_u32(GC * s + tg == j,
                                                  __float_as_uint(acc[0][j][k >> 1][2 * (k & 1) + e]),
                                                  __float_as_uint(o[k])));
-              // F = 0: every w was 0 (or NaN, and O is NaN).  2^24 / F as two factors:
-              // together they can leave the range of fp32
-              const float f = F[s][e] == 0.f ? 1.f : 1.f / F[s][e];
+              // 2^24 / F as two factors: together they can leave the range of fp32
+              const float f = 1.f / F[s][e];
               if (GC * s + tg < NG && tc + e < ncolv)
                 put(tc + e, GC * s + tg,
                     make_float4(o[0] * 16777216.f * f, o[1] * 1048576.f * f,
