@@ -433,14 +433,16 @@ iha_status mu_attention_fused(const void* x, const int32_t* keep, void* canvas, 
 
 /*
  * Test hook for the failure path; never needed in normal use.  Arms the next
- * bf16 mha_fwd launch made on the calling host thread (one shot) so that
- * CTA 0 withholds the load of its first V tile and every wait of that launch
+ * bf16 mha_fwd or mha_fwd_kv4 launch made on the calling host thread (one shot)
+ * so that CTA 0 withholds the load of its first V tile (mha_fwd_kv4: the
+ * completion of its first blocks' copy) and every wait of that launch
  * gives up after limit_us microseconds (1 .. 1e6) instead of the normal 4 s.
  * The launch then takes its abort path: the waiting role raises the block's
- * abort flag, the others unwind, TMA copies in flight land, the MMAs drain,
+ * abort flag, the others unwind, copies in flight land, the MMAs drain,
  * tensor memory is released, and the kernel returns with device error 2
- * (iha_device_error); the rows of CTA 0's work are left unwritten.  The GPU
- * context stays usable and the next launch runs normally.
+ * (iha_device_error); rows that CTA 0 had a part in are left unwritten.  The GPU
+ * context stays usable and the next launch runs normally (mha_fwd_kv4: once its
+ * workspace is zeroed again).
  * IHA_ERR_INVALID_ARG for a limit out of range.
  */
 iha_status iha_test_fail_next_wait(int limit_us);

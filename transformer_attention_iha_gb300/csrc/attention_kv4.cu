@@ -108,6 +108,7 @@ struct Kv4AttnParams {
   float scale_log2;
   iha_strides sq, so;
   uint64_t wait_ns;
+  int withhold;  // failure-path test: the first stage of CTA 0's warps never completes
 };
 
 // d = a b + c on fp16 or bf16 operands, fp32 accumulators.
@@ -431,7 +432,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
 
   // ---- this warp's stretch of the line
   if (lane == 0)
-    for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&sm.full[warp][i]), 1);
+    for (int i = 0; i < kStages; ++i)
+      mbar_init(smem_u32(&sm.full[warp][i]),
+                p.withhold && blockIdx.x == 0 && i == 0 ? 2 : 1);
   if (tid <= kWarps) sm.span[tid][5] = 0;
   if (tid == 0) sm.abort = 0;
   mbar_init_fence();
@@ -1268,7 +1271,6 @@ iha_status mha_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
   p.ncols = (int)ncols;
   p.ncb = (int)ncb;
   p.inv_g = ((1ull << 32) + G - 1) / G;
-  p.wait_ns = kWaitLimitNs;
   p.counters = static_cast<unsigned*>(workspace);
   p.parts = reinterpret_cast<float*>(p.counters + kMaxCtas);
   p.part_cols = part_cols(ncols);
@@ -1294,6 +1296,8 @@ iha_status mha_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
   if (grid > cap) grid = cap;
   if (most / (grid * kWarps) > (1 << 29))
     return fail(IHA_ERR_UNSUPPORTED, "%s: too many new tokens or keys for one launch", name);
+  p.wait_ns = wait_limit_for_next_launch();
+  p.withhold = withhold_for_this_launch() ? 1 : 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   switch (d / kKv4Group) {
     case 1: return launch<1>(p, nt, (int)grid, s);
