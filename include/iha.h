@@ -336,7 +336,8 @@ iha_status kv4_store(const void* k, const void* v, const int32_t* slots, void* c
  * Read rows back: (k, v)[b, n, :, :] <- cache[slots[b, n]], s * c exactly in
  * f32 or rounded to bf16 (nearest even).  Slot -1, and a slot outside the
  * cache (also flagged), gives a row of zeros.  A slot may occur any number of
- * times.  Arguments as kv4_store; the strides of k and v must not repeat rows.
+ * times.  Arguments as kv4_store; no row of k or v may lie on another row of
+ * either (one row between others is fine: slices of one tensor).
  */
 iha_status kv4_load(const void* cache, const int32_t* slots, void* k, void* v, int B_outer,
                     int B_inner, int N, int n_pages, int page, int Hkv, int d, iha_strides sk,
@@ -357,8 +358,8 @@ iha_status kv4_load(const void* cache, const int32_t* slots, void* k, void* v, i
  * A row without visible keys (an empty sequence, i < 0) gives o = 0 and
  * lse = -inf.  What hidden keys hold, NaN too, has no influence.
  *   q, o         bf16 [B, Nq, Hq, d] views, element strides sq, so (b_outer,
- *                seq, head; b_inner unused), >= 0, multiples of 8; those of o
- *                not 0
+ *                seq, head; b_inner unused), >= 0, multiples of 8; no row of o
+ *                may lie on another
  *   cache        as kv4_store; block_table int32 [B, table_width] dense, only
  *                entries of pages with visible keys are read; seq_lens int32
  *                [B].  A page id outside the cache counts as hidden keys, a

@@ -1232,6 +1232,9 @@ iha_status mha_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
     return fail(IHA_ERR_INVALID_ARG, "%s: negative stride", name);
   if ((B > 1 && so.b_outer == 0) || (Nq > 1 && so.seq == 0) || (Hq > 1 && so.head == 0))
     return fail(IHA_ERR_INVALID_ARG, "%s: the output repeats rows (stride 0)", name);
+  const Kv4View wo = {3, {B, Nq, Hq}, {so.b_outer, so.seq, so.head}};
+  if (kv4_views_meet(wo, wo, 0, d, true))
+    return fail(IHA_ERR_INVALID_ARG, "%s: rows of the output overlap one another", name);
   if ((sq.b_outer | sq.seq | sq.head | so.b_outer | so.seq | so.head) & 7)
     return fail(IHA_ERR_ALIGNMENT, "%s: strides must be multiples of 8 elements", name);
   if (reinterpret_cast<uintptr_t>(workspace) & 255)

@@ -70,6 +70,16 @@ __device__ __forceinline__ int64_t kv4_block_of(int page_id, int blk_in_page, in
 }
 #endif
 
+// Two strided views of rows of d elements (extents n, strides s in elements, none
+// negative; view b starts `delta` elements after view a): does a row of one lie on
+// a row of the other?  With self, delta is 0 and a row does not meet itself.  Exact,
+// except that layouts that take more than 2^20 steps to tell apart count as meeting.
+struct Kv4View {
+  int dims;
+  int64_t n[4], s[4];
+};
+bool kv4_views_meet(const Kv4View& a, const Kv4View& b, int64_t delta, int d, bool self);
+
 // Host checks shared by the cache's entry points.
 iha_status kv4_check_cache(const char* name, const void* cache, int n_pages, int page, int Hkv,
                            int d);

@@ -300,6 +300,28 @@ int64_t view_bytes(const iha_strides& s, int Bo, int Bi, int N, int H, int d, in
          es;
 }
 
+// Coefficients lo .. hi of a stride; the least and the most that this one and the
+// smaller ones reach.
+struct Step {
+  int64_t s, lo, hi, least, most;
+};
+
+// Is there a choice of coefficients with |at + sum c s| < d?  Steps in falling order
+// of their strides, so each level has few coefficients that the rest can still undo.
+bool reaches(const Step* t, int n, int64_t at, int d, int& budget) {
+  if (--budget < 0) return true;
+  if (n == 0) return at < d && at > -d;
+  const int64_t least = n > 1 ? t[1].least : 0, most = n > 1 ? t[1].most : 0;
+  // at + c s + [least, most] has to meet (-d, d)
+  const int64_t a = 1 - d - most - at, b = d - 1 - least - at;
+  int64_t c0 = a / t->s + (a > 0 && a % t->s != 0), c1 = b / t->s - (b < 0 && b % t->s != 0);
+  if (c0 < t->lo) c0 = t->lo;
+  if (c1 > t->hi) c1 = t->hi;
+  for (int64_t c = c0; c <= c1; ++c)
+    if (reaches(t + 1, n - 1, at + c * t->s, d, budget)) return true;
+  return false;
+}
+
 bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
@@ -369,12 +391,19 @@ iha_status move(const char* name, bool store, const void* k, const void* v, cons
       overlaps(cache, bc, slots, toks * 4))
     return fail(IHA_ERR_INVALID_ARG, "%s: the cache overlaps another buffer", name);
   if (!store) {
-    if (k == v || overlaps(k, bk, slots, toks * 4) || overlaps(v, bv, slots, toks * 4))
+    if (overlaps(k, bk, slots, toks * 4) || overlaps(v, bv, slots, toks * 4))
       return fail(IHA_ERR_INVALID_ARG, "%s: an output overlaps another tensor", name);
     for (const iha_strides* t : {&sk, &sv})
       if ((B_outer > 1 && t->b_outer == 0) || (B_inner > 1 && t->b_inner == 0) ||
           (N > 1 && t->seq == 0) || (Hkv > 1 && t->head == 0))
         return fail(IHA_ERR_INVALID_ARG, "%s: an output repeats rows (stride 0)", name);
+    const Kv4View wk = {4, {B_outer, B_inner, N, Hkv}, {sk.b_outer, sk.b_inner, sk.seq, sk.head}};
+    const Kv4View wv = {4, {B_outer, B_inner, N, Hkv}, {sv.b_outer, sv.b_inner, sv.seq, sv.head}};
+    if (kv4_views_meet(wk, wk, 0, d, true) || kv4_views_meet(wv, wv, 0, d, true))
+      return fail(IHA_ERR_INVALID_ARG, "%s: rows of an output overlap one another", name);
+    const int64_t apart = static_cast<const char*>(v) - static_cast<const char*>(k);
+    if (overlaps(k, bk, v, bv) && kv4_views_meet(wk, wv, apart / es, d, false))
+      return fail(IHA_ERR_INVALID_ARG, "%s: the outputs overlap one another", name);
   }
   const int ng = d / kKv4Group;
   const int heads_of_warp = ng == 3 ? 1 : 4 / ng;
@@ -414,6 +443,62 @@ iha_status move(const char* name, bool store, const void* k, const void* v, cons
 }
 
 }  // namespace
+
+bool kv4_views_meet(const Kv4View& a, const Kv4View& b, int64_t delta, int d, bool self) {
+  Step t[8];
+  int n = 0;
+  auto add = [&](int64_t s, int64_t lo, int64_t hi) {  // kept in falling order of s
+    int i = 0;
+    while (i < n && t[i].s > s) ++i;
+    if (i < n && t[i].s == s) {
+      t[i].lo += lo;
+      t[i].hi += hi;
+      return;
+    }
+    for (int k = n++; k > i; --k) t[k] = t[k - 1];
+    t[i].s = s;
+    t[i].lo = lo;
+    t[i].hi = hi;
+  };
+  auto sums = [&](int last) {
+    int64_t least = 0, most = 0;
+    for (int i = n - 1; i >= last; --i) {
+      t[i].least = least += t[i].lo * t[i].s;
+      t[i].most = most += t[i].hi * t[i].s;
+    }
+  };
+  int budget = 1 << 20;
+  if (self) {
+    bool zero = false;
+    for (int i = 0; i < a.dims; ++i)
+      if (a.n[i] > 1) {
+        if (a.s[i] == 0) zero = true;
+        for (int k = 0; k < n; ++k)
+          if (t[k].s == a.s[i]) zero = true;  // rows (1, 0) and (0, 1) are one
+        add(a.s[i], -(a.n[i] - 1), a.n[i] - 1);
+      }
+    if (zero) return true;
+    bool nested = true;  // each stride steps over all that the smaller ones reach
+    int64_t reach = d;
+    for (int i = n - 1; i >= 0; --i) {
+      nested = nested && t[i].s >= reach;
+      reach += t[i].hi * t[i].s;
+    }
+    if (nested) return false;
+    for (int i = 0; i < n; ++i) {  // two rows that differ in t[i] and smaller strides only
+      t[i].lo = 1;
+      sums(i);
+      if (reaches(t + i, n - i, 0, d, budget)) return true;
+    }
+    return false;
+  }
+  for (int i = 0; i < a.dims; ++i)
+    if (a.n[i] > 1 && a.s[i] > 0) add(a.s[i], -(a.n[i] - 1), 0);
+  for (int i = 0; i < b.dims; ++i)
+    if (b.n[i] > 1 && b.s[i] > 0) add(b.s[i], 0, b.n[i] - 1);
+  sums(0);
+  return reaches(t, n, delta, d, budget);
+}
 
 iha_status kv4_check_cache(const char* name, const void* cache, int n_pages, int page, int Hkv,
                            int d) {
