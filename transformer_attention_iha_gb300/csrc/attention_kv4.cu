@@ -1297,7 +1297,8 @@ iha_status mha_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
   const int64_t useful = (most + kMinShare * kWarps - 1) / (kMinShare * kWarps);
   if (grid > useful) grid = useful;
   if (grid > cap) grid = cap;
-  if (most / (grid * kWarps) > (1 << 29))
+  // the kernel counts positions of a CTA (kWarps shares and a unit) in 32 bits
+  if (most / (grid * kWarps) > (1 << 28))
     return fail(IHA_ERR_UNSUPPORTED, "%s: too many new tokens or keys for one launch", name);
   p.wait_ns = wait_limit_for_next_launch();
   p.withhold = withhold_for_this_launch() ? 1 : 0;
