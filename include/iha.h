@@ -374,8 +374,8 @@ iha_status kv4_load(const void* cache, const int32_t* slots, void* k, void* v, i
  *                workspace each.
  *   scale <= 0 selects 1/sqrt(d); at most 1e30, and |q| * scale below 2^117 (beyond
  *   it a score's factor leaves fp32)
- * Hq a multiple of Hkv (at most 2048 times), Nq * Hq / Hkv <= 2^20, d in {32,
- * 64, 96, 128}, bf16.  No length is read on
+ * Hq a multiple of Hkv (at most 2048 times), Nq * Hq / Hkv <= 2^20, B and
+ * table_width * page <= 2^30, d in {32, 64, 96, 128}, bf16.  No length is read on
  * the host, so a captured call replays with new seq_lens and block_table.  The
  * result does not depend on timing (no atomics on values).
  */

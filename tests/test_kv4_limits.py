@@ -35,3 +35,10 @@ def test_positions_of_a_cta_fit_32_bits(L):
     assert attend(L, 32, 1 << 30) == 4
     assert attend(L, 95, 1 << 30) == 2
     assert "one launch" in L.iha_last_error().decode()
+
+
+def test_more_sequences_than_the_scan_can_count(L):
+    """Its index moves in steps of 128 and would pass 2^31 - 1 (refused everywhere)."""
+    for B in ((1 << 30) + 1, (1 << 31) - 1):
+        assert attend(L, B, 16) == 2
+        assert "sequences" in L.iha_last_error().decode()

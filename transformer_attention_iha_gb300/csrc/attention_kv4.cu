@@ -1211,6 +1211,8 @@ iha_status mha_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
   if (dt != IHA_BF16) return fail(IHA_ERR_UNSUPPORTED, "%s: q and o must be bf16", name);
   if (Hq % Hkv)
     return fail(IHA_ERR_INVALID_ARG, "%s: Hq %d is not a multiple of Hkv %d", name, Hq, Hkv);
+  if (B > (1 << 30))  // the scan of the lengths counts sequences in steps of a CTA
+    return fail(IHA_ERR_UNSUPPORTED, "%s: more than 2^30 sequences", name);
   if ((int64_t)table_width * page > (1 << 30))
     return fail(IHA_ERR_UNSUPPORTED, "%s: block table longer than 2^30 tokens", name);
   const int G = Hq / Hkv;
