@@ -115,10 +115,11 @@ iha_status iha_premix_fwd_qkv(const void* xq, const void* xk, const void* xv,
  * positions[b * N + n] instead of n.
  *   positions  int32 [B, N] (device), any order; |position| < 2^24 (beyond it
  *              the angles of the bf16 kernel lose accuracy)
- * All other buffers and limits as iha_premix_fwd_qkv.  Up to 64 bf16 tokens of
- * d in {64, 128} run on a latency-bound kernel with fp32 products of the fp32
+ * All other buffers and limits as iha_premix_fwd_qkv.  Few bf16 tokens of d in
+ * {64, 128}, 3 * B * N * ceil(H * P / 16) <= 768 (51 tokens of 20 -> 80 heads, 256
+ * of 8 -> 16), run on a latency-bound kernel with fp32 products of the fp32
  * weight (last bits may differ from iha_premix_fwd_qkv's); more tokens and other
- * shapes on the same kernels as iha_premix_fwd_qkv.
+ * shapes on the same kernels as iha_premix_fwd_qkv, with the same bits.
  */
 iha_status iha_premix_fwd_qkv_at(const void* xq, const void* xk, const void* xv,
                                  const float* wq, const float* wk, const float* wv,
