@@ -368,8 +368,9 @@ iha_status kv4_load(const void* cache, const int32_t* slots, void* k, void* v, i
  *                flagged (iha_device_error).
  *   lse_out      nullable; float32 [B, Hq, Nq] dense, natural log, with scale
  *   workspace    device scratch of mha_fwd_kv4_workspace_bytes() bytes, 256-byte
- *                aligned, ZERO-FILLED once before its first use (and again
- *                after device error 2); every call leaves it ready for the
+ *                aligned, its first 4096 bytes ZERO-FILLED once before its first
+ *                use (and again after device error 2; what the rest holds does
+ *                not matter); every call leaves it ready for the
  *                next, of any shape that fits it.  Calls that may run at the
  *                same time (other streams, graphs replayed together) need a
  *                workspace each.

@@ -636,7 +636,8 @@ def kv4_load(cache, slots, Hkv: int, d: int, page: int, dtype=None, out=None, st
 
 
 def mha_fwd_kv4_workspace_bytes(B: int, Nq: int, Hq: int, Hkv: int, d: int) -> int:
-    """Bytes of device scratch of mha_fwd_kv4; zero-filled once, then reusable."""
+    """Bytes of device scratch of mha_fwd_kv4; the first 4096 zero-filled once, then
+    reusable."""
     return int(lib().mha_fwd_kv4_workspace_bytes(B, Nq, Hq, Hkv, d))
 
 
@@ -649,9 +650,9 @@ def mha_fwd_kv4(q, cache, block_table, seq_lens, Hkv: int, page: int, mask: int 
     (int32 [B, table_width]).  Token t sits at position seq_lens[b] - Nq + t.
 
     Returns O shaped like q; with return_lse, also lse [B, Hq, Nq] fp32.
-    `workspace` (uint8 CUDA tensor of mha_fwd_kv4_workspace_bytes, zero-filled
-    before its first use, one for each call that may run at the same time) is
-    made here when not given."""
+    `workspace` (uint8 CUDA tensor of mha_fwd_kv4_workspace_bytes, its first 4096
+    bytes zero-filled before its first use, one for each call that may run at the
+    same time) is made here when not given."""
     torch = _torch()
     shape = q.shape
     if len(shape) != 4:
@@ -675,6 +676,8 @@ def mha_fwd_kv4(q, cache, block_table, seq_lens, Hkv: int, page: int, mask: int 
     elif return_lse:
         lse = _make((B, Hq, Nq), torch.float32, q, stream)
     if workspace is None:
+        # all of it zeroed: a fill of the first bytes alone is a slice more, which takes
+        # the host longer (a call on 777 keys 29 to 31 us, against 32 to 35)
         workspace = _make(mha_fwd_kv4_workspace_bytes(B, Nq, Hq, Hkv, d), torch.uint8, q, stream,
                           zero=True)
     else:

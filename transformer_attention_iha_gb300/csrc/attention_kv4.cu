@@ -87,6 +87,9 @@ constexpr int kUnitCost = 6;
 constexpr int kMinShare = 4;
 constexpr int kMaxCtas = 480;  // counters for 152 SMs x 3 CTAs and some
 constexpr int kCounterBytes = kMaxCtas * 4;
+// What a caller zeroes of a workspace.  Parts are written before they are read.
+constexpr int kZeroBytes = 4096;
+static_assert(kCounterBytes <= kZeroBytes, "4-bit attention: counters within the zeroed bytes");
 // Parts a CTA may leave in the workspace: of the unit it begins in and the one it
 // ends in; and of the unit each of its warps begins in, for the CTA itself.
 constexpr int kCtaParts = 2 + kWarps;
