@@ -29,8 +29,8 @@
 //       the codes as bf16 (128 + n) - 136, exact.
 //     P^T turns from accumulator to B operand by movmatrix.
 //   Softmax in the log2 domain, fp32; a column's reference moves only when a
-//   score exceeds it, to the next integer 8 above that score (so by a whole power
-//   of two, which F can take up exactly); then O and the sum are rescaled.
+//   score exceeds it, to 8 above that score (a token that weighs alone has p = 2^-8,
+//   and its P s exactly); then O and the sum are rescaled.
 // Codes are never expanded in memory: 36 NG bytes per token and head are read
 // once, by bulk copies of whole blocks into a ring that each warp owns, and
 // unpacked in the registers of the lanes that use them.
@@ -684,8 +684,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
           if (u.at + u.n + kUnitCost < stretch && next_unit<COLS>(p, n)) prefetch_q(n);
         }
 
-        // a column's reference: 8 above the maximum (rounded up) when it was last set, so
-        // that p = 2^(x - mref) stays below 1 (p times a scale then cannot overflow);
+        // a column's reference: 8 above the maximum when it was last set, so that
+        // p = 2^(x - mref) stays below 1 (p times a scale then cannot overflow);
         // mlim is the same, or -inf while no key has been seen (mref = 0)
         float mlim[NT][2], mref[NT][2], l[NT][2];
         float off[SH][4];        // FEW: -8 2^-24 sum P since the last flush
@@ -819,9 +819,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
                   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
                   // a column below its limit keeps its reference
-                  v = v > mlim[nt][e] ? ceilf(v) + 8.f : mlim[nt][e];
+                  v = v > mlim[nt][e] ? v + 8.f : mlim[nt][e];
                   const float ref = v == -INFINITY ? 0.f : v;
-                  // the move, a whole number; 0 from the first reference (nothing to rescale)
+                  // the move; 0 from the first reference (nothing to rescale)
                   const float up = mlim[nt][e] == -INFINITY ? 0.f : ref - mref[nt][e];
                   const float f = exp2f(-up);
                   mlim[nt][e] = v;
@@ -829,11 +829,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
                   l[nt][e] *= f;
 #pragma unroll
                   for (int s = 0; s < SH; ++s) {
-                    // FEW: F rises by 2^up, and O stays as it is, as far as F's range goes
+                    // FEW: F rises by the next power of two, as far as its range goes, and
+                    // O grows by what that is above the move (less than 2; each move is by
+                    // 2^8 at least, so F is at its top after 32 of them, if no p s lowers it)
                     float k = f;
                     if constexpr (FEW) {
                       const int ef = __float_as_uint(F[s][e]) >> 23;
-                      const int to = min(ef + (int)fminf(up, 512.f), kTopFExp);
+                      const int to = min(ef + (int)ceilf(fminf(up, 512.f)), kTopFExp);
                       F[s][e] = __uint_as_float((uint32_t)to << 23);
                       k = exp2f((float)(to - ef) - up);
                       off[s][e] *= k;
