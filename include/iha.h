@@ -376,6 +376,12 @@ iha_status kv4_load(const void* cache, const int32_t* slots, void* k, void* v, i
  *                workspace each.
  *   scale <= 0 selects 1/sqrt(d); at most 1e30, and |q| * scale below 2^117 (beyond
  *   it a score's factor leaves fp32)
+ * Accuracy: scores, sums and O are held in fp32.  A score is off by at most
+ * scale 2^-13 sum over groups of (largest scale of K) (sum |q|), since codes enter
+ * as c + 8; features of q below 2^-28 of its row's largest lose bits.  The products
+ * p s with V's scales are rounded: up to 4 rows a key head (Nq * Hq / Hkv) to fp16
+ * (2^-11 of a term, and the offset adds 2^-11 of sum p s), more rows to bf16 (2^-8 of
+ * a term, as mha_fwd does).  o is rounded to bf16.
  * Hq a multiple of Hkv (at most 2048 times), Nq * Hq / Hkv <= 2^20, B and
  * table_width * page <= 2^30, d in {32, 64, 96, 128}, bf16.  No length is read on
  * the host, so a captured call replays with new seq_lens and block_table.  The

@@ -45,7 +45,9 @@
 // call replays with other lengths.  A unit that lies in one warp's stretch is
 // finished by that warp; one that spans several is joined from the warps' parts
 // (m, l, O in fp32), first inside each CTA, then, if it spans CTAs, through the
-// workspace by the CTA that arrives last, always in the order of the line.
+// workspace by the CTA that arrives last.  The order of the join follows from the
+// lengths and the grid (with few columns every n-th part, then the n sums), never from
+// timing.
 //
 // What bounds it: long contexts of one column, HBM and instruction issue about
 // alike (131071 keys x 80 heads of 128, 1.51 GB: 243 us, 6.2 TB/s; the same
