@@ -50,10 +50,10 @@
 // timing.
 //
 // What bounds it: long contexts of one column, HBM and instruction issue about
-// alike (131071 keys x 80 heads of 128, 1.51 GB: 243 us, 6.2 TB/s; the same
-// kernel without its arithmetic 219 us; 243 warp instructions a block of 16
+// alike (131071 keys x 80 heads of 128, 1.51 GB: 246 us, 6.15 TB/s; the same
+// kernel without its arithmetic 219 us; 244 warp instructions a block of 16
 // tokens, 80 of them the unpacking).  More columns: issue (8 columns 50 us where
-// 1 takes 42; 32 columns 116).  Short work: latency, 11.6 us for 777 keys x 80
+// 1 takes 42; 32 columns 116).  Short work: latency, 11.6 to 12.6 us for 777 keys x 80
 // heads: lengths and stretch 1.7, page ids and first copies 1.5, Q 0.6, blocks 2,
 // joining 2 to 4.
 #include <math.h>
