@@ -25,6 +25,9 @@
  *     serving: a paged key-value cache held in 4 bits, the attention of new
  *     tokens over it and the premix of tokens that continue a sequence (no
  *     counterpart in the pages).
+ *   iha_rope_fwd / iha_rope_bwd, kv8_append / kv8_load / mha_fwd_kv8 / kv8_evict
+ *     rotary positions as operators of their own; the same kind of cache held in
+ *     8 bits, and its eviction by the attention weight that keys gather (likewise).
  *
  * Conventions shared by every entry point:
  *   - Pointers named x, y, q, ... are DEVICE pointers owned by the caller.
@@ -144,6 +147,69 @@ iha_status iha_premix_fwd_qkv_interleaved(const void* xq, const void* xk, const 
                                           void* yq, void* yk, void* yv, int B, int N, int H,
                                           int P, int d, iha_dtype dt, int rope,
                                           float rope_base, void* stream);
+
+/*
+ * Rotary positions of query and key rows, for layers whose rotation is not the
+ * premix's own: either layout of the pairs, part of a head, frequencies scaled for
+ * long contexts, any positions.  Row (b, n, h) at position t = positions[b * N + n]:
+ *   (y_a, y_b) = gain * (x_a cos - x_b sin, x_b cos + x_a sin),   angle = t * w_i,
+ * for pairs i < rot / 2 of its first rot features: (a, b) = (i, i + rot / 2), or with
+ * interleaved (2 i, 2 i + 1).  The other d - rot features are copied.
+ * w_i = base^(-2 i / rot), changed by a factor f >= 1 as `scaling` says:
+ *   IHA_ROPE_NONE    not at all
+ *   IHA_ROPE_LINEAR  w_i / f
+ *   IHA_ROPE_BASE    base * f^(rot / (rot - 2)) in the place of base
+ *   IHA_ROPE_PARTS   w_i (g + (1 - g) / f), g = (trained w_i / 2 pi - slow) / (fast - slow)
+ *                    within [0, 1]: pairs that turn more than `fast` times over the
+ *                    trained length keep their frequency, below `slow` times it is w_i / f
+ */
+typedef enum {
+  IHA_ROPE_NONE = 0,
+  IHA_ROPE_LINEAR = 1,
+  IHA_ROPE_BASE = 2,
+  IHA_ROPE_PARTS = 3
+} iha_rope_scaling;
+
+typedef struct {
+  /* set by the caller before iha_rope_init */
+  int32_t rot;         /* rotated features of a head, even, 2 .. 256 */
+  int32_t interleaved; /* 0 or 1 */
+  int32_t scaling;     /* iha_rope_scaling */
+  int32_t trained;     /* PARTS: positions of the trained length */
+  double base;         /* > 1, usually 10000 */
+  double factor;       /* f */
+  double fast, slow;   /* PARTS: 0 <= slow < fast, usually 32 and 1 */
+  double gain;         /* 0: 1, with PARTS 0.1 ln f + 1 */
+  /* set by iha_rope_init */
+  uint64_t turn[128];  /* 2^-64 turns of pair i per position */
+  float mul;           /* the gain */
+  int32_t unused;
+} iha_rope;
+
+/* Checks the caller's fields of a rope and fills in the others (host only). */
+iha_status iha_rope_init(iha_rope* rope);
+
+/*
+ * The rotation of q and k in one launch, and of their gradients (which turns the
+ * other way, with the same gain):
+ *   q, yq      [B, N, Hq, d] views, dtype dt (bf16 or f32), element strides sq, syq
+ *              (b_outer, seq, head; b_inner unused), >= 0, multiples of 16 bytes
+ *   k, yk      [B, N, Hk, d] views likewise; both NULL with Hk = 0 for q alone
+ *   positions  int32 [B, N] dense (device), any values; NULL: row (b, n) is at n
+ *   rope       host memory, from iha_rope_init; copied before the call returns
+ * yq may be q itself (same pointer and strides: in place), yk may be k; else no row of
+ * an output may lie on a row of an input or of another output.
+ * d a multiple of 16 bytes, rot <= d.  Angles are exact modulo a turn to 2^-32 turns
+ * wherever the position, sines and cosines good to about 2^-23, products in fp32.
+ */
+iha_status iha_rope_fwd(const void* q, const void* k, const int32_t* positions, void* yq,
+                        void* yk, const iha_rope* rope, int B, int N, int Hq, int Hk, int d,
+                        iha_strides sq, iha_strides sk, iha_strides syq, iha_strides syk,
+                        iha_dtype dt, void* stream);
+iha_status iha_rope_bwd(const void* dyq, const void* dyk, const int32_t* positions, void* dq,
+                        void* dk, const iha_rope* rope, int B, int N, int Hq, int Hk, int d,
+                        iha_strides sdyq, iha_strides sdyk, iha_strides sdq, iha_strides sdk,
+                        iha_dtype dt, void* stream);
 
 /*
  * Premix input gradient ("Pseudo-Token Mixing", backward, dX = W^T dY):
@@ -395,6 +461,105 @@ iha_status mha_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
                        float scale, iha_mask mask_mode, int window, iha_dtype dt, void* stream);
 
 /*
+ * The 8-bit key-value cache.  16 consecutive positions of a sequence (a block) hold, for
+ * each key-value head, K rows and V rows of d features as e4m3 codes c (8 bits: 4
+ * of exponent, 3 of fraction) with one scale s = 2^e for the block's K and one for its
+ * V: e is the smallest with every |x| <= 448 * 2^e, at least -100, and c = x / s rounded
+ * to nearest even.  A value stands for s * c.  A row (one token and head, of K or
+ * of V) that holds a NaN or an infinity stands for NaN throughout, and has no part in s.
+ * 2 d + 1 bytes per token and head.
+ *
+ * The cache is n_pages pages of kv8_page_bytes() bytes, dense, 16-byte aligned; a page
+ * holds `page` tokens (a multiple of 16) of all Hkv heads, K and V.  Key j of sequence
+ * b is in page block_table[b, j / page]; a slot is page id * page + offset.  The order
+ * of the bytes inside a page belongs to the library.  Pages need no initial value.
+ * d is 32, 64, 96 or 128; n_pages * page < 2^31.
+ */
+size_t kv8_page_bytes(int page, int Hkv, int d);  /* 0 for sizes it cannot hold */
+
+/*
+ * Add rows to the ends of sequences: sequence b has seq_lens[b] keys once they are
+ * added, and row (b, n) of k and v is its key seq_lens[b] - N + n.  Of the N rows the
+ * last counts[b] are added (all N if counts is NULL); rows of keys before the first
+ * are padding.
+ *   k, v         [B, N, Hkv, d] views, dtype dt (bf16 or f32), element strides sk, sv
+ *                (b_outer, seq, head; b_inner unused), >= 0, multiples of 16 bytes
+ *   block_table  int32 [B, table_width] dense, only entries of pages that get rows are read
+ *   seq_lens     int32 [B], counts int32 [B] or NULL.  A length outside [0, table_width *
+ *                page], a count outside [0, N] is clamped, a page id outside the cache is
+ *                skipped; all are flagged (iha_device_error).
+ * A block that has keys before its first new row keeps them: its scales become the
+ * larger of what they were and what the new rows need, and where one grows the
+ * codes that are there are rounded again (exact but for codes that become subnormal).
+ * A block whose first row is new starts afresh, its rows behind the last key become
+ * zeros.  Every other byte of the cache keeps its value.  Blocks that two sequences of
+ * a call share race.
+ */
+iha_status kv8_append(const void* k, const void* v, const int32_t* block_table,
+                      const int32_t* seq_lens, const int32_t* counts, void* cache, int B, int N,
+                      int n_pages, int page, int table_width, int Hkv, int d, iha_strides sk,
+                      iha_strides sv, iha_dtype dt, void* stream);
+
+/*
+ * Read rows back by their slots, s * c exactly in f32 or rounded to bf16 (exact too,
+ * unless it overflows); arguments, padding and checks as kv4_load.
+ */
+iha_status kv8_load(const void* cache, const int32_t* slots, void* k, void* v, int B_outer,
+                    int B_inner, int N, int n_pages, int page, int Hkv, int d, iha_strides sk,
+                    iha_strides sv, iha_dtype dt, void* stream);
+
+/*
+ * Softmax attention of Nq new tokens of each of B sequences over the 8-bit cache:
+ * arguments, masks, lengths, limits and results as mha_fwd_kv4, and
+ *   weights, weights_out   both NULL, or float32 [B, Hkv, table_width * page] dense: the
+ *                attention weight that each key has gathered,
+ *       weights_out[b, h, j] = weights[b, h, j] + sum over t and the query heads of h of
+ *                              softmax_j(scale <q[b, t, .], k_j>),
+ *                where key j is visible, else weights[b, h, j].  They may be the same
+ *                array.  Needs Nq * Hq / Hkv <= 64; new keys usually start at 0.
+ *   workspace    of mha_fwd_kv8_workspace_bytes() bytes, weight_keys = table_width * page
+ *                for a call with weights, else 0; zeroed and shared like mha_fwd_kv4's
+ *                (one workspace serves calls of both, one after the other)
+ * Accuracy: scores, sums, weights and O are held in fp32, codes enter exactly, q with its
+ * 8-bit mantissas (features below 2^-28 of a row's largest lose bits); p times V's scale
+ * is rounded to fp16, 2^-11 of a term.  o is rounded to bf16.  |q| * |k| * scale has to
+ * stay within fp32.  The result does not depend on timing.
+ */
+size_t mha_fwd_kv8_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, int weight_keys);
+iha_status mha_fwd_kv8(const void* q, const void* cache, const int32_t* block_table,
+                       const int32_t* seq_lens, void* o, float* lse_out, const float* weights,
+                       float* weights_out, void* workspace, size_t workspace_bytes, int B, int Nq,
+                       int Hq, int Hkv, int d, int n_pages, int page, int table_width,
+                       iha_strides sq, iha_strides so, float scale, iha_mask mask_mode, int window,
+                       iha_dtype dt, void* stream);
+
+/*
+ * Eviction: shorten sequences to the keys that matter, head by head.  Of a sequence of
+ * n = seq_lens[b] > keep keys each head keeps its last `recent` and, of the others, the
+ * keep - recent of the largest weight (of equal ones the first; NaN counts as -inf); a
+ * sequence of up to keep keys is kept whole.  Kept rows are copied in the order of their
+ * positions to positions 0, 1, ... of pages dest_table[b, .]; a block's scales there are the
+ * largest that its rows come with, codes of other blocks are rounded again (exact but for
+ * codes that become subnormal).  Rows behind the last key of a block become zeros.
+ *   block_table  int32 [B, table_width], seq_lens int32 [B] (clamped and flagged as above)
+ *   weights      float32 [B, Hkv, table_width * page] dense
+ *   dest_table   int32 [B, dest_width]: pages that no sequence of the call reads and
+ *                that differ from one another (not checked; sources may be shared)
+ *   new_lens     int32 [B], written: min(n, keep)
+ *   kept         int32 [B, Hkv, keep], written: positions of the kept keys, then -1
+ *   weights_out  nullable; float32 [B, Hkv, dest_width * page], written: their weights,
+ *                then 0
+ * 0 <= recent <= keep, dest_width * page >= min(keep, table_width * page).  Afterwards
+ * keys sit at other distances than their tokens: attend with IHA_MASK_CAUSAL or
+ * IHA_MASK_NONE.  A page id outside the cache leaves its rows zero or unwritten (flagged).
+ */
+iha_status kv8_evict(void* cache, const int32_t* block_table, const int32_t* seq_lens,
+                     const float* weights, const int32_t* dest_table, int32_t* new_lens,
+                     int32_t* kept, float* weights_out, int B, int n_pages, int page,
+                     int table_width, int dest_width, int Hkv, int d, int keep, int recent,
+                     void* stream);
+
+/*
  * Mask-unit gather (README item 2, x[mask] -> gather):
  *   out[b,k,t,:] = x[b, tok(keep[b,k], t), :]
  * where the grid is row-major [grid_h, grid_w], mask units are mu_h x mu_w
@@ -442,15 +607,15 @@ iha_status mu_attention_fused(const void* x, const int32_t* keep, void* canvas, 
 
 /*
  * Test hook for the failure path; never needed in normal use.  Arms the next
- * bf16 mha_fwd or mha_fwd_kv4 launch made on the calling host thread (one shot)
- * so that CTA 0 withholds the load of its first V tile (mha_fwd_kv4: the
+ * bf16 mha_fwd, mha_fwd_kv4 or mha_fwd_kv8 launch made on the calling host thread (one shot)
+ * so that CTA 0 withholds the load of its first V tile (the caches' attentions: the
  * completion of its first blocks' copy) and every wait of that launch
  * gives up after limit_us microseconds (1 .. 1e6) instead of the normal 4 s.
  * The launch then takes its abort path: the waiting role raises the block's
  * abort flag, the others unwind, copies in flight land, the MMAs drain,
  * tensor memory is released, and the kernel returns with device error 2
  * (iha_device_error); rows that CTA 0 had a part in are left unwritten.  The GPU
- * context stays usable and the next launch runs normally (mha_fwd_kv4: once its
+ * context stays usable and the next launch runs normally (caches: once its
  * workspace is zeroed again).
  * IHA_ERR_INVALID_ARG for a limit out of range.
  */
@@ -466,8 +631,8 @@ const char* iha_last_error(void);
  * Device error word of the current device: 0 if no kernel has flagged an
  * error, else a bitwise OR of codes (1 = out-of-range keep index, 2 = a
  * bounded internal wait gave up, 4 = a kernel found its dynamic shared memory
- * not 1024-byte aligned and did nothing, 8 = a slot, page id or length outside
- * the 4-bit cache).  Synchronises the device; clears the word if clear != 0.
+ * not 1024-byte aligned and did nothing, 8 = a slot, page id, length or count
+ * outside the 4-bit or 8-bit cache).  Synchronises the device; clears the word if clear != 0.
  * Returns -1 if the word cannot be read.
  */
 int iha_device_error(int clear);

@@ -371,3 +371,141 @@ def premix_at(x: np.ndarray, w: np.ndarray, P: int, positions: np.ndarray,
             y[b, n] = premix_fwd(np.ascontiguousarray(x[b:b + 1, n:n + 1]), w, P, rope=True,
                                  rope_base=rope_base, pos0=int(positions[b, n]))[0, 0]
     return y
+
+
+# ---------------------------------------------------------------- rotary positions
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None,
+                     factor: float = 1.0, trained: int = 0, fast: float = 32.0, slow: float = 1.0):
+    """(w [rot/2] radians per position, gain), float64: base^(-2i/rot), unscaled or
+    "linear" (divided by factor), "base" (base * factor^(rot/(rot-2))), "parts" (mixed by
+    how often a pair turns over the trained length; gain 0.1 ln factor + 1)."""
+    i = np.arange(rot // 2, dtype=np.float64)
+    if scaling == "base":
+        base = base * factor ** (rot / (rot - 2))
+    w = base ** (-2.0 * i / rot)
+    if scaling == "linear":
+        return w / factor, 1.0
+    if scaling == "parts":
+        g = np.clip((trained * w / (2 * np.pi) - slow) / (fast - slow), 0.0, 1.0)
+        return w * (g + (1 - g) / factor), 0.1 * math.log(factor) + 1.0
+    return w, 1.0
+
+
+def rope(x: np.ndarray, positions: np.ndarray, w: np.ndarray, gain: float = 1.0,
+         interleaved: bool = False, back: bool = False) -> np.ndarray:
+    """x [B, N, H, d] (float32 or bf16 bits) rotated at positions [B, N], float64: pair
+    i of the first 2 len(w) features by positions * w[i], times gain; back: the
+    transpose of that (the gradient)."""
+    y = _as_f32(x).astype(np.float64)
+    n = len(w)
+    a = positions.astype(np.float64)[..., None, None] * w
+    c, s = gain * np.cos(a), gain * np.sin(a) * (-1.0 if back else 1.0)
+    lo, hi = (slice(0, 2 * n, 2), slice(1, 2 * n, 2)) if interleaved else \
+        (slice(0, n), slice(n, 2 * n))
+    p, q = y[..., lo].copy(), y[..., hi].copy()
+    y[..., lo] = p * c - q * s
+    y[..., hi] = q * c + p * s
+    return y
+
+
+# ---------------------------------------------------------------- 8-bit key-value cache
+def round_e4m3(y: np.ndarray) -> np.ndarray:
+    """The nearest number of 4 exponent and 3 fraction bits (exponent >= -6), ties to
+    even; |y| <= 448."""
+    _, e = np.frexp(np.asarray(y, dtype=np.float64))
+    step = np.ldexp(1.0, np.maximum(e - 1, -6) - 3)
+    return np.rint(y / step) * step
+
+
+def kv8_exponent(x: np.ndarray) -> np.ndarray:
+    """The smallest e >= -100 with every |x| <= 448 * 2^e, over rows x [n, H, d]: [H]."""
+    top = np.abs(x).max(axis=(0, 2), initial=0.0)
+    f, e = np.frexp(top)                               # top = f 2^e, 1/2 <= f < 1; 448 = 7/8 2^9
+    return np.where(top == 0, -100, np.maximum(e - 9 + (f > 0.875), -100)).astype(np.int64)
+
+
+class Kv8Rows:
+    """The K (or V) rows of one sequence in the 8-bit cache: values [n, H, d] float64,
+    e [blocks, H] of each block of 16 positions."""
+
+    def __init__(self, H: int, d: int):
+        self.values = np.zeros((0, H, d))
+        self.e = np.zeros((0, H), np.int64)
+
+    def append(self, x: np.ndarray) -> "Kv8Rows":
+        """Rows x [m, H, d] (float32 or bf16 bits) added at the end, in one call."""
+        x = _as_f32(x).astype(np.float64)
+        x = np.where(np.isfinite(x).all(axis=2, keepdims=True), x, np.nan)  # a row of NaN
+        n, at = len(self.values), 0
+        self.values = np.concatenate([self.values, np.zeros_like(x)])
+        while at < len(x):
+            blk, had = divmod(n + at, 16)
+            m = min(16 - had, len(x) - at)
+            new = x[at:at + m]
+            e = kv8_exponent(np.nan_to_num(new, nan=0.0))
+            first = 16 * blk
+            if had:
+                e = np.maximum(e, self.e[blk])
+                old = self.values[first:first + had]
+                self.values[first:first + had] = _at_scale(old, e)
+                self.e[blk] = e
+            else:
+                self.e = np.concatenate([self.e, e[None]])
+            self.values[first + had:first + had + m] = _at_scale(new, e)
+            at += m
+        return self
+
+    def evicted(self, kept: np.ndarray) -> "Kv8Rows":
+        """The rows of kept [H, m] (positions, head by head) in blocks of their own."""
+        H, m = kept.shape
+        out = Kv8Rows(H, self.values.shape[2])
+        h = np.arange(H)[:, None]
+        v, e = self.values[kept, h], self.e[kept // 16, h]           # [H, m, d], [H, m]
+        out.values = np.zeros((m, H, v.shape[2]))
+        out.e = np.zeros((-(-m // 16), H), np.int64)
+        for i in range(len(out.e)):
+            s = slice(16 * i, min(m, 16 * i + 16))
+            out.e[i] = e[:, s].max(axis=1)
+            out.values[s] = _at_scale(v[:, s].transpose(1, 0, 2), out.e[i])
+        return out
+
+
+def _at_scale(x: np.ndarray, e: np.ndarray) -> np.ndarray:
+    s = np.ldexp(1.0, e)[:, None]
+    with np.errstate(invalid="ignore"):
+        return np.where(np.isnan(x), np.nan, round_e4m3(np.nan_to_num(x, nan=0.0) / s) * s)
+
+
+def kv8_kept(weights: np.ndarray, keep: int, recent: int) -> np.ndarray:
+    """Positions [H, min(n, keep)] that each head of a sequence keeps, of weights [H, n]:
+    the last `recent`, and of the others those of the largest weight (NaN as -inf; of
+    equal ones the first)."""
+    H, n = weights.shape
+    if n <= keep:
+        return np.broadcast_to(np.arange(n), (H, n)).copy()
+    w = np.where(np.isnan(weights), -np.inf, weights).astype(np.float64)
+    out = np.empty((H, keep), np.int64)
+    for h in range(H):
+        order = sorted(range(n - recent), key=lambda j: (-w[h, j], j))[:keep - recent]
+        out[h] = sorted(order) + list(range(n - recent, n))
+    return out
+
+
+def kv8_weights(q: np.ndarray, k: np.ndarray, mask: int = MASK_CAUSAL, window: int = 0,
+                scale: float | None = None) -> np.ndarray:
+    """[Hkv, n]: the softmax weights of kv4_attention's rows on each key, summed over the
+    rows and the query heads of a key head."""
+    qf = _as_f32(q).astype(np.float64)
+    Nq, Hq, d = qf.shape
+    n, Hkv, _ = k.shape
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    out = np.zeros((Hkv, n))
+    for t in range(Nq):
+        i = n - Nq + t
+        hi = n if mask == MASK_NONE else min(n, i + 1)
+        lo = max(0, i - window + 1) if mask == MASK_CAUSAL_WINDOW else 0
+        for h in range(Hq if hi > lo else 0):
+            x = scale * (k[lo:hi, h * Hkv // Hq] @ qf[t, h])
+            p = np.exp(x - x.max())
+            out[h * Hkv // Hq, lo:hi] += p / p.sum()
+    return out

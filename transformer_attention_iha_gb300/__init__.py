@@ -16,6 +16,11 @@ Entry points (same names as the C ABI in include/iha.h):
                                             -- serving: the premix of tokens at
       given positions, a paged key-value cache held in 4 bits, the attention
       of new tokens over it
+  Rope, rope_fwd, rope_bwd                  -- rotary positions as operators of
+      their own: both layouts, part of a head, scaled for long contexts
+  kv8_append, kv8_load, mha_fwd_kv8, kv8_evict
+                                            -- a paged cache held in 8 bits, the
+      attention over it with the weight that each key gathers, eviction by it
 PyTorch supplies device memory and the current stream only.
 """
 from __future__ import annotations
@@ -31,7 +36,9 @@ __all__ = ["build", "lib", "premix_fwd", "premix_bwd_dx", "premix_bwd_dw", "prem
            "mu_gather", "mu_scatter", "device_error", "IHAError", "Strides", "MASK_NONE",
            "MASK_CAUSAL", "MASK_CAUSAL_WINDOW", "F32", "BF16",
            "premix_fwd_qkv_at", "kv4_page_bytes", "kv4_store", "kv4_load",
-           "mha_fwd_kv4", "mha_fwd_kv4_workspace_bytes"]
+           "mha_fwd_kv4", "mha_fwd_kv4_workspace_bytes",
+           "Rope", "rope_fwd", "rope_bwd", "kv8_page_bytes", "kv8_append", "kv8_load",
+           "mha_fwd_kv8", "mha_fwd_kv8_workspace_bytes", "kv8_evict"]
 
 IHA_OK, IHA_ERR_INVALID_ARG, IHA_ERR_UNSUPPORTED, IHA_ERR_ALIGNMENT, IHA_ERR_CUDA = range(5)
 F32, BF16 = 0, 1
@@ -43,7 +50,9 @@ SYMBOLS = ("iha_premix_fwd", "iha_premix_bwd_dx", "iha_premix_bwd_dw", "iha_prem
            "mha_bwd_noalloc", "iha_premix_fwd_qkv", "mu_attention_fused",
            "iha_premix_fwd_qkv_interleaved", "iha_premix_bwd_qkv", "mha_fwd_qpool",
            "iha_premix_fwd_qkv_at", "kv4_page_bytes", "kv4_store", "kv4_load",
-           "mha_fwd_kv4_workspace_bytes", "mha_fwd_kv4")
+           "mha_fwd_kv4_workspace_bytes", "mha_fwd_kv4",
+           "iha_rope_init", "iha_rope_fwd", "iha_rope_bwd", "kv8_page_bytes", "kv8_append",
+           "kv8_load", "mha_fwd_kv8_workspace_bytes", "mha_fwd_kv8", "kv8_evict")
 
 
 class IHAError(RuntimeError):
@@ -103,7 +112,20 @@ def lib() -> C.CDLL:
     L.mha_fwd_kv4_workspace_bytes.argtypes = [i, i, i, i, i]
     L.mha_fwd_kv4_workspace_bytes.restype = C.c_size_t
     L.mha_fwd_kv4.argtypes = [vp] * 7 + [C.c_size_t] + [i] * 8 + [Strides, Strides, f, i, i, i, vp]
-    for name in ("iha_premix_fwd_qkv_at", "kv4_store", "kv4_load", "mha_fwd_kv4",
+    L.iha_rope_init.argtypes = [vp]
+    for name in ("iha_rope_fwd", "iha_rope_bwd"):
+        getattr(L, name).argtypes = [vp] * 6 + [i] * 5 + [Strides] * 4 + [i, vp]
+    L.kv8_page_bytes.argtypes = [i, i, i]
+    L.kv8_page_bytes.restype = C.c_size_t
+    L.kv8_append.argtypes = [vp] * 6 + [i] * 7 + [Strides, Strides, i, vp]
+    L.kv8_load.argtypes = [vp] * 4 + [i] * 7 + [Strides, Strides, i, vp]
+    L.mha_fwd_kv8_workspace_bytes.argtypes = [i] * 6
+    L.mha_fwd_kv8_workspace_bytes.restype = C.c_size_t
+    L.mha_fwd_kv8.argtypes = [vp] * 9 + [C.c_size_t] + [i] * 8 + [Strides, Strides, f, i, i, i, vp]
+    L.kv8_evict.argtypes = [vp] * 8 + [i] * 9 + [vp]
+    for name in ("iha_rope_init", "iha_rope_fwd", "iha_rope_bwd", "kv8_append", "kv8_load",
+                 "mha_fwd_kv8", "kv8_evict",
+                 "iha_premix_fwd_qkv_at", "kv4_store", "kv4_load", "mha_fwd_kv4",
                  "iha_premix_fwd", "iha_premix_fwd_qkv", "iha_premix_fwd_qkv_interleaved",
                  "iha_premix_bwd_dx",
                  "iha_premix_bwd_dw", "iha_premix_bwd", "mha_fwd", "mha_bwd", "mu_gather",
@@ -691,6 +713,298 @@ def mha_fwd_kv4(q, cache, block_table, seq_lens, Hkv: int, page: int, mask: int 
                             Strides(so[0], 0, so[1], so[2]), scale, mask, window, BF16, sp),
           "mha_fwd_kv4")
     return (out, lse) if return_lse else out
+
+
+# ---------------------------------------------------------------- rotary positions
+class _RopeC(C.Structure):
+    _fields_ = [("rot", C.c_int32), ("interleaved", C.c_int32), ("scaling", C.c_int32),
+                ("trained", C.c_int32), ("base", C.c_double), ("factor", C.c_double),
+                ("fast", C.c_double), ("slow", C.c_double), ("gain", C.c_double),
+                ("turn", C.c_uint64 * 128), ("mul", C.c_float), ("unused", C.c_int32)]
+
+
+_ROPE_SCALING = {None: 0, "linear": 1, "base": 2, "parts": 3}
+
+
+class Rope:
+    """The frequencies of a rotation, for rope_fwd and rope_bwd; made once and kept.
+
+    rot: rotated features of a head (even, from the first on; the others are copied).
+    interleaved: pairs (2i, 2i+1) instead of (i, i + rot/2).  Pair i turns by
+    base^(-2i/rot) a position, changed for long contexts by `factor` as `scaling`
+    says: "linear" (divided by it), "base" (base times factor^(rot/(rot-2))), "parts"
+    (pairs of more than `fast` turns over `trained` positions as they are, of fewer
+    than `slow` divided, in between mixed; results times 0.1 ln factor + 1).
+    gain: the results' factor instead of the usual one."""
+
+    def __init__(self, rot: int, base: float = 10000.0, interleaved: bool = False, scaling=None,
+                 factor: float = 1.0, trained: int = 0, fast: float = 32.0, slow: float = 1.0,
+                 gain: float = 0.0):
+        if scaling not in _ROPE_SCALING:
+            raise ValueError(f"scaling {scaling!r}: one of None, 'linear', 'base', 'parts'")
+        self._c = _RopeC(rot=int(rot), interleaved=int(bool(interleaved)),
+                         scaling=_ROPE_SCALING[scaling], trained=int(trained), base=base,
+                         factor=factor, fast=fast, slow=slow, gain=gain)
+        check(lib().iha_rope_init(C.addressof(self._c)), "iha_rope_init")
+        self.rot, self.gain = self._c.rot, self._c.mul
+
+
+def _strides4(t) -> Strides:
+    s = t.stride()
+    return Strides(s[0], 0, s[1], s[2])
+
+
+_NO_STRIDES = Strides(0, 0, 0, 0)
+
+
+def _rotate(fn, where, q, k, positions, rope, out, stream):
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must be a Rope")
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError(f"q must be [B, N, H, d], got {tuple(shape)}")
+    B, N, Hq, d = shape
+    dev, dt = q.get_device(), _dt(q)
+    _view(q, "q", shape, q.dtype, dev)
+    Hk = 0
+    if k is not None:
+        if k.dim() != 4:
+            raise ValueError(f"k must be [B, N, Hk, d], got {tuple(k.shape)}")
+        Hk = k.shape[2]
+        _view(k, "k", (B, N, Hk, d), q.dtype, dev)
+    if positions is not None:
+        _dense(positions, "positions", (B, N), _torch().int32, dev)
+    sp = _raw_stream(dev, stream)
+    if out is None:
+        yq = _make(shape, q.dtype, q, stream)
+        yk = None if k is None else _make(k.shape, q.dtype, q, stream)
+    else:
+        if len(out) != 2 or (out[1] is None) != (k is None):
+            raise ValueError("out must hold two tensors (q, k), the second None without k")
+        yq, yk = out
+        _view(yq, "out[0]", shape, q.dtype, dev)
+        if yk is not None:
+            _view(yk, "out[1]", k.shape, q.dtype, dev)
+    check(fn(q.data_ptr(), 0 if k is None else k.data_ptr(),
+             0 if positions is None else positions.data_ptr(), yq.data_ptr(),
+             0 if k is None else yk.data_ptr(), C.addressof(rope._c), B, N, Hq, Hk, d, _strides4(q),
+             _NO_STRIDES if k is None else _strides4(k), _strides4(yq),
+             _NO_STRIDES if k is None else _strides4(yk), dt, sp), where)
+    return yq, yk
+
+
+def rope_fwd(q, k, positions, rope: Rope, out=None, stream=None):
+    """(Y_q, Y_k): the rows of q [B,N,Hq,d] and k [B,N,Hk,d] (views, bf16 or fp32; k
+    may be None) rotated at positions int32 [B,N] (None: 0 .. N-1).  out: the two
+    tensors to write instead, q and k themselves to rotate in place."""
+    return _rotate((_lib or lib()).iha_rope_fwd, "iha_rope_fwd", q, k, positions, rope, out, stream)
+
+
+def rope_bwd(dyq, dyk, positions, rope: Rope, out=None, stream=None):
+    """(dQ, dK) of rope_fwd, from the gradients of its results: turned back, times
+    the same gain.  Arguments as rope_fwd."""
+    return _rotate((_lib or lib()).iha_rope_bwd, "iha_rope_bwd", dyq, dyk, positions, rope, out,
+                   stream)
+
+
+# ---------------------------------------------------------------- 8-bit key-value cache
+@functools.lru_cache(maxsize=256)
+def kv8_page_bytes(page: int, Hkv: int, d: int) -> int:
+    """Bytes of one page of `page` tokens (K and V of Hkv heads of d features).  A
+    cache is a uint8 CUDA tensor [n_pages, kv8_page_bytes(page, Hkv, d)]; it needs no
+    initial value."""
+    n = int(lib().kv8_page_bytes(page, Hkv, d))
+    if n == 0:
+        raise ValueError(f"no 8-bit cache of page {page}, {Hkv} heads of {d} features: page must "
+                         "be a multiple of 16, d one of 32, 64, 96, 128")
+    return n
+
+
+def _kv8_pages(cache, page: int, Hkv: int, d: int, dev: int) -> int:
+    """Checks a cache tensor; its number of pages."""
+    nb = kv8_page_bytes(page, Hkv, d)
+    if cache.dim() != 2 or cache.shape[1] != nb:
+        raise ValueError(f"cache must be [n_pages, kv8_page_bytes = {nb}], got "
+                         f"{tuple(cache.shape)}")
+    _dense(cache, "cache", None, _torch().uint8, dev)
+    return cache.shape[0]
+
+
+def _table(table, name: str, B: int, dev: int) -> int:
+    """Checks a table of pages [B, width]; its width."""
+    _dense(table, name, None, _torch().int32, dev)
+    if table.dim() != 2 or table.shape[0] != B:
+        raise ValueError(f"{name} must be [B={B}, width], got {tuple(table.shape)}")
+    return table.shape[1]
+
+
+def kv8_append(k, v, block_table, seq_lens, cache, page: int, counts=None, stream=None):
+    """Add rows to the ends of sequences in the 8-bit cache: row n of k, v
+    ([B,N,Hkv,d] views, bf16 or fp32) of sequence b is its key seq_lens[b] - N + n.
+    seq_lens int32 [B] counts the keys with the new ones; key j is in page
+    block_table[b, j // page] (int32 [B, table_width]).  Of the N rows the last
+    counts[b] (int32 [B]; all without it) are added.  Returns the cache."""
+    torch = _torch()
+    shape = k.shape
+    if len(shape) != 4:
+        raise ValueError(f"k and v must be [B, N, Hkv, d], got {tuple(shape)}")
+    B, N, Hkv, d = shape
+    dev, dt = k.get_device(), _dt(k)
+    _view(k, "k", shape, k.dtype, dev)
+    _view(v, "v", shape, k.dtype, dev)
+    width = _table(block_table, "block_table", B, dev)
+    _dense(seq_lens, "seq_lens", (B,), torch.int32, dev)
+    if counts is not None:
+        _dense(counts, "counts", (B,), torch.int32, dev)
+    n_pages = _kv8_pages(cache, page, Hkv, d, dev)
+    check((_lib or lib()).kv8_append(
+        k.data_ptr(), v.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        0 if counts is None else counts.data_ptr(), cache.data_ptr(), B, N, n_pages, page, width,
+        Hkv, d, _strides4(k), _strides4(v), dt, _raw_stream(dev, stream)), "kv8_append")
+    return cache
+
+
+def kv8_load(cache, slots, Hkv: int, d: int, page: int, dtype=None, out=None, stream=None):
+    """(k, v), each [*slots.shape, Hkv, d] in dtype (bf16 unless given, or fp32):
+    the rows of the 8-bit cache at int32 slots [B,N] or [Bo,Bi,N] (page id * page +
+    offset); slot -1 gives zeros.  out: the two tensors to write instead (strided
+    views allowed)."""
+    torch = _torch()
+    dev = slots.get_device()
+    if slots.dim() not in (2, 3):
+        raise ValueError(f"slots must be [B, N] or [Bo, Bi, N], got {tuple(slots.shape)}")
+    _dense(slots, "slots", None, torch.int32, dev)
+    n_pages = _kv8_pages(cache, page, Hkv, d, dev)
+    sp = _raw_stream(dev, stream)
+    shape = slots.shape + (Hkv, d)
+    if out is None:
+        dtype = dtype or torch.bfloat16
+        k = _make(shape, dtype, cache, stream)
+        v = _make(shape, dtype, cache, stream)
+    else:
+        if len(out) != 2:
+            raise ValueError("out must hold two tensors (k, v)")
+        k, v = out
+        dtype = dtype or k.dtype
+        _view(k, "out[0]", shape, dtype, dev)
+        _view(v, "out[1]", shape, dtype, dev)
+    check((_lib or lib()).kv8_load(
+        cache.data_ptr(), slots.data_ptr(), k.data_ptr(), v.data_ptr(), shape[0],
+        1 if len(shape) == 4 else shape[1], shape[-3], n_pages, page, Hkv, d, _strides45(k),
+        _strides45(v), _dt(k), sp), "kv8_load")
+    return k, v
+
+
+def mha_fwd_kv8_workspace_bytes(B: int, Nq: int, Hq: int, Hkv: int, d: int,
+                                weight_keys: int = 0) -> int:
+    """Bytes of device scratch of mha_fwd_kv8; the first 4096 zero-filled once, then
+    reusable.  weight_keys: table_width * page for calls with weights, else 0."""
+    return int(lib().mha_fwd_kv8_workspace_bytes(B, Nq, Hq, Hkv, d, weight_keys))
+
+
+def mha_fwd_kv8(q, cache, block_table, seq_lens, Hkv: int, page: int, mask: int = MASK_CAUSAL,
+                window: int = 0, scale: float = 0.0, out=None, lse=None, return_lse: bool = False,
+                weights=None, weights_out=None, workspace=None, stream=None):
+    """Attention of the last Nq tokens of each sequence (q [B,Nq,Hq,d] bf16 view)
+    over the 8-bit paged cache; arguments as mha_fwd_kv4.
+
+    weights (fp32 [B, Hkv, table_width * page]): the attention weight that each key has
+    gathered; weights_out (may be weights itself, made here when not given) becomes it
+    plus the weights of this call.  Returns O shaped like q, and after it lse
+    [B, Hq, Nq] fp32 with return_lse, weights_out with weights.
+    `workspace` (uint8 CUDA tensor of mha_fwd_kv8_workspace_bytes, its first 4096
+    bytes zero-filled before its first use, one for each call that may run at the
+    same time) is made here when not given."""
+    torch = _torch()
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError("q must be [B, Nq, Hq, d]")
+    B, Nq, Hq, d = shape
+    dev = q.get_device()
+    _view(q, "q", shape, torch.bfloat16, dev)
+    n_pages = _kv8_pages(cache, page, Hkv, d, dev)
+    width = _table(block_table, "block_table", B, dev)
+    _dense(seq_lens, "seq_lens", (B,), torch.int32, dev)
+    sp = _raw_stream(dev, stream)
+    if out is None:
+        out = _make(shape, torch.bfloat16, q, stream)
+    else:
+        _view(out, "out", shape, torch.bfloat16, dev)
+    if lse is not None:
+        _dense(lse, "lse", (B, Hq, Nq), torch.float32, dev)
+    elif return_lse:
+        lse = _make((B, Hq, Nq), torch.float32, q, stream)
+    keys = 0
+    if weights is not None:
+        keys = width * page
+        _dense(weights, "weights", (B, Hkv, keys), torch.float32, dev)
+        if weights_out is None:
+            weights_out = _make((B, Hkv, keys), torch.float32, q, stream)
+        else:
+            _dense(weights_out, "weights_out", (B, Hkv, keys), torch.float32, dev)
+    elif weights_out is not None:
+        raise ValueError("weights_out needs weights")
+    if workspace is None:
+        # all of it zeroed where that is little: a slice of it takes the host longer
+        workspace = _make(mha_fwd_kv8_workspace_bytes(B, Nq, Hq, Hkv, d, keys), torch.uint8, q,
+                          stream, zero=keys == 0)
+        if keys:
+            with torch.cuda.stream(stream or torch.cuda.current_stream()):
+                workspace[:4096].zero_()
+    else:
+        _dense(workspace, "workspace", None, torch.uint8, dev)
+    check((_lib or lib()).mha_fwd_kv8(
+        q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+        0 if weights is None else weights.data_ptr(),
+        0 if weights is None else weights_out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        B, Nq, Hq, Hkv, d, n_pages, page, width, _strides4(q), _strides4(out), scale, mask, window,
+        BF16, sp), "mha_fwd_kv8")
+    if not return_lse and weights is None:
+        return out
+    return (out,) + ((lse,) if return_lse else ()) + (() if weights is None else (weights_out,))
+
+
+def kv8_evict(cache, block_table, seq_lens, weights, dest_table, Hkv: int, d: int, page: int,
+              keep: int, recent: int, new_lens=None, kept=None, weights_out=None, stream=None):
+    """Shorten sequences of the 8-bit cache to `keep` keys a head: the last `recent`,
+    and of the others those of the largest weight (fp32 [B, Hkv, table_width * page], as
+    mha_fwd_kv8 gathers it), copied in their order to the pages of dest_table (int32
+    [B, dest_width], pages that no sequence of the call uses).
+
+    Returns (new_lens [B], kept [B, Hkv, keep] = the kept keys' positions and then -1,
+    both int32, weights_out fp32 [B, Hkv, dest_width * page] = their weights and then 0);
+    each is made here when not given."""
+    torch = _torch()
+    dev = cache.get_device()
+    n_pages = _kv8_pages(cache, page, Hkv, d, dev)
+    if seq_lens.dim() != 1:
+        raise ValueError(f"seq_lens must be [B], got {tuple(seq_lens.shape)}")
+    B = seq_lens.shape[0]
+    _dense(seq_lens, "seq_lens", (B,), torch.int32, dev)
+    width = _table(block_table, "block_table", B, dev)
+    dest_width = _table(dest_table, "dest_table", B, dev)
+    _dense(weights, "weights", (B, Hkv, width * page), torch.float32, dev)
+    sp = _raw_stream(dev, stream)
+    if keep < 1 or not 0 <= recent <= keep:
+        raise ValueError(f"keep {keep} must be positive and recent {recent} within [0, keep]")
+    if new_lens is None:
+        new_lens = _make((B,), torch.int32, cache, stream)
+    else:
+        _dense(new_lens, "new_lens", (B,), torch.int32, dev)
+    if kept is None:
+        kept = _make((B, Hkv, keep), torch.int32, cache, stream)
+    else:
+        _dense(kept, "kept", (B, Hkv, keep), torch.int32, dev)
+    if weights_out is None:
+        weights_out = _make((B, Hkv, dest_width * page), torch.float32, cache, stream)
+    else:
+        _dense(weights_out, "weights_out", (B, Hkv, dest_width * page), torch.float32, dev)
+    check((_lib or lib()).kv8_evict(
+        cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), weights.data_ptr(),
+        dest_table.data_ptr(), new_lens.data_ptr(), kept.data_ptr(), weights_out.data_ptr(), B,
+        n_pages, page, width, dest_width, Hkv, d, keep, recent, sp), "kv8_evict")
+    return new_lens, kept, weights_out
 
 
 # ---------------------------------------------------------------- gather / scatter

@@ -1,0 +1,572 @@
+// Softmax attention of new queries over a paged cache held in 8 bits
+// (mha_fwd_kv8; layout of the cache: kv8.cuh), and the keys' weights in it.
+//
+//   x_j = scale <q, k_j>,  o = sum_j softmax_j(x) v_j,  k_j = 2^e c
+//
+// One warp works on blocks of 16 tokens of one key-value head, for 8 NT columns; a
+// column is one (new token, query head of the group) pair.
+//   S^T [16 tokens x 8 columns] = K Q^T by mma.m16n8k16 on fp16: codes are exact in
+//     fp16, Q's row is scaled by a power of two to below 2^15 so that its 8-bit
+//     mantissas are too (features below 2^-28 of the largest lose bits).  The block's
+//     scale multiplies the fp32 accumulators.
+//   O^T [d x 8 columns] += V^T P^T, V's scale inside P: P s F in fp16, with a power of
+//     two F per column that keeps the largest of the sum so far between 2^5 and 2^15: F
+//     falls when a p s outgrows that, and rises with the softmax reference.  A term is
+//     off by 2^-11 of itself or, below 2^-19 of the largest, 2^-30 of that.  V's codes
+//     are turned by ldmatrix as pairs of features, P^T by movmatrix.
+//   Softmax in the log2 domain, fp32; a column's reference moves only when a score
+//     exceeds it, to 8 above that score (a token that weighs alone has p = 2^-8, and
+//     its P s exactly); then O and the sum are rescaled.
+#include <cuda_fp16.h>
+
+#include "kv8.cuh"
+#include "kv_attn.cuh"
+
+namespace iha {
+namespace {
+
+IHA_DEVICE_ERROR_WORD(attention_kv8)
+
+constexpr int NB = 2;  // blocks computed together
+// The largest F, 2^126 (its reciprocal is a normal number), and its exponent field.
+constexpr float kTopF = 8.5070591730234616e37f;
+constexpr int kTopFExp = 126 + 127;
+
+struct Kv8AttnParams : KvAttnParams {
+  float* scores;  // nullable: [B, Hkv, ncols, table_w * page], log2 domain, -inf where hidden
+};
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 u;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+               : "r"(addr)
+               : "memory");
+  return u;
+}
+
+// A warp's softmax state over one unit: 8 NT columns of one head.  ONE: a single
+// column, the odd columns of the operands are not computed.
+template <int D, int NT, bool ONE>
+struct Attend {
+  static constexpr int CH = D / 16, BYTES = kv8_block_bytes(D);
+  static constexpr int ES = ONE ? 2 : 1;  // step over the columns of a pair
+  int lane, g, t;
+  uint32_t row_at, row_chunk;  // this lane's row for ldmatrix: its offset, its first chunk
+  uint32_t qf[NT == 1 ? CH : 1][2];
+  uint2* q_smem;               // NT > 1: [NT * CH * 32]
+  float cm[NT][2];             // accumulators of columns 2 t, 2 t + 1 to scores, log2 domain
+  // a column's reference: 8 above the maximum when it was last set; mlim is the same,
+  // or -inf while no key has been seen (mref = 0)
+  float mlim[NT][2], mref[NT][2], l[NT][2], F[NT][2];
+  float acc[NT][CH][4];        // (feature 16 c + 2 g, columns 2 t, 2 t + 1), (the next feature, ...)
+
+  __device__ __forceinline__ void init(int lane_, uint2* smem) {
+    lane = lane_;
+    g = lane >> 2;
+    t = lane & 3;
+    q_smem = smem;
+    const int row = lane & 15;
+    row_at = row * D;
+    row_chunk = (uint32_t)((lane >> 4) ^ kv8_swap(D, row));
+  }
+
+  // Q as B operand: column 8 nt + g, features 16 c + 4 t .. + 3
+  __device__ __forceinline__ void load_q(const KvAttnParams& p, int b, int hk, int c_first) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int col = c_first + 8 * nt + g;
+      const bool in = col < p.ncols;
+      const int qi = in ? token_of(p, col) : 0, qh = hk * p.G + (in ? col - qi * p.G : 0);
+      const __nv_bfloat16* qp = p.q + b * p.sq.b_outer + qi * p.sq.seq + qh * p.sq.head + 4 * t;
+      uint2 v[CH];
+      uint32_t top = 0;
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+        v[c] = in ? __ldg(reinterpret_cast<const uint2*>(qp + 16 * c)) : make_uint2(0, 0);
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+        top = __vmaxu2(top, __vmaxu2(v[c].x & 0x7FFF7FFFu, v[c].y & 0x7FFF7FFFu));
+      top = max(top & 0xFFFFu, top >> 16);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // largest |q| in [2^e, 2^(e + 1)): Q is scaled by 2^(14 - e)
+      const int e = max((int)(top >> 7) - 127, -112);
+      const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+      const float back = ldexpf(p.scale_log2, e - 14);
+      cm[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);
+      cm[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const uint32_t h0 = pack_f16x2(bf16lo_to_f32(v[c].x) * up, bf16hi_to_f32(v[c].x) * up);
+        const uint32_t h1 = pack_f16x2(bf16lo_to_f32(v[c].y) * up, bf16hi_to_f32(v[c].y) * up);
+        if constexpr (NT == 1) {
+          qf[c][0] = h0;
+          qf[c][1] = h1;
+        } else {
+          q_smem[(nt * CH + c) * 32 + lane] = make_uint2(h0, h1);
+        }
+      }
+      mlim[nt][0] = mlim[nt][1] = -INFINITY;
+      mref[nt][0] = mref[nt][1] = 0.f;
+      l[nt][0] = l[nt][1] = 0.f;
+      F[nt][0] = F[nt][1] = kTopF;
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int e_ = 0; e_ < 4; ++e_) acc[nt][c][e_] = 0.f;
+    }
+    __syncwarp();
+  }
+
+  // A operand of 16 features: K rows (tokens), or V columns turned.
+  __device__ __forceinline__ uint32_t at(uint32_t s, int cc) const {
+    return s + row_at + ((row_chunk ^ (2 * cc)) << 4);
+  }
+
+  // Two blocks in shared memory at s, of keys from key0 on.  edge: not all of their keys
+  // are visible to every column; gone: a bit per block that no page holds or that lies
+  // past the unit's end, past: a bit per block past it.  scores: nullable, of column 0.
+  __device__ __forceinline__ void step(const Kv8AttnParams& p, uint32_t s, int key0, bool edge,
+                                       uint32_t gone, uint32_t past, int len, int c_first,
+                                       float* scores, int64_t cap) {
+    float x[NT][NB][4];  // (token g, columns 2 t, 2 t + 1), (token g + 8, ...)
+    float sv[NB];
+    uint32_t nan[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const uint4 tail = lds128(s + b * BYTES + 32 * D);
+      const float sk = __uint_as_float(tail.x);
+      sv[b] = __uint_as_float(tail.y);
+      nan[b] = tail.z;
+      float c4[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c4[nt][e] = 0.f;
+#pragma unroll
+      for (int cc = 0; cc < CH / 2; ++cc) {
+        uint32_t w[4];  // rows g, g + 8 of chunk 2 cc, then of 2 cc + 1
+        ldmatrix4(at(s + b * BYTES, cc), w);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t a0 = e4m3_to_f16((uint16_t)w[2 * h]);
+          const uint32_t a1 = e4m3_to_f16((uint16_t)w[2 * h + 1]);
+          const uint32_t a2 = e4m3_to_f16((uint16_t)(w[2 * h] >> 16));
+          const uint32_t a3 = e4m3_to_f16((uint16_t)(w[2 * h + 1] >> 16));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (NT == 1) {
+              mma_f16(c4[nt], a0, a1, a2, a3, qf[2 * cc + h][0], qf[2 * cc + h][1]);
+            } else {
+              const uint2 f = q_smem[(nt * CH + 2 * cc + h) * 32 + lane];
+              mma_f16(c4[nt], a0, a1, a2, a3, f.x, f.y);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; e += ES) x[nt][b][e] = c4[nt][e] * (sk * cm[nt][e & 1]);
+    }
+    const bool any_nan = (nan[0] | nan[1]) != 0;
+    if (any_nan) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; e += ES)
+            if ((nan[b] >> (g + (e & 2) * 4)) & 1u) x[nt][b][e] = __uint_as_float(0x7FC00000u);
+    }
+    uint32_t hidden = 0;  // bit 4 (nt NB + b) + e
+    if (edge) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; e += ES) {
+          const int col = c_first + 8 * nt + 2 * t + e;
+          int lo, hi;
+          col_range(p, len, col, lo, hi);
+          if (col >= p.ncols) hi = 0;
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int key = key0 + b * kKv8Tok + g + 8 * h;
+              if (key < lo || key >= hi || ((gone >> b) & 1u)) {
+                hidden |= 1u << (4 * (nt * NB + b) + 2 * h + e);
+                x[nt][b][2 * h + e] = -INFINITY;
+              }
+            }
+        }
+    }
+    if (scores != nullptr) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; e += ES) {
+          const int col = c_first + 8 * nt + 2 * t + e;
+          if (col < p.ncols)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+              if (!((past >> b) & 1u)) {
+                float* to = scores + col * cap + key0 + b * kKv8Tok + g;
+                to[0] = x[nt][b][e];
+                to[8] = x[nt][b][e + 2];
+              }
+        }
+    }
+    uint32_t pf[NT][NB][2];  // P as B operand
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float top[2];
+#pragma unroll
+      for (int e = 0; e < 2; e += ES)
+        top[e] = fmaxf(fmaxf(x[nt][0][e], x[nt][0][e + 2]), fmaxf(x[nt][1][e], x[nt][1][e + 2]));
+      if (__any_sync(0xffffffffu, top[0] > mlim[nt][0] || (!ONE && top[1] > mlim[nt][1]))) {
+#pragma unroll
+        for (int e = 0; e < 2; e += ES) {
+          float v = top[e];
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+          // a column below its limit keeps its reference
+          v = v > mlim[nt][e] ? v + 8.f : mlim[nt][e];
+          const float ref = v == -INFINITY ? 0.f : v;
+          // the move; 0 from the first reference (nothing to rescale)
+          const float up = mlim[nt][e] == -INFINITY ? 0.f : ref - mref[nt][e];
+          mlim[nt][e] = v;
+          mref[nt][e] = ref;
+          l[nt][e] *= exp2f(-up);
+          // F rises by the next power of two, as far as its range goes, and O grows by
+          // what that is above the move
+          const int ef = __float_as_uint(F[nt][e]) >> 23;
+          const int to = min(ef + (int)ceilf(fminf(up, 512.f)), kTopFExp);
+          F[nt][e] = __uint_as_float((uint32_t)to << 23);
+          const float k = exp2f((float)(to - ef) - up);
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            acc[nt][c][e] *= k;
+            acc[nt][c][e + 2] *= k;
+          }
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+#pragma unroll
+        for (int e = 0; e < 4; e += ES) x[nt][b][e] = fast_exp2(x[nt][b][e] - mref[nt][e & 1]);
+        l[nt][0] += x[nt][b][0] + x[nt][b][2];
+        if (!ONE) l[nt][1] += x[nt][b][1] + x[nt][b][3];
+      }
+      // x becomes w = p s; P = w F.  When a w F exceeds 2^15, F falls to where the
+      // largest of them is 2^5
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; e += ES) x[nt][b][e] *= sv[b];
+      if (edge) {  // the scale of a block that no page holds may be anything
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; e += ES)
+            if ((hidden >> (4 * (nt * NB + b) + e)) & 1u) x[nt][b][e] = 0.f;
+      }
+      bool grow = false;
+      float wt[2];
+#pragma unroll
+      for (int e = 0; e < 2; e += ES) {
+        wt[e] = fmaxf(fmaxf(x[nt][0][e], x[nt][0][e + 2]), fmaxf(x[nt][1][e], x[nt][1][e + 2]));
+        grow |= wt[e] * F[nt][e] > 32768.f;
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int e = 0; e < 2; e += ES) {
+          float v = wt[e];
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+          // 2^(5 - exponent of v), from its bits; v is 0 or positive, infinite at most
+          const int ex = __float_as_uint(fmaxf(v, 0.f)) >> 23;
+          const float to = __uint_as_float((uint32_t)min(259 - ex, kTopFExp) << 23);
+          if (to < F[nt][e]) {
+            const float f = to / F[nt][e];
+            F[nt][e] = to;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+              acc[nt][c][e] *= f;
+              acc[nt][c][e + 2] *= f;
+            }
+          }
+        }
+      }
+      if (any_nan) {  // a visible V row of NaN makes all of O NaN
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; e += ES)
+            if (((nan[b] >> (16 + g + (e & 2) * 4)) & 1u) &&
+                !((hidden >> (4 * (nt * NB + b) + e)) & 1u))
+              x[nt][b][e] = __uint_as_float(0x7FC00000u);
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        pf[nt][b][0] = transpose8x8(
+            pack_f16x2(x[nt][b][0] * F[nt][0], ONE ? 0.f : x[nt][b][1] * F[nt][1]));
+        pf[nt][b][1] = transpose8x8(
+            pack_f16x2(x[nt][b][2] * F[nt][0], ONE ? 0.f : x[nt][b][3] * F[nt][1]));
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int cc = 0; cc < CH / 2; ++cc) {
+        uint32_t w[4];  // tokens 2 t, 2 t + 1 of each half, features 2 g, 2 g + 1 of two chunks
+        ldmatrix4_trans(at(s + b * BYTES + kKv8Tok * D, cc), w);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // (token, token') of the first feature in the low half, of the second in the high
+          const uint32_t u0 = __byte_perm(w[2 * h], 0, 0x3120);
+          const uint32_t u1 = __byte_perm(w[2 * h + 1], 0, 0x3120);
+          const uint32_t a0 = e4m3_to_f16((uint16_t)u0), a1 = e4m3_to_f16((uint16_t)(u0 >> 16));
+          const uint32_t a2 = e4m3_to_f16((uint16_t)u1), a3 = e4m3_to_f16((uint16_t)(u1 >> 16));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_f16(acc[nt][2 * cc + h], a0, a1, a2, a3, pf[nt][b][0], pf[nt][b][1]);
+        }
+      }
+  }
+
+  // Sums over the warp's lanes; put(column, feature, two features' O, lim, ref, l).
+  template <typename Put>
+  __device__ __forceinline__ void finish(int ncolv, Put put) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 4);
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
+        const int cc = 8 * nt + 2 * t + e;
+        const float f = 1.f / F[nt][e];
+        if (cc < ncolv)
+#pragma unroll
+          for (int c = 0; c < CH; ++c)
+            put(cc, 16 * c + 2 * g, make_float2(acc[nt][c][e] * f, acc[nt][c][e + 2] * f),
+                mlim[nt][e], mref[nt][e], l[nt][e]);
+      }
+  }
+};
+
+template <int D, int NT>
+struct Smem {
+  alignas(128) uint8_t blocks[kWarps][NB][kv8_block_bytes(D)];
+  float part[kWarps][8 * NT * (D + 2)];
+  uint2 q[NT > 1 ? kWarps : 1][NT > 1 ? NT * (D / 16) * 32 : 1];
+};
+
+// A CTA per sequence, head and column block; each warp takes every fourth pair of blocks.
+template <int D, int NT, bool ONE>
+__global__ void __launch_bounds__(kThreads) attn_kv8_kernel(const Kv8AttnParams p) {
+  constexpr int COLS = 8 * NT, BYTES = kv8_block_bytes(D);
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  Smem<D, NT>& sm = *reinterpret_cast<Smem<D, NT>*>(smem_raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cb = blockIdx.x % p.ncb, rest = blockIdx.x / p.ncb;
+  const int hk = rest % p.Hkv, b = rest / p.Hkv;
+  const int raw = __ldg(p.lens + b), len = seq_len(p, b);
+  if (raw != len && tid == 0) atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
+  int b0, n;
+  unit_blocks<COLS>(p, len, cb, b0, n);
+  const int c_first = cb * COLS, ncolv = min(COLS, p.ncols - c_first);
+  const int64_t cap = (int64_t)p.table_w * p.page;
+  float* scores = p.scores ? p.scores + ((int64_t)b * p.Hkv + hk) * p.ncols * cap : nullptr;
+  Attend<D, NT, ONE> a;
+  a.init(lane, sm.q[NT > 1 ? warp : 0]);
+  a.load_q(p, b, hk, c_first);
+  for (int r = warp * NB; r < n; r += kWarps * NB) {
+    uint32_t gone = 0, past = 0;
+    for (int k = 0; k < NB; ++k) {
+      const int blk = b0 + r + k, pi = blk / p.blocks_per_page;
+      uint4* to = reinterpret_cast<uint4*>(sm.blocks[warp][k]);
+      const uint4* from = nullptr;
+      if (r + k >= n) {
+        past |= 1u << k;
+      } else {
+        const int id = __ldg(p.table + (int64_t)b * p.table_w + pi);
+        if (id >= 0 && id < p.n_pages)
+          from = reinterpret_cast<const uint4*>(
+              p.cache +
+              kv8_block_of(id, blk - pi * p.blocks_per_page, hk, p.Hkv, p.blocks_per_page, D));
+        else if (lane == 0)
+          atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
+      }
+      if (from == nullptr) gone |= 1u << k;
+      for (int i = lane; i < BYTES / 16; i += 32) to[i] = from ? __ldg(from + i) : make_uint4(0, 0, 0, 0);
+    }
+    __syncwarp();
+    a.step(p, smem_u32(sm.blocks[warp][0]), (b0 + r) * kKv8Tok, true, gone, past, len, c_first,
+           scores, cap);
+    __syncwarp();
+  }
+  float* part = sm.part[warp];
+  a.finish(ncolv, [&](int cc, int f, float2 o, float lim, float, float l) {
+    *reinterpret_cast<float2*>(part + cc * D + f) = o;
+    if (f == 0) {
+      part[COLS * D + cc] = lim;
+      part[COLS * D + COLS + cc] = l;
+    }
+  });
+  __syncthreads();
+  const int span[3] = {b, hk, cb};
+  for (int i = tid; i < ncolv * (D / 4); i += kThreads) {
+    const int cc = i / (D / 4), f = (i - cc * (D / 4)) * 4;
+    Joined j;
+    j.clear();
+    for (int w = 0; w < kWarps; ++w) {
+      const float* pp = sm.part[w];
+      j.add(pp[COLS * D + cc], pp[COLS * D + COLS + cc],
+            *reinterpret_cast<const float4*>(pp + cc * D + f));
+    }
+    j.write(p, span, c_first + cc, f);
+  }
+}
+
+struct WeighParams {
+  KvAttnParams a;
+  const float *scores, *weights;
+  float* out;
+  int64_t cap;
+  int chunks;  // CTAs of a head
+};
+
+// out[b, h, j] = weights[b, h, j] + the sum over columns of exp(score - lse), a thread per key.
+__global__ void __launch_bounds__(256) kv8_weigh_kernel(const WeighParams p) {
+  const int plane = blockIdx.x / p.chunks, b = plane / p.a.Hkv, hk = plane - b * p.a.Hkv;
+  const int64_t j64 = (int64_t)(blockIdx.x - plane * p.chunks) * 256 + threadIdx.x;
+  if (j64 >= p.cap) return;
+  const int j = (int)j64, len = seq_len(p.a, b);
+  const int64_t at = plane * p.cap + j;
+  if (j >= len && p.weights == p.out) return;
+  float sum = 0.f;
+  for (int col = 0; j < len && col < p.a.ncols; ++col) {
+    int lo, hi;
+    col_range(p.a, len, col, lo, hi);
+    if (j < lo || j >= hi) continue;
+    const int qi = token_of(p.a, col), qh = hk * p.a.G + (col - qi * p.a.G);
+    const float x = __ldcg(p.scores + (plane * (int64_t)p.a.ncols + col) * p.cap + j);
+    const float lse = __ldg(p.a.lse + ((int64_t)b * p.a.Hq + qh) * p.a.Nq + qi);
+    if (x != -INFINITY) sum += exp2f(x - lse * 1.4426950408889634f);
+  }
+  p.out[at] = p.weights[at] + sum;
+}
+
+template <int D, int NT, bool ONE>
+iha_status launch_nt(const Kv8AttnParams& p, cudaStream_t s) {
+  static SmemLimit limit;
+  const cudaError_t e = limit.ensure(attn_kv8_kernel<D, NT, ONE>, (int)sizeof(Smem<D, NT>));
+  if (e != cudaSuccess)
+    return fail(IHA_ERR_CUDA, "mha_fwd_kv8 (smem attribute): %s", cudaGetErrorString(e));
+  attn_kv8_kernel<D, NT, ONE>
+      <<<(unsigned)((int64_t)p.B * p.Hkv * p.ncb), kThreads, sizeof(Smem<D, NT>), s>>>(p);
+  return check_launch("mha_fwd_kv8");
+}
+template <int D>
+iha_status launch(const Kv8AttnParams& p, int nt, cudaStream_t s) {
+  if (p.ncols == 1) return launch_nt<D, 1, true>(p, s);
+  return nt == 1 ? launch_nt<D, 1, false>(p, s) : launch_nt<D, 2, false>(p, s);
+}
+
+size_t part_bytes(int64_t ncols, int d) {
+  const int ctas = kMaxCtas * ctas_per_sm(pick_nt(ncols)) / ctas_per_sm(1);
+  return (size_t)ctas * kCtaParts * part_stride(ncols, d) * sizeof(float);
+}
+
+constexpr int kMaxWeighed = 64;  // columns whose scores a call with weights keeps
+
+}  // namespace
+}  // namespace iha
+
+extern "C" {
+
+size_t mha_fwd_kv8_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, int weight_keys) {
+  if (B <= 0 || Nq <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv || d <= 0 || weight_keys < 0) return 0;
+  const int64_t ncols = (int64_t)Nq * (Hq / Hkv);
+  size_t n = iha::kCounterBytes + iha::part_bytes(ncols, d);
+  if (weight_keys > 0)  // the rows' lse, their scores
+    n += ((size_t)B * Hq * Nq + (size_t)B * Hkv * ncols * weight_keys) * sizeof(float);
+  return n;
+}
+
+iha_status mha_fwd_kv8(const void* q, const void* cache, const int32_t* block_table,
+                       const int32_t* seq_lens, void* o, float* lse_out, const float* weights,
+                       float* weights_out, void* workspace, size_t workspace_bytes, int B, int Nq,
+                       int Hq, int Hkv, int d, int n_pages, int page, int table_width,
+                       iha_strides sq, iha_strides so, float scale, iha_mask mask_mode, int window,
+                       iha_dtype dt, void* stream) {
+  using namespace iha;
+  const char* name = "mha_fwd_kv8";
+  const int64_t cap = (int64_t)table_width * page;
+  if ((weights == nullptr) != (weights_out == nullptr))
+    return fail(IHA_ERR_INVALID_ARG, "%s: weights and weights_out go together", name);
+  const int keys = weights && cap > 0 && cap <= (1 << 30) ? (int)cap : 0;
+  Kv8AttnParams p;
+  int nt, grid;
+  iha_status st = kv_attn_setup(
+      name, p, nt, grid, kv8_check_cache, kv8_page_bytes(page, Hkv, d),
+      mha_fwd_kv8_workspace_bytes(B, Nq, Hq, Hkv, d, keys), q, cache, block_table, seq_lens, o,
+      lse_out, workspace, workspace_bytes, B, Nq, Hq, Hkv, d, n_pages, page, table_width, sq, so,
+      scale, mask_mode, window, dt);
+  if (st != IHA_OK) return st;
+  p.scores = nullptr;
+  if (weights) {
+    if (p.ncols > kMaxWeighed)
+      return fail(IHA_ERR_UNSUPPORTED, "%s: weights of more than %d rows of a key head", name,
+                  kMaxWeighed);
+    if ((reinterpret_cast<uintptr_t>(weights) | reinterpret_cast<uintptr_t>(weights_out)) & 3)
+      return fail(IHA_ERR_ALIGNMENT, "%s: weights must be 4-byte aligned", name);
+    bool neg;
+    auto span_of = [&](const iha_strides& t) { return view_bytes(t, B, 1, Nq, Hq, d, 2, &neg); };
+    const int64_t nw = (int64_t)B * Hkv * cap * 4, no = span_of(p.so);
+    if ((int64_t)B * Hkv * ((cap + 255) / 256) > INT32_MAX)
+      return fail(IHA_ERR_UNSUPPORTED, "%s: too many weights for one launch", name);
+    if ((weights != weights_out && overlaps(weights, nw, weights_out, nw)) ||
+        overlaps(weights_out, nw, q, span_of(p.sq)) ||
+        overlaps(weights_out, nw, cache, (int64_t)n_pages * (int64_t)kv8_page_bytes(page, Hkv, d)) ||
+        overlaps(weights_out, nw, block_table, (int64_t)B * table_width * 4) ||
+        overlaps(weights_out, nw, seq_lens, (int64_t)B * 4) ||
+        overlaps(weights_out, nw, workspace, (int64_t)workspace_bytes) ||
+        overlaps(weights, nw, workspace, (int64_t)workspace_bytes) ||
+        overlaps(weights_out, nw, o, no) || overlaps(weights, nw, o, no) ||
+        (lse_out && (overlaps(weights_out, nw, lse_out, (int64_t)B * Hq * Nq * 4) ||
+                     overlaps(weights, nw, lse_out, (int64_t)B * Hq * Nq * 4))))
+      return fail(IHA_ERR_INVALID_ARG, "%s: weights overlap another tensor", name);
+    float* own = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterBytes +
+                                          part_bytes(p.ncols, d));
+    if (!p.lse) p.lse = own;
+    p.scores = own + (int64_t)B * Hq * Nq;
+  }
+  p.wait_ns = wait_limit_for_next_launch();
+  p.withhold = withhold_for_this_launch() ? 1 : 0;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  IHA_KV8_D_SWITCH(d, st = launch<kD>(p, nt, s))
+  if (st != IHA_OK || !weights) return st;
+  const WeighParams w = {p, p.scores, weights, weights_out, cap, (int)((cap + 255) / 256)};
+  kv8_weigh_kernel<<<(unsigned)(B * Hkv * w.chunks), 256, 0, s>>>(w);
+  return check_launch(name);
+}
+
+}  // extern "C"

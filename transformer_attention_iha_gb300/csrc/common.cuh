@@ -26,6 +26,11 @@ iha_status fail(iha_status s, const char* fmt, ...);
 iha_status check_launch(const char* what);
 // 16-byte alignment of a device pointer.
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Do two byte ranges share a byte?
+inline bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
 // SM count of the current device (cached per device).
 int sm_count();
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no -lcuda).
@@ -105,6 +110,20 @@ class SmemLimit {
 
 // ---------------------------------------------------------------- device side
 #if defined(__CUDACC__)
+
+// n / d for 0 <= n < 2^31 by multiplication: inv = ceil(2^64 / d) is too large
+// by less than d / 2^64 of itself, so the product by less than 1 / d.
+struct FastDiv {
+  uint64_t inv;
+  int d;
+  __host__ void set(int x) {
+    d = x;
+    inv = x > 1 ? ~0ull / (unsigned)x + 1 : 0;
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return d == 1 ? n : (int)__umul64hi((uint64_t)(unsigned)n, inv);
+  }
+};
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

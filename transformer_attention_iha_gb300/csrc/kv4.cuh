@@ -80,6 +80,20 @@ struct Kv4View {
 };
 bool kv4_views_meet(const Kv4View& a, const Kv4View& b, int64_t delta, int d, bool self);
 
+// Byte strides of a view are multiples of 16.
+inline bool strides_ok(const iha_strides& s, int es) {
+  const int64_t m = 16 / es;
+  return s.b_outer % m == 0 && s.b_inner % m == 0 && s.seq % m == 0 && s.head % m == 0;
+}
+
+// Bytes from the first to one past the last element of a strided view.
+inline int64_t view_bytes(const iha_strides& s, int Bo, int Bi, int N, int H, int d, int es, bool* neg) {
+  *neg = s.b_outer < 0 || s.b_inner < 0 || s.seq < 0 || s.head < 0;
+  return ((int64_t)(Bo - 1) * s.b_outer + (int64_t)(Bi - 1) * s.b_inner +
+          (int64_t)(N - 1) * s.seq + (int64_t)(H - 1) * s.head + d) *
+         es;
+}
+
 // Host checks shared by the cache's entry points.
 iha_status kv4_check_cache(const char* name, const void* cache, int n_pages, int page, int Hkv,
                            int d);

@@ -38,20 +38,6 @@ namespace {
 
 IHA_DEVICE_ERROR_WORD(kv4_cache)
 
-// n / d for 0 <= n < 2^31 by multiplication: inv = ceil(2^64 / d) is too large
-// by less than d / 2^64 of itself, so the product by less than 1 / d.
-struct FastDiv {
-  uint64_t inv;
-  int d;
-  __host__ void set(int x) {
-    d = x;
-    inv = x > 1 ? ~0ull / (unsigned)x + 1 : 0;
-  }
-  __device__ __forceinline__ int div(int n) const {
-    return d == 1 ? n : (int)__umul64hi((uint64_t)(unsigned)n, inv);
-  }
-};
-
 struct Kv4Geom {
   FastDiv N, Bi, page, units;  // tokens of a batch row; inner batch; page; head units of a warp
   int toks, H, n_units, blocks_per_page;
@@ -287,19 +273,6 @@ __global__ void __launch_bounds__(256)
   for (int j = 0; j < NG; ++j) write_v(pv + 32 * j + 4 * i, vh[j], vs[j]);
 }
 
-bool strides_ok(const iha_strides& s, int es) {
-  const int64_t m = 16 / es;
-  return s.b_outer % m == 0 && s.b_inner % m == 0 && s.seq % m == 0 && s.head % m == 0;
-}
-
-// Bytes from the first to one past the last element of a strided view.
-int64_t view_bytes(const iha_strides& s, int Bo, int Bi, int N, int H, int d, int es, bool* neg) {
-  *neg = s.b_outer < 0 || s.b_inner < 0 || s.seq < 0 || s.head < 0;
-  return ((int64_t)(Bo - 1) * s.b_outer + (int64_t)(Bi - 1) * s.b_inner +
-          (int64_t)(N - 1) * s.seq + (int64_t)(H - 1) * s.head + d) *
-         es;
-}
-
 // Coefficients lo .. hi of a stride; the least and the most that this one and the
 // smaller ones reach.
 struct Step {
@@ -320,11 +293,6 @@ bool reaches(const Step* t, int n, int64_t at, int d, int& budget) {
   for (int64_t c = c0; c <= c1; ++c)
     if (reaches(t + 1, n - 1, at + c * t->s, d, budget)) return true;
   return false;
-}
-
-bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
 }
 
 #define IHA_NG_SWITCH(NG, ...)                                  \

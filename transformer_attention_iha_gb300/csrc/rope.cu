@@ -1,0 +1,343 @@
+// Rotary positions of query and key rows (iha_rope_fwd) and of their gradients
+// (iha_rope_bwd).
+//
+//   (y_a, y_b) = gain (x_a cos - x_b sin, x_b cos + x_a sin),  angle = position w_i
+//
+// for pair i of the first rot features: (i, i + rot / 2) or (2 i, 2 i + 1); the other
+// features are copied.  The backward pass turns the other way.
+//
+// Angles: a pair's frequency is held as turns per position in 64-bit fixed point,
+// turn = w / 2 pi * 2^64 mod 2^64, so position * turn in 64-bit integers is the angle
+// in turns modulo 1 for any position, without the loss of a 32-bit product (position
+// 2^20 in fp32 is off by 2^-4 radians).  Its upper 32 bits, as a signed number, go
+// through sincospif: off by about 2^-24 in all.
+//
+// A thread takes 32 bytes of a row, 8 pairs of bf16 or 4 of fp32, works out their
+// sines once and applies them to up to `hg` heads of its token.
+#include <math.h>
+
+#include "kv4.cuh"
+
+namespace iha {
+namespace {
+
+constexpr int kMaxPairs = 128;
+constexpr int kRopeThreads = 256;
+
+struct RopeParams {
+  const void *q, *k;
+  void *yq, *yk;
+  const int32_t* pos;  // null: the place in the sequence
+  iha_strides sq, sk, tq, tk;
+  FastDiv units, groups, N;  // units of a row, groups of heads of a token, tokens of a sequence
+  int items;                 // tokens * groups * units
+  int turning;               // units that turn; the rest copy
+  int Hq, H, hg;             // heads of q, of both, of a group
+  int rot;
+  float gain, sign;
+  uint64_t turn[kMaxPairs];
+};
+
+template <typename T>
+__device__ __forceinline__ void unpack(uint4 v, float (&f)[16 / sizeof(T)]);
+template <>
+__device__ __forceinline__ void unpack<__nv_bfloat16>(uint4 v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16lo_to_f32(w[i]);
+    f[2 * i + 1] = bf16hi_to_f32(w[i]);
+  }
+}
+template <>
+__device__ __forceinline__ void unpack<float>(uint4 v, float (&f)[4]) {
+  f[0] = __uint_as_float(v.x);
+  f[1] = __uint_as_float(v.y);
+  f[2] = __uint_as_float(v.z);
+  f[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ uint4 repack(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+__device__ __forceinline__ uint4 repack(const float (&f)[4]) {
+  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                    __float_as_uint(f[3]));
+}
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void narrow(float* p, float x) { *p = x; }
+__device__ __forceinline__ void narrow(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// VEC: 16-byte vectors; else a thread takes one pair, or one feature to copy.
+template <typename T, bool INTER, bool VEC>
+__global__ void __launch_bounds__(kRopeThreads)
+    rope_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int V = 16 / sizeof(T);      // features of a vector
+  constexpr int PAIRS = VEC ? V : 1;     // pairs of a thread
+  __shared__ uint64_t turn[kMaxPairs];
+  for (int i = threadIdx.x; i < p.rot / 2; i += kRopeThreads) turn[i] = p.turn[i];
+  __syncthreads();
+  const int id = blockIdx.x * kRopeThreads + threadIdx.x;
+  if (id >= p.items) return;
+  const int rest = p.units.div(id), u = id - rest * p.units.d;
+  const int tok = p.groups.div(rest), head0 = (rest - tok * p.groups.d) * p.hg;
+  const int b = p.N.div(tok), n = tok - b * p.N.d;
+  const int head1 = min(head0 + p.hg, p.H);
+  const bool turns = u < p.turning;
+  // the thread's two vectors (or features) in a row
+  int at0, at1;
+  if (!turns) {
+    at0 = at1 = p.rot + (u - p.turning) * (VEC ? V : 1);
+  } else if (INTER) {
+    at0 = u * 2 * PAIRS;
+    at1 = at0 + PAIRS;
+  } else {
+    at0 = u * PAIRS;
+    at1 = p.rot / 2 + at0;
+  }
+  float cs[PAIRS], sn[PAIRS];
+  if (turns) {
+    const int64_t pos = p.pos ? __ldg(p.pos + tok) : n;
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+      const int32_t part = (int32_t)(((uint64_t)pos * turn[u * PAIRS + i]) >> 32);
+      sincospif((float)part * 4.656612873077393e-10f, &sn[i], &cs[i]);  // 2^-31
+      cs[i] *= p.gain;
+      sn[i] *= p.sign;
+    }
+  }
+  const T* q = static_cast<const T*>(p.q) + b * p.sq.b_outer + n * p.sq.seq;
+  const T* k = static_cast<const T*>(p.k) + (p.k ? b * p.sk.b_outer + n * p.sk.seq : 0);
+  T* yq = static_cast<T*>(p.yq) + b * p.tq.b_outer + n * p.tq.seq;
+  T* yk = static_cast<T*>(p.yk) + (p.k ? b * p.tk.b_outer + n * p.tk.seq : 0);
+#pragma unroll 4
+  for (int h = head0; h < head1; ++h) {
+    const bool isq = h < p.Hq;
+    const T* x = isq ? q + h * p.sq.head : k + (h - p.Hq) * p.sk.head;
+    T* y = isq ? yq + h * p.tq.head : yk + (h - p.Hq) * p.tk.head;
+    if constexpr (VEC) {
+      const uint4 v0 = *reinterpret_cast<const uint4*>(x + at0);
+      if (!turns) {
+        *reinterpret_cast<uint4*>(y + at0) = v0;
+        continue;
+      }
+      const uint4 v1 = *reinterpret_cast<const uint4*>(x + at1);
+      float f[2][V], g[2][V];
+      unpack<T>(v0, f[0]);
+      unpack<T>(v1, f[1]);
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i) {
+        // element i of a pair list: (vector, place) of its two features
+        const int va = INTER ? 2 * i / V : 0, ia = INTER ? 2 * i % V : i;
+        const int vb = INTER ? va : 1, ib = INTER ? ia + 1 : i;
+        const float a = f[va][ia], c = f[vb][ib];
+        g[va][ia] = a * cs[i] - c * sn[i];
+        g[vb][ib] = c * cs[i] + a * sn[i];
+      }
+      *reinterpret_cast<uint4*>(y + at0) = repack(g[0]);
+      *reinterpret_cast<uint4*>(y + at1) = repack(g[1]);
+    } else {
+      if (!turns) {
+        y[at0] = x[at0];
+        continue;
+      }
+      const float a = widen(x[at0]), c = widen(x[at1]);
+      narrow(y + at0, a * cs[0] - c * sn[0]);
+      narrow(y + at1, c * cs[0] + a * sn[0]);
+    }
+  }
+}
+
+template <typename T, bool INTER>
+void launch(const RopeParams& p, bool vec, unsigned blocks, cudaStream_t s) {
+  if (vec)
+    rope_kernel<T, INTER, true><<<blocks, kRopeThreads, 0, s>>>(p);
+  else
+    rope_kernel<T, INTER, false><<<blocks, kRopeThreads, 0, s>>>(p);
+}
+
+iha_status rotate(const char* name, bool back, const void* q, const void* k,
+                  const int32_t* positions, void* yq, void* yk, const iha_rope* rope, int B, int N,
+                  int Hq, int Hk, int d, iha_strides sq, iha_strides sk, iha_strides tq,
+                  iha_strides tk, iha_dtype dt, void* stream) {
+  if (!q || !yq || !rope) return fail(IHA_ERR_INVALID_ARG, "%s: null pointer", name);
+  if ((k == nullptr) != (yk == nullptr) || (k == nullptr) != (Hk == 0))
+    return fail(IHA_ERR_INVALID_ARG, "%s: k, its output and Hk > 0 go together", name);
+  if (B <= 0 || N <= 0 || Hq <= 0 || Hk < 0 || d <= 0)
+    return fail(IHA_ERR_INVALID_ARG, "%s: sizes must be positive", name);
+  if (dt != IHA_BF16 && dt != IHA_F32) return fail(IHA_ERR_INVALID_ARG, "%s: bad dtype", name);
+  if (rope->rot < 2 || rope->rot > 2 * kMaxPairs || (rope->rot & 1) || !(rope->mul > 0.f))
+    return fail(IHA_ERR_INVALID_ARG, "%s: rope is not as iha_rope_init leaves it", name);
+  if (rope->rot > d)
+    return fail(IHA_ERR_INVALID_ARG, "%s: %d rotated features of %d", name, rope->rot, d);
+  const int es = dt == IHA_BF16 ? 2 : 4, V = 16 / es;
+  if (d % V)
+    return fail(IHA_ERR_UNSUPPORTED, "%s: d %d is not a multiple of %d", name, d, V);
+  for (iha_strides* t : {&sq, &tq, &sk, &tk}) {  // the stride of an extent of 1 is never used
+    const bool isq = t == &sq || t == &tq;
+    if (B == 1) t->b_outer = 0;
+    if (N == 1) t->seq = 0;
+    if ((isq ? Hq : Hk) <= 1) t->head = 0;
+    if (!isq && Hk == 0) *t = iha_strides{0, 0, 0, 0};
+    if (t->b_outer < 0 || t->seq < 0 || t->head < 0)
+      return fail(IHA_ERR_INVALID_ARG, "%s: negative stride", name);
+    if (t->b_outer % V || t->seq % V || t->head % V)
+      return fail(IHA_ERR_ALIGNMENT, "%s: strides must be multiples of 16 bytes", name);
+  }
+  if (!aligned16(q) || !aligned16(yq) || !aligned16(k) || !aligned16(yk))
+    return fail(IHA_ERR_ALIGNMENT, "%s: tensors must be 16-byte aligned", name);
+  if (reinterpret_cast<uintptr_t>(positions) & 3)
+    return fail(IHA_ERR_ALIGNMENT, "%s: positions must be 4-byte aligned", name);
+  const int64_t toks = (int64_t)B * N;
+  if (toks > (1 << 30))
+    return fail(IHA_ERR_UNSUPPORTED, "%s: more than 2^30 tokens in one call", name);
+
+  // outputs: rows apart from one another, from the other output and from the inputs,
+  // but for a tensor turned in place
+  struct Tensor {
+    const void* p;
+    int H;
+    iha_strides s;
+  };
+  const Tensor in[2] = {{q, Hq, sq}, {k, Hk, sk}}, out[2] = {{yq, Hq, tq}, {yk, Hk, tk}};
+  const int nt = k ? 2 : 1;
+  auto view = [&](const Tensor& t) {
+    return Kv4View{3, {B, N, t.H}, {t.s.b_outer, t.s.seq, t.s.head}};
+  };
+  auto bytes = [&](const Tensor& t) {
+    return ((int64_t)(B - 1) * t.s.b_outer + (int64_t)(N - 1) * t.s.seq +
+            (int64_t)(t.H - 1) * t.s.head + d) * es;
+  };
+  auto meet = [&](const Tensor& a, const Tensor& b) {
+    if (!overlaps(a.p, bytes(a), b.p, bytes(b))) return false;
+    const int64_t apart = static_cast<const char*>(b.p) - static_cast<const char*>(a.p);
+    return kv4_views_meet(view(a), view(b), apart / es, d, false);
+  };
+  for (int i = 0; i < nt; ++i) {
+    const Tensor& o = out[i];
+    if ((B > 1 && o.s.b_outer == 0) || (N > 1 && o.s.seq == 0) || (o.H > 1 && o.s.head == 0) ||
+        kv4_views_meet(view(o), view(o), 0, d, true))
+      return fail(IHA_ERR_INVALID_ARG, "%s: rows of an output overlap one another", name);
+    if (positions && overlaps(o.p, bytes(o), positions, toks * 4))
+      return fail(IHA_ERR_INVALID_ARG, "%s: an output overlaps positions", name);
+    for (int j = 0; j < nt; ++j) {
+      const bool in_place = i == j && o.p == in[j].p && o.s.b_outer == in[j].s.b_outer &&
+                            o.s.seq == in[j].s.seq && o.s.head == in[j].s.head;
+      if (!in_place && meet(o, in[j]))
+        return fail(IHA_ERR_INVALID_ARG, "%s: an output overlaps an input it is not in place of",
+                    name);
+    }
+  }
+  if (nt == 2 && meet(out[0], out[1]))
+    return fail(IHA_ERR_INVALID_ARG, "%s: the outputs overlap one another", name);
+
+  RopeParams p;
+  p.q = q;
+  p.k = k;
+  p.yq = yq;
+  p.yk = yk;
+  p.pos = positions;
+  p.sq = sq;
+  p.sk = sk;
+  p.tq = tq;
+  p.tk = tk;
+  p.Hq = Hq;
+  p.H = Hq + Hk;
+  p.rot = rope->rot;
+  p.gain = rope->mul;
+  p.sign = back ? -rope->mul : rope->mul;
+  for (int i = 0; i < rope->rot / 2; ++i) p.turn[i] = rope->turn[i];
+  // vectors where both halves of a turn start on 16 bytes
+  const bool vec = rope->rot / 2 % V == 0;
+  p.turning = vec ? rope->rot / 2 / V : rope->rot / 2;
+  const int units = p.turning + (vec ? (d - rope->rot) / V : d - rope->rot);
+  p.hg = 1;
+  const int64_t items = toks * p.H * units;
+  if (items > (1 << 30))
+    return fail(IHA_ERR_UNSUPPORTED, "%s: too many rows in one call", name);
+  const int groups = (p.H + p.hg - 1) / p.hg;
+  p.units.set(units);
+  p.groups.set(groups);
+  p.N.set(N);
+  p.items = (int)(toks * groups * units);
+  const unsigned blocks = (unsigned)((p.items + kRopeThreads - 1) / kRopeThreads);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (dt == IHA_BF16) {
+    if (rope->interleaved)
+      launch<__nv_bfloat16, true>(p, vec, blocks, s);
+    else
+      launch<__nv_bfloat16, false>(p, vec, blocks, s);
+  } else {
+    if (rope->interleaved)
+      launch<float, true>(p, vec, blocks, s);
+    else
+      launch<float, false>(p, vec, blocks, s);
+  }
+  return check_launch(name);
+}
+
+}  // namespace
+}  // namespace iha
+
+extern "C" {
+
+iha_status iha_rope_init(iha_rope* r) {
+  using namespace iha;
+  const char* name = "iha_rope_init";
+  if (!r) return fail(IHA_ERR_INVALID_ARG, "%s: null pointer", name);
+  if (r->rot < 2 || (r->rot & 1))
+    return fail(IHA_ERR_INVALID_ARG, "%s: rot %d is not an even number above 0", name, r->rot);
+  if (r->rot > 2 * kMaxPairs)
+    return fail(IHA_ERR_UNSUPPORTED, "%s: more than %d rotated features", name, 2 * kMaxPairs);
+  if (r->interleaved != 0 && r->interleaved != 1)
+    return fail(IHA_ERR_INVALID_ARG, "%s: interleaved is 0 or 1", name);
+  if (!(r->base > 1.0) || !isfinite(r->base))
+    return fail(IHA_ERR_INVALID_ARG, "%s: base must be finite and above 1", name);
+  if (!(r->gain >= 0.0) || !(r->gain < 1e30))
+    return fail(IHA_ERR_INVALID_ARG, "%s: gain must be positive, or 0 for the usual one", name);
+  if (r->scaling < IHA_ROPE_NONE || r->scaling > IHA_ROPE_PARTS)
+    return fail(IHA_ERR_INVALID_ARG, "%s: bad scaling %d", name, r->scaling);
+  const double f = r->factor;
+  if (r->scaling != IHA_ROPE_NONE && (!(f >= 1.0) || !(f < 1e30)))
+    return fail(IHA_ERR_INVALID_ARG, "%s: factor must be at least 1", name);
+  if (r->scaling == IHA_ROPE_BASE && r->rot == 2)
+    return fail(IHA_ERR_INVALID_ARG, "%s: a scaled base needs rot > 2", name);
+  if (r->scaling == IHA_ROPE_PARTS &&
+      (r->trained < 1 || !(r->slow >= 0.0) || !(r->fast > r->slow) || !isfinite(r->fast)))
+    return fail(IHA_ERR_INVALID_ARG, "%s: parts needs trained >= 1 and 0 <= slow < fast", name);
+  const double two_pi = 6.283185307179586476925;
+  double base = r->base;
+  if (r->scaling == IHA_ROPE_BASE) base *= pow(f, r->rot / (r->rot - 2.0));
+  for (int i = 0; i < r->rot / 2; ++i) {
+    double turns = pow(base, -2.0 * i / r->rot) / two_pi;  // per position, below 1 / 6
+    if (r->scaling == IHA_ROPE_LINEAR) turns /= f;
+    if (r->scaling == IHA_ROPE_PARTS) {
+      const double g = fmin(1.0, fmax(0.0, (r->trained * turns - r->slow) / (r->fast - r->slow)));
+      turns *= g + (1.0 - g) / f;
+    }
+    r->turn[i] = (uint64_t)(turns * 18446744073709551616.0);
+  }
+  r->mul = (float)(r->gain > 0.0 ? r->gain
+                                 : r->scaling == IHA_ROPE_PARTS ? 0.1 * log(f) + 1.0 : 1.0);
+  if (!(r->mul > 0.f)) return fail(IHA_ERR_INVALID_ARG, "%s: gain is 0 in fp32", name);
+  return IHA_OK;
+}
+
+iha_status iha_rope_fwd(const void* q, const void* k, const int32_t* positions, void* yq, void* yk,
+                        const iha_rope* rope, int B, int N, int Hq, int Hk, int d, iha_strides sq,
+                        iha_strides sk, iha_strides syq, iha_strides syk, iha_dtype dt,
+                        void* stream) {
+  return iha::rotate("iha_rope_fwd", false, q, k, positions, yq, yk, rope, B, N, Hq, Hk, d, sq, sk,
+                     syq, syk, dt, stream);
+}
+
+iha_status iha_rope_bwd(const void* dyq, const void* dyk, const int32_t* positions, void* dq,
+                        void* dk, const iha_rope* rope, int B, int N, int Hq, int Hk, int d,
+                        iha_strides sdyq, iha_strides sdyk, iha_strides sdq, iha_strides sdk,
+                        iha_dtype dt, void* stream) {
+  return iha::rotate("iha_rope_bwd", true, dyq, dyk, positions, dq, dk, rope, B, N, Hq, Hk, d,
+                     sdyq, sdyk, sdq, sdk, dt, stream);
+}
+
+}  // extern "C"
