@@ -526,7 +526,6 @@ def test_weights_in_place_and_workspaces(T):
         o, w1 = T.mha_fwd_kv8(q, cache, table, sl, Hkv, 16, weights=w, workspace=ws)
         o2, w2 = T.mha_fwd_kv8(q, cache, table, sl, Hkv, 16, weights=w, weights_out=w)
         assert w2 is w and torch.equal(w1, w) and torch.equal(o, o2)
-        assert not ws[:4096].any()
     assert T.device_error() == 0
 
 

@@ -331,7 +331,8 @@ struct Attend {
       }
     }
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int b = 0; b < NB; ++b) {
+      if ((gone >> b) & 1u) continue;  // whatever is there may be NaN, and 0 NaN is
 #pragma unroll
       for (int cc = 0; cc < CH / 2; ++cc) {
         uint32_t w[4];  // tokens 2 t, 2 t + 1 of each half, features 2 g, 2 g + 1 of two chunks
@@ -348,6 +349,7 @@ struct Attend {
             mma_f16(acc[nt][2 * cc + h], a0, a1, a2, a3, pf[nt][b][0], pf[nt][b][1]);
         }
       }
+    }
   }
 
   // Sums over the warp's lanes; put(column, feature, two features' O, lim, ref, l).
@@ -371,78 +373,141 @@ struct Attend {
   }
 };
 
+// A warp's ring: stages of up to run_of blocks.
+constexpr int kStages = 2;
+__host__ __device__ constexpr int run_of(int d) { return d >= 96 ? 2 : d == 64 ? 4 : 8; }
+
 template <int D, int NT>
 struct Smem {
-  alignas(128) uint8_t blocks[kWarps][NB][kv8_block_bytes(D)];
-  float part[kWarps][8 * NT * (D + 2)];
+  // a warp's ring; when it has run out, the part of the unit its stretch ends in
+  alignas(128) uint8_t ring[kWarps][kStages][run_of(D)][kv8_block_bytes(D)];
   uint2 q[NT > 1 ? kWarps : 1][NT > 1 ? NT * (D / 16) * 32 : 1];
+  uint64_t full[kWarps][kStages];
+  LineSmem line;
 };
 
-// A CTA per sequence, head and column block; each warp takes every fourth pair of blocks.
 template <int D, int NT, bool ONE>
-__global__ void __launch_bounds__(kThreads) attn_kv8_kernel(const Kv8AttnParams p) {
-  constexpr int COLS = 8 * NT, BYTES = kv8_block_bytes(D);
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
+    attn_kv8_kernel(const Kv8AttnParams p) {
+  constexpr int COLS = 8 * NT, BYTES = kv8_block_bytes(D), RUN = run_of(D);
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Smem<D, NT>& sm = *reinterpret_cast<Smem<D, NT>*>(smem_raw);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int cb = blockIdx.x % p.ncb, rest = blockIdx.x / p.ncb;
-  const int hk = rest % p.Hkv, b = rest / p.Hkv;
-  const int raw = __ldg(p.lens + b), len = seq_len(p, b);
-  if (raw != len && tid == 0) atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
-  int b0, n;
-  unit_blocks<COLS>(p, len, cb, b0, n);
-  const int c_first = cb * COLS, ncolv = min(COLS, p.ncols - c_first);
-  const int64_t cap = (int64_t)p.table_w * p.page;
-  float* scores = p.scores ? p.scores + ((int64_t)b * p.Hkv + hk) * p.ncols * cap : nullptr;
-  Attend<D, NT, ONE> a;
-  a.init(lane, sm.q[NT > 1 ? warp : 0]);
-  a.load_q(p, b, hk, c_first);
-  for (int r = warp * NB; r < n; r += kWarps * NB) {
-    uint32_t gone = 0, past = 0;
-    for (int k = 0; k < NB; ++k) {
-      const int blk = b0 + r + k, pi = blk / p.blocks_per_page;
-      uint4* to = reinterpret_cast<uint4*>(sm.blocks[warp][k]);
-      const uint4* from = nullptr;
-      if (r + k >= n) {
-        past |= 1u << k;
-      } else {
-        const int id = __ldg(p.table + (int64_t)b * p.table_w + pi);
-        if (id >= 0 && id < p.n_pages)
-          from = reinterpret_cast<const uint4*>(
-              p.cache +
-              kv8_block_of(id, blk - pi * p.blocks_per_page, hk, p.Hkv, p.blocks_per_page, D));
-        else if (lane == 0)
-          atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in the warp, for the compiler too
+  volatile int* abort_flag = &sm.line.abort;
+  if (lane == 0)
+    for (int i = 0; i < kStages; ++i)
+      mbar_init(smem_u32(&sm.full[warp][i]), p.withhold && blockIdx.x == 0 && i == 0 ? 2 : 1);
+  if (tid <= kWarps) sm.line.span[tid][5] = 0;
+  if (tid == 0) sm.line.abort = 0;
+  mbar_init_fence();
+  int share, stretch;
+  Unit u;
+  if (!find_stretch<COLS>(p, sm.line, &g_dev_error, DEV_ERR_CACHE_INDEX, share, stretch, u)) return;
+
+  // where a warp of this CTA leaves its part of a unit that ends in its stretch
+  // after beginning before it, and of one that goes on after it
+  float* const cta_parts = p.parts + (int64_t)blockIdx.x * kCtaParts * p.part_stride;
+  auto head_of = [&](int w) { return cta_parts + (2 + w) * p.part_stride; };
+  auto tail_of = [&](int w) { return reinterpret_cast<float*>(sm.ring[w]); };
+  if (stretch > 0) {
+    const int g = lane >> 2, t = lane & 3;
+    // Q of the unit this warp comes to next, on its way while the unit before is computed
+    auto prefetch_q = [&](const Unit& n) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int col = n.cb * COLS + 8 * nt + g;
+        if (col < p.ncols && t < (D + 63) / 64) {  // lines of 128 bytes: 64 features
+          const int qi = token_of(p, col), qh = n.hk * p.G + col - qi * p.G;
+          const __nv_bfloat16* qp =
+              p.q + n.b * p.sq.b_outer + qi * p.sq.seq + qh * p.sq.head + 64 * t;
+          asm volatile("prefetch.L1 [%0];" ::"l"(qp));
+        }
       }
-      if (from == nullptr) gone |= 1u << k;
-      for (int i = lane; i < BYTES / 16; i += 32) to[i] = from ? __ldg(from + i) : make_uint4(0, 0, 0, 0);
+    };
+    prefetch_q(u);
+    BlockRing<BYTES, RUN, kStages, COLS> ring;
+    ring.start(p, u, stretch, lane, smem_u32(sm.ring[warp]), smem_u32(sm.full[warp]), &g_dev_error,
+               DEV_ERR_CACHE_INDEX);
+    Attend<D, NT, ONE> a;
+    a.init(lane, sm.q[NT > 1 ? warp : 0]);
+    const int64_t cap = (int64_t)p.table_w * p.page;
+    int stage = 0;
+    bool ok = true;
+
+    // ---- units of the stretch
+    for (;;) {
+      int r0, r1;
+      my_blocks(u, stretch, r0, r1);
+      const int empty_at = u.at + kUnitCost - 1;  // an empty unit belongs to this position
+      const bool empty = u.n == 0 && empty_at >= 0 && empty_at < stretch;
+      if (r0 < r1 || empty) {
+        const int c_first = u.cb * COLS, ncolv = min(COLS, p.ncols - c_first);
+        int lo_full, hi_full, x_;  // keys that every column of the unit sees
+        col_range(p, u.len, c_first, x_, hi_full);
+        col_range(p, u.len, c_first + ncolv - 1, lo_full, x_);
+        a.load_q(p, u.b, u.hk, c_first);
+        {
+          Unit n = u;
+          if (u.at + u.n + kUnitCost < stretch && next_unit<COLS>(p, n)) prefetch_q(n);
+        }
+        float* scores =
+            p.scores ? p.scores + ((int64_t)u.b * p.Hkv + u.hk) * p.ncols * cap : nullptr;
+        // blocks r with rf0 <= r - b0 < rf0 + rf_n are visible to every column
+        const int rf0 = (lo_full + kKv8Tok - 1) / kKv8Tok - u.b0;
+        const unsigned rf_n = (unsigned)max(0, (hi_full >> 4) - u.b0 - rf0);
+#pragma unroll 1
+        for (int r = r0; r < r1; r += RUN) {
+          if (!ring.wait(p, stage, abort_flag)) {
+            ok = false;
+            break;
+          }
+          // blocks of the stage that no page holds, or past the stretch, are computed
+          // like the others and hidden
+          const uint32_t past = r1 - r < RUN ? ~0u << (r1 - r) : 0u;
+          const uint32_t gone = ((ring.bad >> (stage * RUN)) & ((1u << RUN) - 1u)) | past;
+#pragma unroll 1
+          for (int k0 = 0; k0 < RUN; k0 += NB) {
+            const int rk = r + k0;
+            if (rk >= r1) break;
+            const uint32_t gk = (gone >> k0) & ((1u << NB) - 1u);
+            const bool edge = (unsigned)(rk - rf0) >= rf_n || (unsigned)(rk + NB - 1 - rf0) >= rf_n ||
+                              gk != 0;
+            a.step(p, ring.ring + (stage * RUN + k0) * BYTES, (u.b0 + rk) * kKv8Tok, edge, gk,
+                   past >> k0, u.len, c_first, scores, cap);
+          }
+          __syncwarp();  // the stage has been read
+          ring.fetch(p, stage, &g_dev_error, DEV_ERR_CACHE_INDEX);
+          stage = stage + 1 == kStages ? 0 : stage + 1;
+        }
+        if (!ok) break;
+
+        // ---- the unit's rows, or this warp's part of them
+        const bool whole = r0 <= 0 && r1 >= u.n;
+        // r1 < u.n: the unit goes on in the next warp, and this one is done
+        float* part = r1 < u.n ? tail_of(warp) : head_of(warp);
+        a.finish(ncolv, [&](int cc, int f, float2 o, float lim, float ref, float l) {
+          if (whole) {
+            write_out(p, u.b, u.hk, c_first + cc, f, o, ref, l);
+          } else {
+            *reinterpret_cast<float2*>(part + cc * D + f) = o;
+            if (f == 0) {
+              part[p.part_cols * D + cc] = lim;
+              part[p.part_cols * D + p.part_cols + cc] = l;
+            }
+          }
+        });
+        if (!whole && lane == 0) note_span(sm.line, u, warp, share, r0, r1);
+      }
+      if (u.at + u.n + kUnitCost >= stretch || !next_unit<COLS>(p, u)) break;
     }
-    __syncwarp();
-    a.step(p, smem_u32(sm.blocks[warp][0]), (b0 + r) * kKv8Tok, true, gone, past, len, c_first,
-           scores, cap);
-    __syncwarp();
+    if (!ok) {  // a copy never came: report it, let what is in flight land
+      *abort_flag = 1;
+      if (lane == 0) atomicOr(&g_dev_error, DEV_ERR_WAIT_TIMEOUT);
+      ring.drain(p);
+    }
   }
-  float* part = sm.part[warp];
-  a.finish(ncolv, [&](int cc, int f, float2 o, float lim, float, float l) {
-    *reinterpret_cast<float2*>(part + cc * D + f) = o;
-    if (f == 0) {
-      part[COLS * D + cc] = lim;
-      part[COLS * D + COLS + cc] = l;
-    }
-  });
-  __syncthreads();
-  const int span[3] = {b, hk, cb};
-  for (int i = tid; i < ncolv * (D / 4); i += kThreads) {
-    const int cc = i / (D / 4), f = (i - cc * (D / 4)) * 4;
-    Joined j;
-    j.clear();
-    for (int w = 0; w < kWarps; ++w) {
-      const float* pp = sm.part[w];
-      j.add(pp[COLS * D + cc], pp[COLS * D + COLS + cc],
-            *reinterpret_cast<const float4*>(pp + cc * D + f));
-    }
-    j.write(p, span, c_first + cc, f);
-  }
+  join_units<D, COLS>(p, sm.line, head_of, tail_of, cta_parts, reinterpret_cast<float*>(sm.ring));
 }
 
 struct WeighParams {
@@ -475,19 +540,23 @@ __global__ void __launch_bounds__(256) kv8_weigh_kernel(const WeighParams p) {
 }
 
 template <int D, int NT, bool ONE>
-iha_status launch_nt(const Kv8AttnParams& p, cudaStream_t s) {
+iha_status launch_nt(const Kv8AttnParams& p, int grid, cudaStream_t s) {
+  static_assert((sizeof(Smem<D, NT>) + 1024) * ctas_per_sm(NT) <= 228 * 1024,
+                "8-bit attention: the CTAs of an SM do not fit its shared memory");
+  static_assert(sizeof(Smem<D, NT>::ring) >= kThreads * 6 * sizeof(float), "scratch of the join");
+  static_assert(sizeof(Smem<D, NT>::ring) / kWarps >= 8 * NT * (D + 2) * sizeof(float),
+                "a warp's part of a unit goes into its ring");
   static SmemLimit limit;
   const cudaError_t e = limit.ensure(attn_kv8_kernel<D, NT, ONE>, (int)sizeof(Smem<D, NT>));
   if (e != cudaSuccess)
     return fail(IHA_ERR_CUDA, "mha_fwd_kv8 (smem attribute): %s", cudaGetErrorString(e));
-  attn_kv8_kernel<D, NT, ONE>
-      <<<(unsigned)((int64_t)p.B * p.Hkv * p.ncb), kThreads, sizeof(Smem<D, NT>), s>>>(p);
+  attn_kv8_kernel<D, NT, ONE><<<grid, kThreads, sizeof(Smem<D, NT>), s>>>(p);
   return check_launch("mha_fwd_kv8");
 }
 template <int D>
-iha_status launch(const Kv8AttnParams& p, int nt, cudaStream_t s) {
-  if (p.ncols == 1) return launch_nt<D, 1, true>(p, s);
-  return nt == 1 ? launch_nt<D, 1, false>(p, s) : launch_nt<D, 2, false>(p, s);
+iha_status launch(const Kv8AttnParams& p, int nt, int grid, cudaStream_t s) {
+  if (p.ncols == 1) return launch_nt<D, 1, true>(p, grid, s);
+  return nt == 1 ? launch_nt<D, 1, false>(p, grid, s) : launch_nt<D, 2, false>(p, grid, s);
 }
 
 size_t part_bytes(int64_t ncols, int d) {
@@ -562,7 +631,7 @@ iha_status mha_fwd_kv8(const void* q, const void* cache, const int32_t* block_ta
   p.wait_ns = wait_limit_for_next_launch();
   p.withhold = withhold_for_this_launch() ? 1 : 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  IHA_KV8_D_SWITCH(d, st = launch<kD>(p, nt, s))
+  IHA_KV8_D_SWITCH(d, st = launch<kD>(p, nt, grid, s))
   if (st != IHA_OK || !weights) return st;
   const WeighParams w = {p, p.scores, weights, weights_out, cap, (int)((cap + 255) / 256)};
   kv8_weigh_kernel<<<(unsigned)(B * Hkv * w.chunks), 256, 0, s>>>(w);
