@@ -61,8 +61,6 @@
 namespace iha {
 namespace {
 
-IHA_DEVICE_ERROR_WORD(attention_kv4)
-
 // A warp's ring: stages of up to kRun blocks.  Longer stages spread the
 // cost of a wait and a refill; 12 warps of 2 x 4 blocks measured better than 16
 // of 2 x 2 (131071 keys x 80 heads: 241 against 260 us; 8 warps: 256).
@@ -138,7 +136,14 @@ struct Smem {
   // -8 2^-24 sum of a group's q of columns 2 t and 2 t + 1, twice: an accumulator's start
   float4 qc[kWarps][NT * NG][4];
   uint64_t full[kWarps][kStages];
-  LineSmem line;
+  long long scan[kWarps], base[kWarps];
+  int seq[kWarps];
+  // units that span warps: at each end of a warp's stretch, {sequence, head,
+  // column block, first and last warp (-1, kWarps: in other CTAs), blocks (0: none),
+  // CTAs it began before this one, CTAs it ends behind this one}
+  int span[kWarps + 1][8];
+  int last[2], of[2][2];  // unit at each end of the stretch: joined here, its CTAs
+  int abort;
 };
 
 // GC: groups that share a P operand (4, 2: see above; 1: none).  ONE: a single
@@ -156,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
   Smem<NG, NT>& sm = *reinterpret_cast<Smem<NG, NT>*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in the warp, for the compiler too
-  volatile int* abort_flag = &sm.line.abort;
+  volatile int* abort_flag = &sm.abort;
   const int vl = kv4_v_lane(g, t);
   // FEW: of operand s, columns 2 t, 2 t + 1 are columns tc, tc + 1 scaled for group GC s + tg
   const int tg = FEW ? 2 * t / REAL : 0, tc = FEW ? 2 * t % REAL : 2 * t;
@@ -166,12 +171,63 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
     for (int i = 0; i < kStages; ++i)
       mbar_init(smem_u32(&sm.full[warp][i]),
                 p.withhold && blockIdx.x == 0 && i == 0 ? 2 : 1);
-  if (tid <= kWarps) sm.line.span[tid][5] = 0;
-  if (tid == 0) sm.line.abort = 0;
+  if (tid <= kWarps) sm.span[tid][5] = 0;
+  if (tid == 0) sm.abort = 0;
   mbar_init_fence();
-  int share, stretch;
-  Unit u;
-  if (!find_stretch<COLS>(p, sm.line, &g_dev_error, DEV_ERR_CACHE_INDEX, share, stretch, u)) return;
+  // positions of this thread's sequence, and of all; batches longer than the
+  // CTA are summed first and scanned in a second pass
+  auto positions = [&](int b, bool check) {
+    if (b >= p.B) return 0ll;
+    const int raw = __ldg(p.lens + b), len = min(max(raw, 0), p.table_w * p.page);
+    if (check && blockIdx.x == 0 && raw != len) atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
+    return (long long)head_positions<COLS>(p, len) * p.Hkv;
+  };
+  auto scan = [&](long long v, long long& all) {  // inclusive sum over the CTA's threads
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, v, k);
+      if (lane >= k) v += u;
+    }
+    if (lane == 31) sm.scan[warp] = v;
+    __syncthreads();
+    all = 0;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+      if (k < warp) v += sm.scan[k];
+      all += sm.scan[k];
+    }
+    return v;
+  };
+  long long v = positions(tid, true), all, incl = scan(v, all), total = all;
+  for (int b0 = kThreads; b0 < p.B; b0 += kThreads) {
+    long long more;
+    __syncthreads();
+    scan(positions(b0 + tid, true), more);
+    total += more;
+  }
+  const long long workers = gridDim.x * kWarps;
+  const int share = max(kMinShare, (int)((total + workers - 1) / workers));
+  const long long w_cta = (long long)share * (blockIdx.x * kWarps), w = w_cta + share * warp;
+  if (w_cta >= total) return;  // the whole CTA
+  const int stretch = (int)min((long long)share, max(0ll, total - w));
+  // the sequence that holds position w, for each warp
+  for (long long base = 0, b0 = 0;;) {
+    const long long lo = base + incl - v, hi = base + incl;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+      const long long wk = w_cta + share * k;
+      if (wk >= lo && wk < hi) {
+        sm.seq[k] = (int)b0 + tid;
+        sm.base[k] = lo;
+      }
+    }
+    base += all;
+    b0 += kThreads;
+    __syncthreads();
+    if (b0 >= p.B || base > w_cta + share * (kWarps - 1)) break;  // the same everywhere
+    v = positions((int)b0 + tid, false);
+    incl = scan(v, all);
+  }
 
   // where a warp of this CTA leaves its part of a unit that ends in its stretch
   // after beginning before it, and of one that goes on after it
@@ -180,6 +236,22 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
   auto tail_of = [&](int w) { return reinterpret_cast<float*>(sm.ring[w]); };
   bool ok = true;
   if (stretch > 0) {
+    Unit u;
+    u.b = sm.seq[warp];
+    u.len = seq_len(p, u.b);
+    {
+      const int per_head = head_positions<COLS>(p, u.len);
+      const long long rel = w - sm.base[warp];
+      u.hk = (rel >> 31) == 0 ? (int)((unsigned)rel / (unsigned)per_head) : (int)(rel / per_head);
+      int s = (int)(rel - (long long)u.hk * per_head);
+      for (u.cb = 0;; ++u.cb) {
+        unit_blocks<COLS>(p, u.len, u.cb, u.b0, u.n);
+        if (s < u.n + kUnitCost || u.cb == p.ncb - 1) break;
+        s -= u.n + kUnitCost;
+      }
+      u.at = -s;
+    }
+
     // Q of the unit this warp comes to next, on its way while the unit before is computed
     auto prefetch_q = [&](const Unit& n) {
 #pragma unroll
@@ -195,9 +267,79 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
     };
     prefetch_q(u);
 
-    BlockRing<BYTES, kRun, kStages, COLS> ring;
-    ring.start(p, u, stretch, lane, smem_u32(sm.ring[warp]), smem_u32(sm.full[warp]), &g_dev_error,
-               DEV_ERR_CACHE_INDEX);
+    // ---- the ring: stages of up to kRun blocks of one unit, kStages ahead, copied
+    // in runs inside a page; the page id of the run after the current one is
+    // read ahead
+    Unit pu = u;
+    int pr, pr_end;
+    my_blocks(pu, stretch, pr, pr_end);
+    bool more = true;
+    struct Run {
+      int id, head, in_page, cnt;  // cnt blocks of the page, 0: no more
+      int left;                    // blocks of the unit from this run on
+    };
+    auto next_run = [&]() {
+      Run r = {0, 0, 0, 0, 0};
+      while (more && pr >= pr_end) {
+        more = pu.at + pu.n + kUnitCost < stretch && next_unit<COLS>(p, pu);
+        if (more) my_blocks(pu, stretch, pr, pr_end);
+      }
+      if (more) {
+        const int blk = pu.b0 + pr, pi = blk / p.blocks_per_page;
+        r.in_page = blk - pi * p.blocks_per_page;
+        r.left = pr_end - pr;
+        r.cnt = min(p.blocks_per_page - r.in_page, r.left);
+        r.head = pu.hk;
+        r.id = __ldg(p.table + (int64_t)pu.b * p.table_w + pi);
+        pr += r.cnt;
+      }
+      return r;
+    };
+    Run run, run_next = next_run();
+    const uint8_t* src = nullptr;  // the run's next block; null: no such page
+    auto take_run = [&]() {
+      run = run_next;
+      if (run.cnt > 0) {
+        run_next = next_run();
+        const bool in = run.id >= 0 && run.id < p.n_pages;
+        if (!in && lane == 0) atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
+        src = in ? p.cache + kv4_block_of(run.id, run.in_page, run.head, p.Hkv, p.blocks_per_page,
+                                          NG)
+                 : nullptr;
+      }
+    };
+    take_run();
+    // bit per block of the ring: no such page; bit per stage: copies under way,
+    // and the parity of its barrier
+    uint32_t bad = 0, flying = 0, phase = 0;
+    const uint32_t ring = smem_u32(sm.ring[warp]), bars = smem_u32(sm.full[warp]);
+    auto fetch = [&](int stage) {
+      bad &= ~(((1u << kRun) - 1u) << (stage * kRun));
+      flying &= ~(1u << stage);
+      if (run.cnt == 0) return;
+      const int want = min(kRun, run.left);
+      uint32_t bytes = 0;
+      int have = 0;
+      do {
+        const int c = min(want - have, run.cnt);
+        if (src != nullptr) {
+          if (lane == 0)
+            bulk_load(ring + (stage * kRun + have) * BYTES, src, c * BYTES, bars + 8 * stage);
+          bytes += c * BYTES;
+          src += c * BYTES;
+        } else {
+          bad |= ((1u << c) - 1u) << (stage * kRun + have);
+        }
+        have += c;
+        run.cnt -= c;
+        run.left -= c;
+        if (run.cnt == 0) take_run();
+      } while (have < want);
+      if (lane == 0) mbar_arrive_expect_tx(bars + 8 * stage, bytes);
+      flying |= 1u << stage;
+    };
+#pragma unroll 1
+    for (int i = 0; i < kStages; ++i) fetch(i);
     int stage = 0;
 
     // ---- units of the stretch
@@ -318,13 +460,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
         const unsigned rf_n = (unsigned)max(0, (hi_full >> 4) - u.b0 - rf0);
 #pragma unroll 1
         for (int r = r0; r < r1; r += kRun) {
-          if (!ring.wait(p, stage, abort_flag)) {
+          if (!mbar_wait_warp(bars + 8 * stage, (phase >> stage) & 1u, abort_flag, p.wait_ns)) {
             ok = false;
             break;
           }
+          phase ^= 1u << stage;
           // blocks of the stage that no page holds, or past the unit's end, are
           // computed like the others and hidden
-          uint32_t gone = (ring.bad >> (stage * kRun)) & ((1u << kRun) - 1u);
+          uint32_t gone = (bad >> (stage * kRun)) & ((1u << kRun) - 1u);
           if (r1 - r < kRun) gone |= ~0u << (r1 - r);
 #pragma unroll 1
           for (int k0 = 0; k0 < kRun; k0 += NB) {
@@ -574,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
             }
           }
           __syncwarp();  // the stage has been read
-          ring.fetch(p, stage, &g_dev_error, DEV_ERR_CACHE_INDEX);
+          fetch(stage);
           stage = stage + 1 == kStages ? 0 : stage + 1;
         }
         if (!ok) break;
@@ -640,18 +783,94 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
                       mlim[nt][e], mref[nt][e], l[nt][e]);
             }
         }
-        if (!whole && lane == 0) note_span(sm.line, u, warp, share, r0, r1);
+        if (!whole) {
+          if (lane == 0) {
+            const int p0 = share * warp + u.at + kUnitCost;  // of the unit's first block, in the CTA
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              if (k ? r1 < u.n : (r0 > 0 && warp == 0)) {
+                int* sp = sm.span[k ? warp + 1 : 0];
+                sp[0] = u.b;
+                sp[1] = u.hk;
+                sp[2] = u.cb;
+                sp[3] = p0 >= 0 ? p0 / share : -1;
+                sp[4] = min((p0 + u.n - 1) / share, kWarps);
+                sp[5] = u.n;
+                // (in 32 bits: a 64-bit division is a call, and costs the loop registers)
+                sp[6] = p0 >= 0 ? 0 : (-p0 + share * kWarps - 1) / (share * kWarps);
+                sp[7] = (p0 + u.n - 1) / (share * kWarps);
+              }
+          }
+        }
       }
       if (u.at + u.n + kUnitCost >= stretch || !next_unit<COLS>(p, u)) break;
     }
     if (!ok) {  // a copy never came: report it, let what is in flight land
       *abort_flag = 1;
       if (lane == 0) atomicOr(&g_dev_error, DEV_ERR_WAIT_TIMEOUT);
-      ring.drain(p);
+      volatile int no_abort = 0;
+      for (int i = 0; i < kStages; ++i)
+        if ((flying >> i) & 1u) mbar_wait(bars + 8 * i, (phase >> i) & 1u, &no_abort, p.wait_ns);
     }
   }
 
-  join_units<D, COLS>(p, sm.line, head_of, tail_of, cta_parts, reinterpret_cast<float*>(sm.ring));
+  // ---- units that span warps: join this CTA's parts
+  __syncthreads();
+  if (sm.abort) return;
+  auto same_unit = [&](int i, int k) {
+    return sm.span[i][5] != 0 && sm.span[i][0] == sm.span[k][0] && sm.span[i][1] == sm.span[k][1] &&
+           sm.span[i][2] == sm.span[k][2];
+  };
+#pragma unroll 1
+  for (int k = 0; k <= kWarps; ++k) {
+    const int* span = sm.span[k];
+    const int first = span[3], last = span[4];
+    if (span[5] == 0 || (k > 0 && same_unit(k - 1, k))) continue;
+    const int c_first = span[2] * COLS, ncolv = min(COLS, p.ncols - c_first);
+    const int lo = max(first, 0), hi = min(last, kWarps - 1);
+    float* to = cta_parts + (first >= 0 ? 1 : 0) * p.part_stride;
+    for (int i = tid; i < ncolv * (D / 4); i += kThreads) {
+      const int cc = i / (D / 4), f = (i - cc * (D / 4)) * 4;
+      Joined a;
+      a.clear();
+      for (int x = lo; x <= hi; ++x) {
+        const float* pp = x == last ? head_of(x) : tail_of(x);
+        a.add(pp[p.part_cols * D + cc], pp[p.part_cols * D + p.part_cols + cc],
+              *reinterpret_cast<const float4*>(pp + cc * D + f));
+      }
+      if (first >= 0 && last < kWarps) {
+        a.write(p, span, c_first + cc, f);
+      } else {
+        *reinterpret_cast<float4*>(to + cc * D + f) = a.o;
+        if (f == 0) {
+          to[p.part_cols * D + cc] = a.m;
+          to[p.part_cols * D + p.part_cols + cc] = a.l;
+        }
+      }
+    }
+  }
+  // ---- units that span CTAs, the one the CTA begins in and the one it ends in:
+  // the CTA that arrives last joins them
+  __syncthreads();
+  if (tid < 2) {
+    const int* span = sm.span[tid == 0 ? 0 : kWarps];
+    bool join = span[5] != 0 && (tid == 0 || !same_unit(0, kWarps));
+    if (join) {
+      // CTAs of the unit's first and last block
+      const int first = blockIdx.x - span[6], last = blockIdx.x + span[7];
+      join = first != last && arrive(p.counters + first) == (unsigned)(last - first);
+      if (join) p.counters[first] = 0u;  // ready for the next call
+      sm.of[tid][0] = first;
+      sm.of[tid][1] = last;
+    }
+    sm.last[tid] = join;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k)
+    if (sm.last[k])
+      join_ctas<D, COLS>(p, sm.span[k == 0 ? 0 : kWarps], sm.of[k],
+                         reinterpret_cast<float*>(sm.ring));
 }
 
 template <int NG, int NT, int GC, bool ONE>

@@ -63,11 +63,12 @@ __device__ __forceinline__ void encode(uint8_t* to, const uint4& u, float f, flo
       (uint32_t)e4m3_pair(__uint_as_float(u.z) * f, __uint_as_float(u.w) * f) << 16;
 }
 
-template <typename T, int D>
+// ITER: iterations that hold a block's new rows, from the first on.
+template <typename T, int D, int ITER>
 __global__ void __launch_bounds__(32 * kWarps) kv8_append_kernel(const AppendParams p) {
-  constexpr int V = 16 / sizeof(T);                    // features of a lane
-  constexpr int LPR = D / V, RPI = 32 / LPR;           // lanes of a row, rows at once
-  constexpr int ITER = (kKv8Tok + RPI - 1) / RPI;
+  constexpr int V = 16 / sizeof(T);            // features of a lane
+  constexpr int LPR = D / V, RPI = 32 / LPR;   // lanes of a row, rows at once
+  constexpr bool BOTH = ITER <= 8;             // K and V are loaded before either is used
   const int lane = threadIdx.x & 31;
   const int64_t id64 = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (id64 >= p.items) return;
@@ -82,32 +83,36 @@ __global__ void __launch_bounds__(32 * kWarps) kv8_append_kernel(const AppendPar
   const int blk = first / kKv8Tok + nth, pos0 = blk * kKv8Tok;
   if (first >= len || pos0 >= len) return;
   const int pi = blk / p.bpp, page_id = __ldg(p.table + (int64_t)b * p.table_w + pi);
+  const int had = max(0, first - pos0), end = min(len - pos0, kKv8Tok);  // new rows [had, end)
+  const int r = lane / LPR, c = lane - r * LPR;  // row of an iteration, vector of the row
+
+  auto load = [&](int which, uint4 (&x)[ITER]) {
+    const iha_strides& st = which ? p.sv : p.sk;
+    const T* src = static_cast<const T*>(which ? p.v : p.k) + b * st.b_outer + head * st.head +
+                   (int64_t)(pos0 + had - (len - p.N)) * st.seq + c * V;
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (r < RPI && had + i * RPI + r < end)
+        x[i] = __ldg(reinterpret_cast<const uint4*>(src + (i * RPI + r) * st.seq));
+    }
+  };
+  uint4 xk[ITER], xv[ITER];
+  load(0, xk);
+  if (BOTH) load(1, xv);
+
   if (page_id < 0 || page_id >= p.n_pages) {
     if (lane == 0) atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
     return;
   }
   uint8_t* const base =
       p.cache + kv8_block_of(page_id, blk - pi * p.bpp, head, p.heads.d, p.bpp, D);
-  const int had = max(0, first - pos0), end = min(len - pos0, kKv8Tok);  // new rows [had, end)
   Kv8Tail tail = {{0.f, 0.f}, 0u, 0u};
   if (had > 0) tail = kv8_tail(base, D);
 
-  const int r = lane / LPR, c = lane - r * LPR;  // row of an iteration, vector of the row
-  const uint32_t row_lanes = (LPR == 32 ? ~0u : ((1u << LPR) - 1u)) << (LPR == 32 ? 0 : r * LPR % 32);
-#pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    const iha_strides& st = which ? p.sv : p.sk;
-    const T* src = static_cast<const T*>(which ? p.v : p.k) + b * st.b_outer + head * st.head +
-                   (int64_t)(pos0 - (len - p.N)) * st.seq + c * V;
-    uint8_t* const rows = base + which * kKv8Tok * D;
-    uint4 x[ITER];
-#pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-      const int row = i * RPI + r;
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (r < RPI && row >= had && row < end)
-        x[i] = __ldg(reinterpret_cast<const uint4*>(src + row * st.seq));
-    }
+  const uint32_t row_lanes =
+      LPR == 32 ? ~0u : ((1u << (LPR % 32)) - 1u) << (r * LPR % 32);
+  auto store = [&](uint8_t* rows, uint4 (&x)[ITER], float old, int before_bit, float& scale) {
     uint32_t top = 0, nan = 0;
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
@@ -116,7 +121,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv8_append_kernel(const AppendPar
       if (bad != 0 && r < RPI && (bad & row_lanes) != 0) {  // a row of NaN: codes of 0
         m = 0;
         x[i] = make_uint4(0, 0, 0, 0);
-        nan |= 1u << (i * RPI + r);
+        nan |= 1u << (had + i * RPI + r);
       }
       top = max(top, m);
     }
@@ -124,7 +129,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv8_append_kernel(const AppendPar
     nan = __reduce_or_sync(0xffffffffu, nan);
     // 448 = 1.75 * 2^8
     int e = max((int)(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0), kKv8LowestE);
-    const int before = kv8_exponent(tail.scale[which]);
+    const int before = kv8_exponent(old);
     if (had > 0) e = max(e, before);
     const float f = kv8_two(-e), again = kv8_two(before - e);
     auto at = [&](int row) {  // the lane's codes of a row
@@ -132,26 +137,43 @@ __global__ void __launch_bounds__(32 * kWarps) kv8_append_kernel(const AppendPar
     };
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
-      const int row = i * RPI + r;
-      // rows behind the last one of a fresh block become zeros
-      if (r < RPI && row >= had && row < (had > 0 ? end : kKv8Tok)) encode(at(row), x[i], f, T());
+      const int row = had + i * RPI + r;
+      if (r < RPI && row < end) encode(at(row), x[i], f, T());
     }
-    if (had > 0 && e > before) {
+    // rows behind the last one of a fresh block become zeros; earlier ones of a block
+    // that grows are rounded again
+    const int other0 = had > 0 ? 0 : end, other1 = had > 0 ? (e > before ? had : 0) : kKv8Tok;
 #pragma unroll 1
-      for (int row = r; row < had; row += RPI)
-        if (r < RPI) {
-          uint32_t* w = reinterpret_cast<uint32_t*>(at(row));
+    for (int row = other0 + r; row < other1; row += RPI)
+      if (r < RPI) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(at(row));
 #pragma unroll
-          for (int j = 0; j < V / 4; ++j) w[j] = e4m3_rescale(w[j], again);
-        }
-    }
-    tail.scale[which] = kv8_two(e);
-    const uint32_t fresh = (end >= kKv8Tok ? 0xFFFFu : (1u << end) - 1u) & ~((1u << had) - 1u);
-    tail.nan = (tail.nan & ~(fresh << (16 * which))) | (nan << (16 * which));
-  }
+        for (int j = 0; j < V / 4; ++j) w[j] = had > 0 ? e4m3_rescale(w[j], again) : 0u;
+      }
+    scale = kv8_two(e);
+    const uint32_t fresh = ((1u << end) - 1u) & ~((1u << had) - 1u);
+    tail.nan = (tail.nan & ~(fresh << before_bit)) | (nan << before_bit);
+  };
+  float sk, sv;
+  store(base, xk, tail.scale[0], 0, sk);
+  if (!BOTH) load(1, xv);
+  store(base + kKv8Tok * D, xv, tail.scale[1], 16, sv);
   if (lane == 0)
-    *reinterpret_cast<uint4*>(base + 32 * D) = make_uint4(
-        __float_as_uint(tail.scale[0]), __float_as_uint(tail.scale[1]), tail.nan, 0u);
+    *reinterpret_cast<uint4*>(base + 32 * D) =
+        make_uint4(__float_as_uint(sk), __float_as_uint(sv), tail.nan, 0u);
+}
+
+template <typename T, int D>
+void launch_append(const AppendParams& p, unsigned grid, cudaStream_t s) {
+  constexpr int RPI = 32 / (D / (16 / (int)sizeof(T))), FULL = (kKv8Tok + RPI - 1) / RPI;
+  // few new rows of a block: forms that hold no more (32 sequences x 80 heads of 128, one
+  // row each)
+  if (p.N <= RPI)
+    kv8_append_kernel<T, D, 1><<<grid, 32 * kWarps, 0, s>>>(p);
+  else if (FULL > 4 && p.N <= 4 * RPI)
+    kv8_append_kernel<T, D, 4><<<grid, 32 * kWarps, 0, s>>>(p);
+  else
+    kv8_append_kernel<T, D, FULL><<<grid, 32 * kWarps, 0, s>>>(p);
 }
 
 struct LoadParams {
@@ -321,9 +343,9 @@ iha_status kv8_append(const void* k, const void* v, const int32_t* block_table,
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   IHA_KV8_D_SWITCH(d, {
     if (dt == IHA_BF16)
-      kv8_append_kernel<__nv_bfloat16, kD><<<grid, 32 * kWarps, 0, s>>>(p);
+      launch_append<__nv_bfloat16, kD>(p, grid, s);
     else
-      kv8_append_kernel<float, kD><<<grid, 32 * kWarps, 0, s>>>(p);
+      launch_append<float, kD>(p, grid, s);
   })
   return check_launch(name);
 }

@@ -2,10 +2,10 @@
 // (kv8_evict; layout of the cache: kv8.cuh).
 //
 // Two launches.  Select, a CTA per sequence and head: the weights as integers in their
-// order (a float's bits, the negative ones turned round), the smallest kept one found
-// byte by byte from counts (a radix select), then the kept ones in the order of their
-// positions: each warp counts its stretch of keys, the counts are summed over the warps,
-// each warp writes its own.  Copy, a warp per block of 16 kept rows of a head: rows are
+// order (a float's bits, the negative ones turned round), held in shared memory, the
+// smallest kept one found from counts of 11 bits at a time (a radix select), then the
+// kept ones in the order of their positions: each warp counts its stretch of keys, the
+// counts are summed over the warps, each warp writes its own.  Copy, a warp per block of 16 kept rows of a head: rows are
 // gathered whole, 16 bytes a lane, rounded again where their block's scale is not
 // the largest of the sixteen.
 #include "kv8.cuh"
@@ -15,7 +15,7 @@ namespace {
 
 IHA_DEVICE_ERROR_WORD(kv8_evict)
 
-constexpr int kWarps = 16;
+constexpr int kWarps = 32;
 constexpr int kThreads = 32 * kWarps;
 
 struct EvictParams {
@@ -37,10 +37,14 @@ __device__ __forceinline__ uint32_t order_of(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kThreads) kv8_select_kernel(const EvictParams p) {
-  __shared__ int hist[256];
+constexpr int kDigit = 11, kBins = 1 << kDigit;  // three digits: 11, 11 and 10 bits
+constexpr int kCached = 48 * 1024;  // keys whose numbers stay in shared memory
+
+__global__ void __launch_bounds__(kThreads, 1) kv8_select_kernel(const EvictParams p) {
+  extern __shared__ uint32_t held[];
+  __shared__ int hist[kBins];
   __shared__ int count[2][kWarps];
-  __shared__ uint32_t found[2];  // the digit, and how many of it are kept
+  __shared__ int found[3];  // the digit, how many of it are kept, how many have it
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int plane = blockIdx.x, b = plane / p.H, h = plane - b * p.H;
   const int raw = __ldg(p.lens + b), n = min(max(raw, 0), (int)p.cap);
@@ -56,43 +60,62 @@ __global__ void __launch_bounds__(kThreads) kv8_select_kernel(const EvictParams 
   const int older = n > p.keep ? n - p.recent : 0;  // keys [0, older) compete
   int need = n > p.keep ? p.keep - p.recent : 0;
   uint32_t low = 0;  // the smallest kept weight, in order_of's numbers
+  auto number = [&](int j) { return j < kCached ? held[j] : order_of(__ldg(w + j)); };
   if (need > 0) {
+    for (int j = tid; j < min(older, kCached); j += kThreads) held[j] = order_of(__ldg(w + j));
 #pragma unroll 1
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
+    for (int shift = 32 - kDigit; ; shift = max(0, shift - kDigit)) {
+      const int upto = shift == 32 - kDigit ? 32 : shift == 0 ? 32 - 2 * kDigit : shift + kDigit;
+      const uint32_t mask = (1u << (upto - shift)) - 1u;
+      for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
       __syncthreads();
-      for (int j = tid; j < older; j += kThreads) {
-        const uint32_t u = order_of(__ldg(w + j));
-        if (shift == 24 || (u >> (shift + 8)) == (low >> (shift + 8)))
-          atomicAdd(&hist[(u >> shift) & 255u], 1);
-      }
-      __syncthreads();
-      if (warp == 0) {  // from the largest digit down: the one at which `need` is reached
-        int c[8], sum = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum += c[i] = hist[255 - (8 * lane + i)];
-        int upto = sum;
-#pragma unroll
-        for (int k = 1; k < 32; k <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, upto, k);
-          if (lane >= k) upto += v;
+      for (int j0 = warp * 32; j0 < older; j0 += kThreads) {
+        const int j = j0 + lane;
+        const uint32_t u = j < older ? number(j) : 0u;
+        const bool in = j < older && (upto == 32 || (u >> upto) == (low >> upto));
+        const uint32_t who = __ballot_sync(0xffffffffu, in);
+        if (who == 0) continue;
+        const int digit = (int)((u >> shift) & mask);
+        // equal weights (zeros, most often) would add to one counter 32 times
+        const int first = __shfl_sync(0xffffffffu, digit, __ffs(who) - 1);
+        if (__all_sync(0xffffffffu, !in || digit == first)) {
+          if (lane == 0) atomicAdd(&hist[first], __popc(who));
+        } else if (in) {
+          atomicAdd(&hist[digit], 1);
         }
-        int before = upto - sum;
-        if (before < need && upto >= need)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (before < need && before + c[i] >= need) {
-              found[0] = 255 - (8 * lane + i);
-              found[1] = need - before;
-            }
-            before += c[i];
-          }
       }
       __syncthreads();
-      low |= found[0] << shift;
-      need = (int)found[1];  // of those equal so far
+      // from the largest digit down: the one at which `need` is reached
+      constexpr int PER = kBins / kThreads;
+      int c[PER], sum = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) sum += c[i] = hist[kBins - 1 - (PER * tid + i)];
+      int incl = sum;
+#pragma unroll
+      for (int k = 1; k < 32; k <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, k);
+        if (lane >= k) incl += v;
+      }
+      if (lane == 31) count[0][warp] = incl;
       __syncthreads();
+      for (int k = 0; k < warp; ++k) incl += count[0][k];
+      int before = incl - sum;
+      if (before < need && incl >= need)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          if (before < need && before + c[i] >= need) {
+            found[0] = kBins - 1 - (PER * tid + i);
+            found[1] = need - before;
+            found[2] = c[i];
+          }
+          before += c[i];
+        }
+      __syncthreads();
+      low |= (uint32_t)found[0] << shift;
+      need = found[1];  // of those equal so far
+      if (shift == 0 || found[2] == need) break;  // all that have the digits so far are kept
     }
+    __syncthreads();
   }
   // each warp's stretch of keys: how many are above `low`, how many equal it
   const bool all = n <= p.keep;
@@ -103,7 +126,7 @@ __global__ void __launch_bounds__(kThreads) kv8_select_kernel(const EvictParams 
     if (all || j >= older) {
       ++above;
     } else if (p.keep > p.recent) {
-      const uint32_t u = order_of(__ldg(w + j));
+      const uint32_t u = number(j);
       above += u > low;
       equal += u == low;
     }
@@ -125,10 +148,9 @@ __global__ void __launch_bounds__(kThreads) kv8_select_kernel(const EvictParams 
   for (int j = j0; j < j1; j += 32) {
     const int i = j + lane;
     const bool in = i < j1;
-    const float x = in ? __ldg(w + i) : 0.f;
     bool is_above = in && (all || i >= older), is_equal = false;
     if (in && !is_above && p.keep > p.recent) {
-      const uint32_t u = order_of(x);
+      const uint32_t u = number(i);
       is_above = u > low;
       is_equal = u == low;
     }
@@ -138,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) kv8_select_kernel(const EvictParams 
     if (take) {
       const int to = at + __popc(mt & below);
       kept[to] = i;
-      if (out) out[to] = x;
+      if (out) out[to] = __ldg(w + i);
     }
     at += __popc(mt);
     eq += __popc(me);
@@ -304,7 +326,12 @@ iha_status kv8_evict(void* cache, const int32_t* block_table, const int32_t* seq
   p.heads.set(Hkv);
   p.items = planes * blocks;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  kv8_select_kernel<<<(unsigned)planes, kThreads, 0, s>>>(p);
+  static SmemLimit limit;
+  const cudaError_t e = limit.ensure(kv8_select_kernel, kCached * 4);
+  if (e != cudaSuccess)
+    return fail(IHA_ERR_CUDA, "%s (smem attribute): %s", name, cudaGetErrorString(e));
+  const int held = (int)(cap < kCached ? cap : kCached) * 4;
+  kv8_select_kernel<<<(unsigned)planes, kThreads, held, s>>>(p);
   st = check_launch(name);
   if (st != IHA_OK) return st;
   const unsigned grid = (unsigned)((p.items + 7) / 8);

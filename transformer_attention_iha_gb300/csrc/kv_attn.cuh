@@ -17,6 +17,8 @@
 namespace iha {
 namespace {
 
+IHA_DEVICE_ERROR_WORD(kv_attn)  // one for each file that includes this
+
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kKvTok = 16;  // tokens of a block
@@ -293,284 +295,6 @@ __device__ __forceinline__ unsigned arrive(unsigned* counter) {
   return old;
 }
 
-
-// What a CTA keeps in shared memory of its place in the line.
-struct LineSmem {
-  long long scan[kWarps], base[kWarps];
-  int seq[kWarps];
-  // units that span warps: at each end of a warp's stretch, {sequence, head,
-  // column block, first and last warp (-1, kWarps: in other CTAs), blocks (0: none),
-  // CTAs it began before this one, CTAs it ends behind this one}
-  int span[kWarps + 1][8];
-  int last[2], of[2][2];  // unit at each end of the stretch: joined here, its CTAs
-  int abort;
-};
-
-// The stretch of the line that this warp has: the length of every warp's share and of
-// this one's, and the unit it begins in.  False if the CTA has none (all threads call; a
-// length out of range is flagged in *err).
-template <int COLS>
-__device__ __forceinline__ bool find_stretch(const KvAttnParams& p, LineSmem& sm, unsigned* err,
-                                             unsigned err_bit, int& share, int& stretch, Unit& u) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  // positions of this thread's sequence, and of all; batches longer than the
-  // CTA are summed first and scanned in a second pass
-  auto positions = [&](int b, bool check) {
-    if (b >= p.B) return 0ll;
-    const int raw = __ldg(p.lens + b), len = min(max(raw, 0), p.table_w * p.page);
-    if (check && blockIdx.x == 0 && raw != len) atomicOr(err, err_bit);
-    return (long long)head_positions<COLS>(p, len) * p.Hkv;
-  };
-  auto scan = [&](long long v, long long& all) {  // inclusive sum over the CTA's threads
-#pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, v, k);
-      if (lane >= k) v += x;
-    }
-    if (lane == 31) sm.scan[warp] = v;
-    __syncthreads();
-    all = 0;
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-      if (k < warp) v += sm.scan[k];
-      all += sm.scan[k];
-    }
-    return v;
-  };
-  long long v = positions(tid, true), all, incl = scan(v, all), total = all;
-  for (int b0 = kThreads; b0 < p.B; b0 += kThreads) {
-    long long more;
-    __syncthreads();
-    scan(positions(b0 + tid, true), more);
-    total += more;
-  }
-  const long long workers = gridDim.x * kWarps;
-  share = max(kMinShare, (int)((total + workers - 1) / workers));
-  const long long w_cta = (long long)share * (blockIdx.x * kWarps), w = w_cta + share * warp;
-  if (w_cta >= total) return false;
-  stretch = (int)min((long long)share, max(0ll, total - w));
-  // the sequence that holds position w, for each warp
-  for (long long base = 0, b0 = 0;;) {
-    const long long lo = base + incl - v, hi = base + incl;
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-      const long long wk = w_cta + share * k;
-      if (wk >= lo && wk < hi) {
-        sm.seq[k] = (int)b0 + tid;
-        sm.base[k] = lo;
-      }
-    }
-    base += all;
-    b0 += kThreads;
-    __syncthreads();
-    if (b0 >= p.B || base > w_cta + share * (kWarps - 1)) break;  // the same everywhere
-    v = positions((int)b0 + tid, false);
-    incl = scan(v, all);
-  }
-  if (stretch > 0) {
-    u.b = sm.seq[warp];
-    u.len = seq_len(p, u.b);
-    const int per_head = head_positions<COLS>(p, u.len);
-    const long long rel = w - sm.base[warp];
-    u.hk = (rel >> 31) == 0 ? (int)((unsigned)rel / (unsigned)per_head) : (int)(rel / per_head);
-    int s = (int)(rel - (long long)u.hk * per_head);
-    for (u.cb = 0;; ++u.cb) {
-      unit_blocks<COLS>(p, u.len, u.cb, u.b0, u.n);
-      if (s < u.n + kUnitCost || u.cb == p.ncb - 1) break;
-      s -= u.n + kUnitCost;
-    }
-    u.at = -s;
-  }
-  return true;
-}
-
-// A warp's ring of blocks in shared memory: STAGES stages of up to RUN blocks of one
-// unit, filled ahead by bulk copies in runs inside a page; the page id of the run after
-// the current one is read ahead.
-template <int BYTES, int RUN, int STAGES, int COLS>
-struct BlockRing {
-  struct Run {
-    int id, head, in_page, cnt;  // cnt blocks of the page, 0: no more
-    int left;                    // blocks of the unit from this run on
-  };
-  Unit pu;
-  int pr, pr_end, stretch, lane;
-  bool more;
-  Run run, run_next;
-  const uint8_t* src;  // the run's next block; null: no such page
-  // bit per block of the ring: no such page; bit per stage: copies under way, and the
-  // parity of its barrier
-  uint32_t bad, flying, phase, ring, bars;
-
-  __device__ __forceinline__ Run next_run(const KvAttnParams& p) {
-    Run r = {0, 0, 0, 0, 0};
-    while (more && pr >= pr_end) {
-      more = pu.at + pu.n + kUnitCost < stretch && next_unit<COLS>(p, pu);
-      if (more) my_blocks(pu, stretch, pr, pr_end);
-    }
-    if (more) {
-      const int blk = pu.b0 + pr, pi = blk / p.blocks_per_page;
-      r.in_page = blk - pi * p.blocks_per_page;
-      r.left = pr_end - pr;
-      r.cnt = min(p.blocks_per_page - r.in_page, r.left);
-      r.head = pu.hk;
-      r.id = __ldg(p.table + (int64_t)pu.b * p.table_w + pi);
-      pr += r.cnt;
-    }
-    return r;
-  }
-  __device__ __forceinline__ void take_run(const KvAttnParams& p, unsigned* err, unsigned bit) {
-    run = run_next;
-    if (run.cnt > 0) {
-      run_next = next_run(p);
-      const bool in = run.id >= 0 && run.id < p.n_pages;
-      if (!in && lane == 0) atomicOr(err, bit);
-      src = in ? p.cache + (((int64_t)run.id * p.Hkv + run.head) * p.blocks_per_page +
-                            run.in_page) * (int64_t)BYTES
-               : nullptr;
-    }
-  }
-  __device__ __forceinline__ void start(const KvAttnParams& p, const Unit& u, int stretch_,
-                                        int lane_, uint32_t ring_, uint32_t bars_, unsigned* err,
-                                        unsigned bit) {
-    pu = u;
-    stretch = stretch_;
-    lane = lane_;
-    ring = ring_;
-    bars = bars_;
-    more = true;
-    bad = flying = phase = 0;
-    src = nullptr;
-    my_blocks(pu, stretch, pr, pr_end);
-    run_next = next_run(p);
-    take_run(p, err, bit);
-#pragma unroll 1
-    for (int i = 0; i < STAGES; ++i) fetch(p, i, err, bit);
-  }
-  __device__ __forceinline__ void fetch(const KvAttnParams& p, int stage, unsigned* err,
-                                        unsigned bit) {
-    bad &= ~(((1u << RUN) - 1u) << (stage * RUN));
-    flying &= ~(1u << stage);
-    if (run.cnt == 0) return;
-    const int want = min(RUN, run.left);
-    uint32_t bytes = 0;
-    int have = 0;
-    do {
-      const int c = min(want - have, run.cnt);
-      if (src != nullptr) {
-        if (lane == 0)
-          bulk_load(ring + (stage * RUN + have) * BYTES, src, c * BYTES, bars + 8 * stage);
-        bytes += c * BYTES;
-        src += c * BYTES;
-      } else {
-        bad |= ((1u << c) - 1u) << (stage * RUN + have);
-      }
-      have += c;
-      run.cnt -= c;
-      run.left -= c;
-      if (run.cnt == 0) take_run(p, err, bit);
-    } while (have < want);
-    if (lane == 0) mbar_arrive_expect_tx(bars + 8 * stage, bytes);
-    flying |= 1u << stage;
-  }
-  __device__ __forceinline__ bool wait(const KvAttnParams& p, int stage, volatile int* abort_flag) {
-    if (!mbar_wait_warp(bars + 8 * stage, (phase >> stage) & 1u, abort_flag, p.wait_ns))
-      return false;
-    phase ^= 1u << stage;
-    return true;
-  }
-  // After a wait that gave up: what is in flight lands before the memory goes away.
-  __device__ __forceinline__ void drain(const KvAttnParams& p) {
-    volatile int no_abort = 0;
-    for (int i = 0; i < STAGES; ++i)
-      if ((flying >> i) & 1u) mbar_wait(bars + 8 * i, (phase >> i) & 1u, &no_abort, p.wait_ns);
-  }
-};
-
-// Notes where the part of a unit that a warp leaves belongs: with its first and last
-// warp and CTA (one lane calls, for a unit that goes on behind the warp, or began before
-// the CTA).
-__device__ __forceinline__ void note_span(LineSmem& sm, const Unit& u, int warp, int share, int r0,
-                                          int r1) {
-  const int p0 = share * warp + u.at + kUnitCost;  // of the unit's first block, in the CTA
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    if (k ? r1 < u.n : (r0 > 0 && warp == 0)) {
-      int* sp = sm.span[k ? warp + 1 : 0];
-      sp[0] = u.b;
-      sp[1] = u.hk;
-      sp[2] = u.cb;
-      sp[3] = p0 >= 0 ? p0 / share : -1;
-      sp[4] = min((p0 + u.n - 1) / share, kWarps);
-      sp[5] = u.n;
-      // (in 32 bits: a 64-bit division is a call, and costs the loop registers)
-      sp[6] = p0 >= 0 ? 0 : (-p0 + share * kWarps - 1) / (share * kWarps);
-      sp[7] = (p0 + u.n - 1) / (share * kWarps);
-    }
-}
-
-// Units that span warps: joins this CTA's parts, and, of a unit that spans CTAs, all of
-// them in the CTA that arrives last (all threads call).  head_of, tail_of: a warp's part
-// of a unit that ends in its stretch after beginning before it, and of one that goes on.
-template <int D, int COLS, typename Head, typename Tail>
-__device__ __forceinline__ void join_units(const KvAttnParams& p, LineSmem& sm, Head head_of,
-                                           Tail tail_of, float* cta_parts, float* scratch) {
-  const int tid = threadIdx.x;
-  __syncthreads();
-  if (sm.abort) return;
-  auto same_unit = [&](int i, int k) {
-    return sm.span[i][5] != 0 && sm.span[i][0] == sm.span[k][0] && sm.span[i][1] == sm.span[k][1] &&
-           sm.span[i][2] == sm.span[k][2];
-  };
-#pragma unroll 1
-  for (int k = 0; k <= kWarps; ++k) {
-    const int* span = sm.span[k];
-    const int first = span[3], last = span[4];
-    if (span[5] == 0 || (k > 0 && same_unit(k - 1, k))) continue;
-    const int c_first = span[2] * COLS, ncolv = min(COLS, p.ncols - c_first);
-    const int lo = max(first, 0), hi = min(last, kWarps - 1);
-    float* to = cta_parts + (first >= 0 ? 1 : 0) * p.part_stride;
-    for (int i = tid; i < ncolv * (D / 4); i += kThreads) {
-      const int cc = i / (D / 4), f = (i - cc * (D / 4)) * 4;
-      Joined a;
-      a.clear();
-      for (int x = lo; x <= hi; ++x) {
-        const float* pp = x == last ? head_of(x) : tail_of(x);
-        a.add(pp[p.part_cols * D + cc], pp[p.part_cols * D + p.part_cols + cc],
-              *reinterpret_cast<const float4*>(pp + cc * D + f));
-      }
-      if (first >= 0 && last < kWarps) {
-        a.write(p, span, c_first + cc, f);
-      } else {
-        *reinterpret_cast<float4*>(to + cc * D + f) = a.o;
-        if (f == 0) {
-          to[p.part_cols * D + cc] = a.m;
-          to[p.part_cols * D + p.part_cols + cc] = a.l;
-        }
-      }
-    }
-  }
-  // units that span CTAs, the one the CTA begins in and the one it ends in
-  __syncthreads();
-  if (tid < 2) {
-    const int* span = sm.span[tid == 0 ? 0 : kWarps];
-    bool join = span[5] != 0 && (tid == 0 || !same_unit(0, kWarps));
-    if (join) {
-      // CTAs of the unit's first and last block
-      const int first = blockIdx.x - span[6], last = blockIdx.x + span[7];
-      join = first != last && arrive(p.counters + first) == (unsigned)(last - first);
-      if (join) p.counters[first] = 0u;  // ready for the next call
-      sm.of[tid][0] = first;
-      sm.of[tid][1] = last;
-    }
-    sm.last[tid] = join;
-  }
-  __syncthreads();
-#pragma unroll 1
-  for (int k = 0; k < 2; ++k)
-    if (sm.last[k]) join_ctas<D, COLS>(p, sm.span[k == 0 ? 0 : kWarps], sm.of[k], scratch);
-}
 
 // CTAs an SM holds at once (registers and shared memory allow that many).
 __host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }

@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kMaxPairs = 128;
 constexpr int kRopeThreads = 256;
+constexpr int kBatch = 4;  // heads whose rows a thread loads at once
 
 struct RopeParams {
   const void *q, *k;
@@ -111,40 +112,68 @@ __global__ void __launch_bounds__(kRopeThreads)
   const T* k = static_cast<const T*>(p.k) + (p.k ? b * p.sk.b_outer + n * p.sk.seq : 0);
   T* yq = static_cast<T*>(p.yq) + b * p.tq.b_outer + n * p.tq.seq;
   T* yk = static_cast<T*>(p.yk) + (p.k ? b * p.tk.b_outer + n * p.tk.seq : 0);
-#pragma unroll 4
-  for (int h = head0; h < head1; ++h) {
+  auto row = [&](int h, bool out) -> T* {
     const bool isq = h < p.Hq;
-    const T* x = isq ? q + h * p.sq.head : k + (h - p.Hq) * p.sk.head;
-    T* y = isq ? yq + h * p.tq.head : yk + (h - p.Hq) * p.tk.head;
+    if (out) return isq ? yq + h * p.tq.head : yk + (h - p.Hq) * p.tk.head;
+    return const_cast<T*>(isq ? q + h * p.sq.head : k + (h - p.Hq) * p.sk.head);
+  };
+  // all of a batch's loads before its first store (a row turned in place is read and
+  // written by the same thread)
+#pragma unroll 1
+  for (int h0 = head0; h0 < head1; h0 += kBatch) {
     if constexpr (VEC) {
-      const uint4 v0 = *reinterpret_cast<const uint4*>(x + at0);
-      if (!turns) {
-        *reinterpret_cast<uint4*>(y + at0) = v0;
-        continue;
-      }
-      const uint4 v1 = *reinterpret_cast<const uint4*>(x + at1);
-      float f[2][V], g[2][V];
-      unpack<T>(v0, f[0]);
-      unpack<T>(v1, f[1]);
+      uint4 v[kBatch][2];
 #pragma unroll
-      for (int i = 0; i < PAIRS; ++i) {
-        // element i of a pair list: (vector, place) of its two features
-        const int va = INTER ? 2 * i / V : 0, ia = INTER ? 2 * i % V : i;
-        const int vb = INTER ? va : 1, ib = INTER ? ia + 1 : i;
-        const float a = f[va][ia], c = f[vb][ib];
-        g[va][ia] = a * cs[i] - c * sn[i];
-        g[vb][ib] = c * cs[i] + a * sn[i];
+      for (int j = 0; j < kBatch; ++j)
+        if (h0 + j < head1) {
+          const T* x = row(h0 + j, false);
+          v[j][0] = *reinterpret_cast<const uint4*>(x + at0);
+          if (turns) v[j][1] = *reinterpret_cast<const uint4*>(x + at1);
+        }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (h0 + j >= head1) break;
+        T* y = row(h0 + j, true);
+        if (!turns) {
+          *reinterpret_cast<uint4*>(y + at0) = v[j][0];
+          continue;
+        }
+        float f[2][V], g[2][V];
+        unpack<T>(v[j][0], f[0]);
+        unpack<T>(v[j][1], f[1]);
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
+          // element i of a pair list: (vector, place) of its two features
+          const int va = INTER ? 2 * i / V : 0, ia = INTER ? 2 * i % V : i;
+          const int vb = INTER ? va : 1, ib = INTER ? ia + 1 : i;
+          const float a = f[va][ia], c = f[vb][ib];
+          g[va][ia] = a * cs[i] - c * sn[i];
+          g[vb][ib] = c * cs[i] + a * sn[i];
+        }
+        *reinterpret_cast<uint4*>(y + at0) = repack(g[0]);
+        *reinterpret_cast<uint4*>(y + at1) = repack(g[1]);
       }
-      *reinterpret_cast<uint4*>(y + at0) = repack(g[0]);
-      *reinterpret_cast<uint4*>(y + at1) = repack(g[1]);
     } else {
-      if (!turns) {
-        y[at0] = x[at0];
-        continue;
+      T v[kBatch][2];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (h0 + j < head1) {
+          const T* x = row(h0 + j, false);
+          v[j][0] = x[at0];
+          if (turns) v[j][1] = x[at1];
+        }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (h0 + j >= head1) break;
+        T* y = row(h0 + j, true);
+        if (!turns) {
+          y[at0] = v[j][0];
+          continue;
+        }
+        const float a = widen(v[j][0]), c = widen(v[j][1]);
+        narrow(y + at0, a * cs[0] - c * sn[0]);
+        narrow(y + at1, c * cs[0] + a * sn[0]);
       }
-      const float a = widen(x[at0]), c = widen(x[at1]);
-      narrow(y + at0, a * cs[0] - c * sn[0]);
-      narrow(y + at1, c * cs[0] + a * sn[0]);
     }
   }
 }
@@ -252,14 +281,17 @@ iha_status rotate(const char* name, bool back, const void* q, const void* k,
   const bool vec = rope->rot / 2 % V == 0;
   p.turning = vec ? rope->rot / 2 / V : rope->rot / 2;
   const int units = p.turning + (vec ? (d - rope->rot) / V : d - rope->rot);
+  // heads of a thread: its sines cost about as much as four heads' rows, so as many as
+  // leave half of the GPU's threads (3003 tokens x 40 heads of 96, fp32: 18.1 us, with two
+  // full waves left 26.3; 32768 tokens x 40 heads of 128, bf16: 110 us, one head 222)
   p.hg = 1;
-  const int64_t items = toks * p.H * units;
-  if (items > (1 << 30))
-    return fail(IHA_ERR_UNSUPPORTED, "%s: too many rows in one call", name);
+  while (p.hg < 8 && toks * p.H * units / (2 * p.hg) >= 1024 * (int64_t)sm_count()) p.hg *= 2;
   const int groups = (p.H + p.hg - 1) / p.hg;
   p.units.set(units);
   p.groups.set(groups);
   p.N.set(N);
+  if (toks * groups * units > (1 << 30))
+    return fail(IHA_ERR_UNSUPPORTED, "%s: too many rows in one call", name);
   p.items = (int)(toks * groups * units);
   const unsigned blocks = (unsigned)((p.items + kRopeThreads - 1) / kRopeThreads);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
