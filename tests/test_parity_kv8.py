@@ -595,6 +595,45 @@ def test_evictions(T, d, keep, recent):
             assert torch.equal(cache[pg], before[pg])
 
 
+@pytest.mark.parametrize("H,n,keep,recent", [
+    (2, 20000, 5000, 100), (2, 50000, 700, 0), (2, 50000, 45000, 20000), (2, 16389, 16388, 3),
+    (40, 9000, 4000, 4000), (160, 45000, 3000, 10), (160, 5000, 4999, 0)])
+@pytest.mark.parametrize("kind", ["close", "equal", "zeros", "spread", "misaligned"])
+def test_which_keys_stay_of_many(T, H, n, keep, recent, kind):
+    """The selection alone, by one and by several CTAs a head and past what they hold in
+    shared memory: weights that agree in their first 11 or 22 bits, all equal, mostly
+    zeros, of all sizes and signs."""
+    import torch
+    d, page = 32, 128
+    width, dw = -(-n // page), -(-keep // page)
+    cache = torch.zeros((width + dw, T.kv8_page_bytes(page, H, d)), dtype=torch.uint8, device="cuda")
+    table = torch.arange(width, dtype=torch.int32, device="cuda")[None].contiguous()
+    dest = (torch.arange(dw, dtype=torch.int32, device="cuda") + width)[None].contiguous()
+    g = S.rng(155)
+    cap = width * page
+    if kind == "close":
+        w = np.stack([1 + g.integers(0, 1 << 12, cap) * 2.0 ** -23,
+                      1 + g.random(cap) / 5] * (H // 2)).astype(np.float32)
+    elif kind == "equal":
+        w = np.full((H, cap), 0.25, np.float32)
+    elif kind == "zeros":
+        w = (g.random((H, cap)) * (g.random((H, cap)) < 0.01)).astype(np.float32)
+    else:
+        w = (g.standard_normal((H, cap)) * 10.0 ** g.integers(-30, 30, (H, cap))).astype(np.float32)
+    wd = torch.empty(H * cap + 4, device="cuda")
+    wd = wd[1:-3] if kind == "misaligned" else wd[:-4]
+    wd = wd.view(1, H, cap).copy_(to_dev(w)[None])
+    nl, kept, wo = T.kv8_evict(cache, table, ints([n]), wd, dest, H, d, page, keep, recent)
+    for h in sorted({0, 1, H // 2, H - 1}):
+        x = w[h, :n - recent].astype(np.float64)
+        ids = np.sort(np.argsort(-x, kind="stable")[:keep - recent])
+        ids = np.concatenate([ids, np.arange(n - recent, n)])
+        np.testing.assert_array_equal(kept[0, h].cpu().numpy(), ids)
+        np.testing.assert_array_equal(wo[0, h, :keep].cpu().numpy(), w[h, ids])
+        assert not wo[0, h, keep:].any()
+    assert nl.tolist() == [keep] and T.device_error() == 0
+
+
 def test_rows_behind_an_evicted_sequence_and_its_growth(T):
     """The last block's other rows are zeros; the shortened sequence grows on."""
     import torch

@@ -748,48 +748,69 @@ class Rope:
         check(lib().iha_rope_init(C.addressof(self._c)), "iha_rope_init")
         self.rot, self.gain = self._c.rot, self._c.mul
 
-
-def _strides4(t) -> Strides:
-    s = t.stride()
-    return Strides(s[0], 0, s[1], s[2])
+    @property
+    def _at(self) -> int:
+        return C.addressof(self._c)
 
 
 _NO_STRIDES = Strides(0, 0, 0, 0)
+_strides_of = {}  # of 4-D views, by their strides: never changed, so calls share them
+
+
+def _rows(t, name: str, shape, dtype, dev: int) -> Strides:
+    """_view for a 4-D view; its strides."""
+    if t.dtype is not dtype or t.get_device() != dev or dev < 0 or t.shape != shape:
+        _expect(t, name, shape, dtype, _torch().device("cuda", max(dev, 0)), contiguous=False)
+    s = t.stride()
+    r = _strides_of.get(s)
+    if r is None:
+        if s[3] != 1:
+            raise ValueError(f"{name}: the head dimension must be dense")
+        if len(_strides_of) >= 4096:
+            _strides_of.clear()
+        r = _strides_of[s] = Strides(s[0], 0, s[1], s[2])
+    return r
+
+
+def _make_like(t, stream):
+    """_make of t's shape and type."""
+    if stream is None and t.is_contiguous():
+        return _torch().empty_like(t)
+    return _make(t.shape, t.dtype, t, stream)
 
 
 def _rotate(fn, where, q, k, positions, rope, out, stream):
     if not isinstance(rope, Rope):
         raise TypeError("rope must be a Rope")
-    shape = q.shape
+    shape, dtype = q.shape, q.dtype
     if len(shape) != 4:
         raise ValueError(f"q must be [B, N, H, d], got {tuple(shape)}")
     B, N, Hq, d = shape
     dev, dt = q.get_device(), _dt(q)
-    _view(q, "q", shape, q.dtype, dev)
-    Hk = 0
+    sq = _rows(q, "q", shape, dtype, dev)
+    Hk, sk = 0, _NO_STRIDES
     if k is not None:
-        if k.dim() != 4:
-            raise ValueError(f"k must be [B, N, Hk, d], got {tuple(k.shape)}")
-        Hk = k.shape[2]
-        _view(k, "k", (B, N, Hk, d), q.dtype, dev)
+        kshape = k.shape
+        if len(kshape) != 4:
+            raise ValueError(f"k must be [B, N, Hk, d], got {tuple(kshape)}")
+        Hk = kshape[2]
+        sk = _rows(k, "k", (B, N, Hk, d), dtype, dev)
     if positions is not None:
         _dense(positions, "positions", (B, N), _torch().int32, dev)
     sp = _raw_stream(dev, stream)
     if out is None:
-        yq = _make(shape, q.dtype, q, stream)
-        yk = None if k is None else _make(k.shape, q.dtype, q, stream)
+        yq = _make_like(q, stream)
+        yk = None if k is None else _make_like(k, stream)
     else:
         if len(out) != 2 or (out[1] is None) != (k is None):
             raise ValueError("out must hold two tensors (q, k), the second None without k")
         yq, yk = out
-        _view(yq, "out[0]", shape, q.dtype, dev)
-        if yk is not None:
-            _view(yk, "out[1]", k.shape, q.dtype, dev)
+    syq = _rows(yq, "out[0]", shape, dtype, dev)
+    syk = sk if k is None else _rows(yk, "out[1]", kshape, dtype, dev)
     check(fn(q.data_ptr(), 0 if k is None else k.data_ptr(),
              0 if positions is None else positions.data_ptr(), yq.data_ptr(),
-             0 if k is None else yk.data_ptr(), C.addressof(rope._c), B, N, Hq, Hk, d, _strides4(q),
-             _NO_STRIDES if k is None else _strides4(k), _strides4(yq),
-             _NO_STRIDES if k is None else _strides4(yk), dt, sp), where)
+             0 if k is None else yk.data_ptr(), rope._at, B, N, Hq, Hk, d, sq, sk, syq, syk, dt,
+             sp), where)
     return yq, yk
 
 
@@ -850,8 +871,7 @@ def kv8_append(k, v, block_table, seq_lens, cache, page: int, counts=None, strea
         raise ValueError(f"k and v must be [B, N, Hkv, d], got {tuple(shape)}")
     B, N, Hkv, d = shape
     dev, dt = k.get_device(), _dt(k)
-    _view(k, "k", shape, k.dtype, dev)
-    _view(v, "v", shape, k.dtype, dev)
+    sk, sv = _rows(k, "k", shape, k.dtype, dev), _rows(v, "v", shape, k.dtype, dev)
     width = _table(block_table, "block_table", B, dev)
     _dense(seq_lens, "seq_lens", (B,), torch.int32, dev)
     if counts is not None:
@@ -860,7 +880,7 @@ def kv8_append(k, v, block_table, seq_lens, cache, page: int, counts=None, strea
     check((_lib or lib()).kv8_append(
         k.data_ptr(), v.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
         0 if counts is None else counts.data_ptr(), cache.data_ptr(), B, N, n_pages, page, width,
-        Hkv, d, _strides4(k), _strides4(v), dt, _raw_stream(dev, stream)), "kv8_append")
+        Hkv, d, sk, sv, dt, _raw_stream(dev, stream)), "kv8_append")
     return cache
 
 
@@ -921,15 +941,14 @@ def mha_fwd_kv8(q, cache, block_table, seq_lens, Hkv: int, page: int, mask: int 
         raise ValueError("q must be [B, Nq, Hq, d]")
     B, Nq, Hq, d = shape
     dev = q.get_device()
-    _view(q, "q", shape, torch.bfloat16, dev)
+    sq = _rows(q, "q", shape, torch.bfloat16, dev)
     n_pages = _kv8_pages(cache, page, Hkv, d, dev)
     width = _table(block_table, "block_table", B, dev)
     _dense(seq_lens, "seq_lens", (B,), torch.int32, dev)
     sp = _raw_stream(dev, stream)
     if out is None:
-        out = _make(shape, torch.bfloat16, q, stream)
-    else:
-        _view(out, "out", shape, torch.bfloat16, dev)
+        out = _make_like(q, stream)
+    so = _rows(out, "out", shape, torch.bfloat16, dev)
     if lse is not None:
         _dense(lse, "lse", (B, Hq, Nq), torch.float32, dev)
     elif return_lse:
@@ -958,7 +977,7 @@ def mha_fwd_kv8(q, cache, block_table, seq_lens, Hkv: int, page: int, mask: int 
         out.data_ptr(), 0 if lse is None else lse.data_ptr(),
         0 if weights is None else weights.data_ptr(),
         0 if weights is None else weights_out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-        B, Nq, Hq, Hkv, d, n_pages, page, width, _strides4(q), _strides4(out), scale, mask, window,
+        B, Nq, Hq, Hkv, d, n_pages, page, width, sq, so, scale, mask, window,
         BF16, sp), "mha_fwd_kv8")
     if not return_lse and weights is None:
         return out

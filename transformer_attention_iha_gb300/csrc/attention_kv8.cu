@@ -20,6 +20,9 @@
 #include <cuda_fp16.h>
 
 #include "kv8.cuh"
+// Unit cost, on 16 ragged sequences of 1 to 8192 keys and 8 key heads, 16 columns: 2 53.8
+// us, 4 43.8, 6 36.2, 9 35.7, 14 35.0; 131071 keys x 80 heads 407 to 411.
+#define IHA_KV_UNIT_COST 14
 #include "kv_attn.cuh"
 
 namespace iha {
@@ -588,6 +591,48 @@ __device__ __forceinline__ void note_span(LineSmem& sm, const Unit& u, int warp,
     }
 }
 
+// join_ctas for units of many columns: I items of a thread, U parts of each, on their way
+// together (a join waits for memory: 16 columns of 128 features, 7 parts, ...).
+template <int D, int COLS>
+__device__ __forceinline__ void join_wide(const KvAttnParams& p, const int* span, const int* of,
+                                          float* scratch) {
+  const int c_first = span[2] * COLS, first = of[0], last = of[1];
+  const int items = min(COLS, p.ncols - c_first) * (D / 4);
+  if (COLS * D / 4 <= kThreads || items <= kThreads) {
+    join_ctas<D, COLS>(p, span, of, scratch);
+    return;
+  }
+  constexpr int I = COLS * D / 4 > 2 * kThreads ? 4 : 2, U = I == 4 ? 4 : 8;
+  for (int i0 = threadIdx.x; i0 < items; i0 += I * kThreads) {
+    Joined a[I];
+#pragma unroll
+    for (int i = 0; i < I; ++i) a[i].clear();
+    for (int c0 = first; c0 <= last; c0 += U) {
+      float m[I][U], l[I][U];
+      float4 o[I][U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int c = min(c0 + k, last);
+        const float* pp = p.parts + ((int64_t)c * kCtaParts + (c == first ? 1 : 0)) * p.part_stride;
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+          const int at = min(i0 + i * kThreads, items - 1), cc = at / (D / 4);
+          m[i][k] = c0 + k <= last ? __ldcg(pp + p.part_cols * D + cc) : -INFINITY;
+          l[i][k] = c0 + k <= last ? __ldcg(pp + p.part_cols * D + p.part_cols + cc) : 0.f;
+          o[i][k] = __ldcg(reinterpret_cast<const float4*>(pp + 4 * at));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < I; ++i) a[i].add(m[i], l[i], o[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int at = i0 + i * kThreads, cc = at / (D / 4);
+      if (at < items) a[i].write(p, span, c_first + cc, (at - cc * (D / 4)) * 4);
+    }
+  }
+}
+
 // Units that span warps: joins this CTA's parts, and, of a unit that spans CTAs, all of
 // them in the CTA that arrives last (all threads call).  head_of, tail_of: a warp's part
 // of a unit that ends in its stretch after beginning before it, and of one that goes on.
@@ -609,22 +654,38 @@ __device__ __forceinline__ void join_units(const KvAttnParams& p, LineSmem& sm, 
     const int c_first = span[2] * COLS, ncolv = min(COLS, p.ncols - c_first);
     const int lo = max(first, 0), hi = min(last, kWarps - 1);
     float* to = cta_parts + (first >= 0 ? 1 : 0) * p.part_stride;
-    for (int i = tid; i < ncolv * (D / 4); i += kThreads) {
-      const int cc = i / (D / 4), f = (i - cc * (D / 4)) * 4;
-      Joined a;
-      a.clear();
+    constexpr int I = COLS * D / 4 > 2 * kThreads ? 4 : COLS * D / 4 > kThreads ? 2 : 1;
+    const int items = ncolv * (D / 4);
+    for (int i0 = tid; i0 < items; i0 += I * kThreads) {  // I items of a thread at once
+      Joined a[I];
+#pragma unroll
+      for (int i = 0; i < I; ++i) a[i].clear();
       for (int x = lo; x <= hi; ++x) {
         const float* pp = x == last ? head_of(x) : tail_of(x);
-        a.add(pp[p.part_cols * D + cc], pp[p.part_cols * D + p.part_cols + cc],
-              *reinterpret_cast<const float4*>(pp + cc * D + f));
+        float m[I], l[I];
+        float4 o[I];
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+          const int at = min(i0 + i * kThreads, items - 1), cc = at / (D / 4);
+          m[i] = pp[p.part_cols * D + cc];
+          l[i] = pp[p.part_cols * D + p.part_cols + cc];
+          o[i] = *reinterpret_cast<const float4*>(pp + 4 * at);
+        }
+#pragma unroll
+        for (int i = 0; i < I; ++i) a[i].add(m[i], l[i], o[i]);
       }
-      if (first >= 0 && last < kWarps) {
-        a.write(p, span, c_first + cc, f);
-      } else {
-        *reinterpret_cast<float4*>(to + cc * D + f) = a.o;
-        if (f == 0) {
-          to[p.part_cols * D + cc] = a.m;
-          to[p.part_cols * D + p.part_cols + cc] = a.l;
+#pragma unroll
+      for (int i = 0; i < I; ++i) {
+        const int at = i0 + i * kThreads, cc = at / (D / 4), f = (at - cc * (D / 4)) * 4;
+        if (at >= items) break;
+        if (first >= 0 && last < kWarps) {
+          a[i].write(p, span, c_first + cc, f);
+        } else {
+          *reinterpret_cast<float4*>(to + cc * D + f) = a[i].o;
+          if (f == 0) {
+            to[p.part_cols * D + cc] = a[i].m;
+            to[p.part_cols * D + p.part_cols + cc] = a[i].l;
+          }
         }
       }
     }
@@ -647,7 +708,7 @@ __device__ __forceinline__ void join_units(const KvAttnParams& p, LineSmem& sm, 
   __syncthreads();
 #pragma unroll 1
   for (int k = 0; k < 2; ++k)
-    if (sm.last[k]) join_ctas<D, COLS>(p, sm.span[k == 0 ? 0 : kWarps], sm.of[k], scratch);
+    if (sm.last[k]) join_wide<D, COLS>(p, sm.span[k == 0 ? 0 : kWarps], sm.of[k], scratch);
 }
 
 // ---- the kernel
@@ -784,6 +845,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
       ring.drain(p);
     }
   }
+  launch_dependents();  // the weights' CTAs may come; they wait for this grid's end
   join_units<D, COLS>(p, sm.line, head_of, tail_of, cta_parts, reinterpret_cast<float*>(sm.ring));
 }
 
@@ -803,18 +865,21 @@ template <bool VEC>
 __global__ void __launch_bounds__(kWeighKeys / 4) kv8_weigh_kernel(const WeighParams p) {
   const int plane = blockIdx.x / p.chunks, b = plane / p.a.Hkv, hk = plane - b * p.a.Hkv;
   const int j = ((int)blockIdx.x - plane * p.chunks) * kWeighKeys + 4 * (int)threadIdx.x;
-  if (j >= p.cap) return;
   const int len = seq_len(p.a, b);
   const int64_t at = plane * p.cap + j;
-  if (j >= len && p.weights == p.out) return;
-  float w[4], sum[4] = {0.f, 0.f, 0.f, 0.f};
-  if (VEC) {
-    const float4 v = *reinterpret_cast<const float4*>(p.weights + at);
-    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-  } else {
+  float w[4] = {0.f, 0.f, 0.f, 0.f}, sum[4] = {0.f, 0.f, 0.f, 0.f};
+  const bool idle = j >= p.cap || (j >= len && p.weights == p.out);
+  if (!idle) {
+    if (VEC) {
+      const float4 v = *reinterpret_cast<const float4*>(p.weights + at);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = p.weights[at + i];
+      for (int i = 0; i < 4; ++i) w[i] = p.weights[at + i];
+    }
   }
+  wait_for_grid();
+  if (idle) return;
   for (int col = 0; j < len && col < p.a.ncols; ++col) {
     int lo, hi;
     col_range(p.a, len, col, lo, hi);
@@ -939,11 +1004,9 @@ iha_status mha_fwd_kv8(const void* q, const void* cache, const int32_t* block_ta
   const WeighParams w = {p, p.scores, weights, weights_out, cap,
                          (int)((cap + kWeighKeys - 1) / kWeighKeys)};
   const unsigned ctas = (unsigned)(B * Hkv * w.chunks);
-  if (aligned16(weights) && aligned16(weights_out))
-    kv8_weigh_kernel<true><<<ctas, kWeighKeys / 4, 0, s>>>(w);
-  else
-    kv8_weigh_kernel<false><<<ctas, kWeighKeys / 4, 0, s>>>(w);
-  return check_launch(name);
+  return launch_behind(name, aligned16(weights) && aligned16(weights_out) ? kv8_weigh_kernel<true>
+                                                                          : kv8_weigh_kernel<false>,
+                       ctas, kWeighKeys / 4, s, w);
 }
 
 }  // extern "C"

@@ -93,6 +93,25 @@ class SmemLimit {
   std::mutex mu_;
 };
 
+// Launches a kernel that calls wait_for_grid() before it uses what the launch before it on
+// the stream writes; its launch then costs no time of its own.
+template <typename P>
+iha_status launch_behind(const char* what, void (*kernel)(P), unsigned grid, unsigned block,
+                         cudaStream_t stream, const P& p) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  if (e != cudaSuccess) return fail(IHA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+  return check_launch(what);
+}
+
 #define IHA_DEVICE_ERROR_WORD(tag)                                              \
   static __device__ unsigned int g_dev_error;                                   \
   static int tag##_read_dev_error(int clear) {                                  \
@@ -133,6 +152,16 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
+}
+
+// ---- a kernel that is launched before the one it needs has ended (launch_behind): the
+// earlier grid's CTAs let it come, it waits until all of them have ended and what they
+// wrote can be read.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_grid() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---- mbarrier

@@ -8,11 +8,11 @@
 // these are rounded again.  A lane takes 16 bytes of a row at a time, so every access
 // is whole sectors.
 //
-// Load: a thread writes 16 bytes of a K row and of a V row.
+// Load: a thread writes two vectors of 16 bytes of a K row and of a V row.
 //
 // Both move bytes: a token and head of d features is 4 d bytes of bf16 and 2 d + 1
 // of cache.
-#include <cuda_fp16.h>
+#include <type_traits>
 
 #include "kv8.cuh"
 
@@ -181,14 +181,15 @@ struct LoadParams {
   const int32_t* slots;
   void *k, *v;
   iha_strides sk, sv;
-  FastDiv units, heads, N, Bi, page;  // 16-byte units of a row; heads; as kv4_load
+  FastDiv heads, N, Bi, page;  // heads; as kv4_load
   int64_t items;
   int n_slots, bpp;
 };
 
-// 16 bytes of values from codes: 8 bf16 (the products are exact), 4 fp32.
-__device__ __forceinline__ uint4 decode(const uint8_t* from, float s, bool nan, __nv_bfloat16) {
-  const uint2 c = *reinterpret_cast<const uint2*>(from);
+// Codes of 16 bytes of values: 8 bf16 (the products are exact), 4 fp32.
+template <typename T>
+using Codes = typename std::conditional<sizeof(T) == 2, uint2, uint32_t>::type;
+__device__ __forceinline__ uint4 decode(uint2 c, float s, bool nan) {
   uint32_t v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -198,8 +199,7 @@ __device__ __forceinline__ uint4 decode(const uint8_t* from, float s, bool nan, 
   }
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
-__device__ __forceinline__ uint4 decode(const uint8_t* from, float s, bool nan, float) {
-  const uint32_t c = *reinterpret_cast<const uint32_t*>(from);
+__device__ __forceinline__ uint4 decode(uint32_t c, float s, bool nan) {
   uint32_t v[4];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -211,32 +211,47 @@ __device__ __forceinline__ uint4 decode(const uint8_t* from, float s, bool nan, 
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
+// A thread: two vectors of a row, half a row apart (a warp's stores are whole sectors).
 template <typename T, int D>
 __global__ void __launch_bounds__(256) kv8_load_kernel(const LoadParams p) {
-  constexpr int V = 16 / sizeof(T);
+  constexpr int V = 16 / sizeof(T), TPR = D / V / 2;  // threads of a row
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (id >= p.items) return;
-  const int row = (int)(id / (D / V)), c = (int)(id - (int64_t)row * (D / V));
+  const int row = (int)(id / TPR), c = (int)(id - (int64_t)row * TPR);
   const int tok = p.heads.div(row), head = row - tok * p.heads.d;
   const int slot = __ldg(p.slots + tok);
   const bool in = slot >= 0 && slot < p.n_slots;
   if (!in && slot != -1) atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
-  uint4 k = make_uint4(0, 0, 0, 0), v = k;
+  uint4 k[2], v[2];
+  k[0] = k[1] = v[0] = v[1] = make_uint4(0, 0, 0, 0);
   if (in) {
     const int pg = p.page.div(slot), off = slot - pg * p.page.d, r = off % kKv8Tok;
     const uint8_t* blk = p.cache + kv8_block_of(pg, off / kKv8Tok, head, p.heads.d, p.bpp, D);
     const Kv8Tail t = kv8_tail(blk, D);
-    const uint8_t* at = blk + r * D + (((c * V / 16) ^ kv8_swap(D, r)) * 16 + c * V % 16);
-    k = decode(at, t.scale[0], (t.nan >> r) & 1u, T());
-    v = decode(at + kKv8Tok * D, t.scale[1], (t.nan >> (16 + r)) & 1u, T());
+    Codes<T> ck[2], cv[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int f = (c + q * TPR) * V;  // the vector's first feature
+      const uint8_t* at = blk + r * D + (((f / 16) ^ kv8_swap(D, r)) * 16 + f % 16);
+      ck[q] = *reinterpret_cast<const Codes<T>*>(at);
+      cv[q] = *reinterpret_cast<const Codes<T>*>(at + kKv8Tok * D);
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      k[q] = decode(ck[q], t.scale[0], (t.nan >> r) & 1u);
+      v[q] = decode(cv[q], t.scale[1], (t.nan >> (16 + r)) & 1u);
+    }
   }
   const int b = p.N.div(tok), n = tok - b * p.N.d, bo = p.Bi.div(b), bi = b - bo * p.Bi.d;
-  auto to = [&](void* y, const iha_strides& s) {
-    return reinterpret_cast<uint4*>(static_cast<T*>(y) + bo * s.b_outer + bi * s.b_inner +
-                                    n * s.seq + head * s.head + c * V);
-  };
-  *to(p.k, p.sk) = k;
-  *to(p.v, p.sv) = v;
+  T* yk = static_cast<T*>(p.k) + bo * p.sk.b_outer + bi * p.sk.b_inner + n * p.sk.seq +
+          head * p.sk.head + c * V;
+  T* yv = static_cast<T*>(p.v) + bo * p.sv.b_outer + bi * p.sv.b_inner + n * p.sv.seq +
+          head * p.sv.head + c * V;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    *reinterpret_cast<uint4*>(yk + q * TPR * V) = k[q];
+    *reinterpret_cast<uint4*>(yv + q * TPR * V) = v[q];
+  }
 }
 
 // Checks of k, v views that append and load share; strides of extents of 1 become 0.
@@ -395,13 +410,13 @@ iha_status kv8_load(const void* cache, const int32_t* slots, void* k, void* v, i
   p.N.set(N);
   p.Bi.set(B_inner);
   p.page.set(page);
-  p.units.set(d * es / 16);
-  p.items = rows * p.units.d;
+  p.items = rows * (d * es / 32);
   p.n_slots = n_pages * page;
   p.bpp = page / kKv8Tok;
-  if ((p.items + 255) / 256 > INT32_MAX)
+  const int64_t ctas = (p.items + 255) / 256;
+  if (ctas > INT32_MAX)
     return fail(IHA_ERR_UNSUPPORTED, "%s: too many rows in one call", name);
-  const unsigned grid = (unsigned)((p.items + 255) / 256);
+  const unsigned grid = (unsigned)ctas;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   IHA_KV8_D_SWITCH(d, {
     if (dt == IHA_BF16)

@@ -1,13 +1,15 @@
 // Eviction from the 8-bit cache by the attention weight that keys have gathered
 // (kv8_evict; layout of the cache: kv8.cuh).
 //
-// Two launches.  Select, a CTA per sequence and head: the weights as integers in their
+// Two launches.  Select, one or several CTAs per sequence and head: the weights as integers in their
 // order (a float's bits, the negative ones turned round), held in shared memory, the
-// smallest kept one found from counts of 11 bits at a time (a radix select), then the
-// kept ones in the order of their positions: each warp counts its stretch of keys, the
-// counts are summed over the warps, each warp writes its own.  Copy, a warp per block of 16 kept rows of a head: rows are
-// gathered whole, 16 bytes a lane, rounded again where their block's scale is not
-// the largest of the sixteen.
+// smallest kept one found from counts of 11 bits at a time (a radix select; those that
+// share its first digit are listed, and only they are looked at again), then the kept ones
+// written in the order of their positions, 4096 keys at a time by a scan over the CTA.  Few
+// heads of many keys have a cluster of CTAs each, that read one another's counts.
+// Copy, a warp per block of 16 kept rows of a head: a lane finds where a row is, then the
+// rows are gathered whole, 16 bytes a lane, and rounded again where their block's scale is not the
+// largest of its sixteen.
 #include "kv8.cuh"
 
 namespace iha {
@@ -31,76 +33,169 @@ struct EvictParams {
 };
 
 // Larger weights as larger numbers; NaN as the lowest, -0 as 0.
+constexpr uint32_t kLowest = 0x007FFFFFu;  // of -inf, and of NaN
+__device__ __forceinline__ float weight_of(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
 __device__ __forceinline__ uint32_t order_of(float w) {
   if (w != w) w = -INFINITY;
   const uint32_t u = __float_as_uint(w + 0.f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-constexpr int kDigit = 11, kBins = 1 << kDigit;  // three digits: 11, 11 and 10 bits
-constexpr int kCached = 48 * 1024;  // keys whose numbers stay in shared memory
+constexpr int kBins = 2048;        // three digits: 11, 11 and 10 bits
+constexpr int kReplicas = 4;       // of the counts, by lane: neighbours count apart
+constexpr int kReplica = kBins + 8;  // from one to the next, in other banks
+constexpr int kList = 4096;        // keys that share the first digit of the smallest kept
+constexpr int kCached = 40 * 1024;  // keys of a CTA whose numbers stay in shared memory
+constexpr int kChunk = 4 * kThreads;
+// counts, [2][kBins] counts of the whole CTA, the list; and 4 bytes a cached key
+constexpr int kSelectSmem = (kReplicas * kReplica + 2 * kBins + kList) * 4;
 
+__device__ __forceinline__ int cluster_rank() {
+  int r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ int cluster_size() {
+  int r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+// A word of shared memory, of the cluster's CTA `rank`.
+__device__ __forceinline__ int load_of(int rank, const int* p) {
+  uint32_t a = smem_u32(p);
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(a) : "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// A cluster per sequence and head, each CTA a stretch of its keys.  VEC: weights on 16 bytes.
+template <bool VEC>
 __global__ void __launch_bounds__(kThreads, 1) kv8_select_kernel(const EvictParams p) {
-  extern __shared__ uint32_t held[];
-  __shared__ int hist[kBins];
-  __shared__ int count[2][kWarps];
-  __shared__ int found[3];  // the digit, how many of it are kept, how many have it
+  extern __shared__ uint4 smem[];
+  int* const hist = reinterpret_cast<int*>(smem);
+  int* const bins = hist + kReplicas * kReplica;
+  uint32_t* const list = reinterpret_cast<uint32_t*>(bins + 2 * kBins);
+  uint32_t* const held = list + kList;
+  __shared__ int totals[2][kWarps];
+  __shared__ int found[3];   // the digit, how many of it are kept, how many have it
+  __shared__ int sums[3];    // this CTA's: above the digits so far, equal to all, listed
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int plane = blockIdx.x, b = plane / p.H, h = plane - b * p.H;
+  const int size = cluster_size(), rank = cluster_rank();
+  const int plane = blockIdx.x / size, b = plane / p.H, h = plane - b * p.H;
   const int raw = __ldg(p.lens + b), n = min(max(raw, 0), (int)p.cap);
-  if (raw != n && h == 0 && tid == 0) atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
+  const bool writer = rank == 0 && tid == 0 && h == 0;
+  if (raw != n && writer) atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
   const int m = min(n, p.keep);
-  if (h == 0 && tid == 0) p.new_lens[b] = m;
+  if (writer) p.new_lens[b] = m;
   const float* w = p.weights + plane * p.cap;
   int32_t* kept = p.kept + (int64_t)plane * p.keep;
   float* out = p.weights_out ? p.weights_out + plane * p.dest_cap : nullptr;
-  for (int i = m + tid; i < p.keep; i += kThreads) kept[i] = -1;
+  const int all_tid = rank * kThreads + tid, all_threads = size * kThreads;
+  for (int i = m + all_tid; i < p.keep; i += all_threads) kept[i] = -1;
   if (out)
-    for (int64_t i = m + tid; i < p.dest_cap; i += kThreads) out[i] = 0.f;
-  const int older = n > p.keep ? n - p.recent : 0;  // keys [0, older) compete
-  int need = n > p.keep ? p.keep - p.recent : 0;
-  uint32_t low = 0;  // the smallest kept weight, in order_of's numbers
-  auto number = [&](int j) { return j < kCached ? held[j] : order_of(__ldg(w + j)); };
+    for (int64_t i = m + all_tid; i < p.dest_cap; i += all_threads) out[i] = 0.f;
+  // keys [0, older) compete for `need` places; this CTA has keys [first, end)
+  const bool all = n <= p.keep;
+  const int older = all ? 0 : n - p.recent;
+  int need = all ? 0 : p.keep - p.recent;
+  const int per = ((n + size - 1) / size + 127) & ~127;
+  const int first = min(n, rank * per), end = min(n, first + per), mine = min(end, older);
+  // kept: numbers above `low`, and the first `need` of those that equal it
+  uint32_t low = ~0u;
+  // four numbers from key j on, j a multiple of 4; what lies past `mine` means nothing
+  auto numbers = [&](int j, uint32_t (&u)[4], bool fresh) {
+    const bool cached = j + 4 - first <= kCached;
+    if (!fresh && cached) {
+      const uint4 v = *reinterpret_cast<const uint4*>(held + (j - first));
+      u[0] = v.x, u[1] = v.y, u[2] = v.z, u[3] = v.w;
+      return;
+    }
+    float x[4];
+    if (VEC) {  // rows are whole pages, so the vector lies within them
+      const float4 v = __ldg(reinterpret_cast<const float4*>(w + j));
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = __ldg(w + j + i);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = order_of(x[i]);
+    if (fresh && cached)
+      *reinterpret_cast<uint4*>(held + (j - first)) = make_uint4(u[0], u[1], u[2], u[3]);
+  };
+  if (tid < 3) sums[tid] = 0;
   if (need > 0) {
-    for (int j = tid; j < min(older, kCached); j += kThreads) held[j] = order_of(__ldg(w + j));
+    low = 0;
+    bool has_list = false;
 #pragma unroll 1
-    for (int shift = 32 - kDigit; ; shift = max(0, shift - kDigit)) {
-      const int upto = shift == 32 - kDigit ? 32 : shift == 0 ? 32 - 2 * kDigit : shift + kDigit;
-      const uint32_t mask = (1u << (upto - shift)) - 1u;
-      for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const int up = pass == 1 ? 21 : 10;  // of the digits before
+      const uint32_t mask = pass < 2 ? 2047u : 1023u;
+      const int replicas = has_list ? 1 : kReplicas;
+      for (int i = tid; i < replicas * kReplica; i += kThreads) hist[i] = 0;
       __syncthreads();
-      for (int j0 = warp * 32; j0 < older; j0 += kThreads) {
-        const int j = j0 + lane;
-        const uint32_t u = j < older ? number(j) : 0u;
-        const bool in = j < older && (upto == 32 || (u >> upto) == (low >> upto));
-        const uint32_t who = __ballot_sync(0xffffffffu, in);
-        if (who == 0) continue;
-        const int digit = (int)((u >> shift) & mask);
-        // equal weights (zeros, most often) would add to one counter 32 times
-        const int first = __shfl_sync(0xffffffffu, digit, __ffs(who) - 1);
-        if (__all_sync(0xffffffffu, !in || digit == first)) {
-          if (lane == 0) atomicAdd(&hist[first], __popc(who));
-        } else if (in) {
-          atomicAdd(&hist[digit], 1);
+      int* const count = hist + (lane & (replicas - 1)) * kReplica;
+      if (has_list) {
+        const int listed = sums[2];
+        for (int j = tid; j < listed; j += kThreads)
+          if (list[j] >> up == low >> up) atomicAdd(&count[(list[j] >> shift) & mask], 1);
+      } else {
+#pragma unroll 4
+        for (int j = first + 4 * tid; j < mine; j += kChunk) {
+          uint32_t u[4];
+          numbers(j, u, pass == 0);
+          if (pass == 0 && j + 4 <= mine && (u[0] >> 21) == (u[1] >> 21) &&
+              (u[0] >> 21) == (u[2] >> 21) && (u[0] >> 21) == (u[3] >> 21)) {
+            atomicAdd(&count[u[0] >> 21], 4);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (j + i < mine && (pass == 0 || u[i] >> up == low >> up))
+                atomicAdd(&count[(u[i] >> shift) & mask], 1);
+          }
         }
       }
       __syncthreads();
-      // from the largest digit down: the one at which `need` is reached
+      // this CTA's counts, then the cluster's, from the largest digit down
       constexpr int PER = kBins / kThreads;
-      int c[PER], sum = 0;
+      int c[PER], own[PER], sum = 0;
+      int* const my_bins = bins + (pass & 1) * kBins;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) sum += c[i] = hist[kBins - 1 - (PER * tid + i)];
+      for (int i = 0; i < PER; ++i) {
+        const int bin = kBins - 1 - (PER * tid + i);
+        own[i] = 0;
+        for (int k = 0; k < replicas; ++k) own[i] += hist[k * kReplica + bin];
+        my_bins[bin] = own[i];
+        c[i] = own[i];
+      }
+      if (size > 1) {
+        cluster_sync();
+        for (int k = 1; k < size; ++k)
+#pragma unroll
+          for (int i = 0; i < PER; ++i)
+            c[i] += load_of((rank + k) & (size - 1), my_bins + kBins - 1 - (PER * tid + i));
+      }
+#pragma unroll
+      for (int i = 0; i < PER; ++i) sum += c[i];
       int incl = sum;
 #pragma unroll
       for (int k = 1; k < 32; k <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, k);
         if (lane >= k) incl += v;
       }
-      if (lane == 31) count[0][warp] = incl;
+      if (lane == 31) totals[0][warp] = incl;
       __syncthreads();
-      for (int k = 0; k < warp; ++k) incl += count[0][k];
-      int before = incl - sum;
-      if (before < need && incl >= need)
+      int before = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? totals[0][lane] : 0);
+      // the one at which `need` is reached
+      if (before < need && before + sum >= need)
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
           if (before < need && before + c[i] >= need) {
@@ -111,60 +206,94 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_select_kernel(const EvictPara
           before += c[i];
         }
       __syncthreads();
-      low |= (uint32_t)found[0] << shift;
-      need = found[1];  // of those equal so far
-      if (shift == 0 || found[2] == need) break;  // all that have the digits so far are kept
+      const int digit = found[0], same = found[2];
+      low |= (uint32_t)digit << shift;
+      need = found[1];
+      const bool whole = same == need;  // all that have the digits so far are kept
+      int gt = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int bin = kBins - 1 - (PER * tid + i);
+        if (bin > digit || (whole && bin == digit)) gt += own[i];
+        if (!whole && pass == 2 && bin == digit) sums[1] = own[i];
+      }
+      gt = __reduce_add_sync(0xffffffffu, gt);
+      if (lane == 0 && gt != 0) atomicAdd(&sums[0], gt);
+      if (whole) {  // (low is above 0: no number is below that of -inf)
+        low -= 1;
+        need = 0;
+        break;
+      }
+      if (pass == 0 && same <= kList) {
+        has_list = true;
+        for (int j0 = first + 4 * (warp * 32); j0 < mine; j0 += kChunk) {
+          const int j = j0 + 4 * lane;
+          uint32_t u[4] = {0, 0, 0, 0};
+          if (j < mine) numbers(j, u, false);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool in = j + i < mine && u[i] >> 21 == low >> 21;
+            const uint32_t who = __ballot_sync(0xffffffffu, in);
+            if (who == 0) continue;
+            int to = 0;
+            if (lane == 0) to = atomicAdd(&sums[2], __popc(who));
+            to = __shfl_sync(0xffffffffu, to, 0) + __popc(who & ((1u << lane) - 1u));
+            if (in) list[to] = u[i];
+          }
+        }
+        __syncthreads();
+      }
     }
+  }
+  launch_dependents();  // the copy's CTAs may come; they wait for this grid's end
+  // the kept ones in order: key j goes to (those above `low` before it) + (those equal to
+  // it before it, of which the first `need` are kept)
+  int above = max(0, first - older), equal = 0;  // before this CTA's keys
+  if (size > 1) {
+    cluster_sync();
+    for (int k = 0; k < rank; ++k) {
+      above += load_of(k, &sums[0]);
+      equal += load_of(k, &sums[1]);
+    }
+  }
+  for (int j0 = first, buf = 0; j0 < end; j0 += kChunk, buf ^= 1) {
+    const int j = j0 + 4 * tid;
+    uint32_t u[4] = {0, 0, 0, 0};
+    if (j < mine) numbers(j, u, false);
+    int kinds = 0;  // above in the low half, equal in the high
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool in = j + i < mine;
+      kinds += (in ? u[i] > low : j + i < end) ? 1 : in && u[i] == low ? 1 << 16 : 0;
+    }
+    int incl = kinds;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, k);
+      if (lane >= k) incl += v;
+    }
+    if (lane == 31) totals[buf][warp] = incl;
     __syncthreads();
-  }
-  // each warp's stretch of keys: how many are above `low`, how many equal it
-  const bool all = n <= p.keep;
-  const int per = ((n + kWarps - 1) / kWarps + 31) & ~31;
-  const int j0 = min(n, warp * per), j1 = min(n, j0 + per);
-  int above = 0, equal = 0;
-  for (int j = j0 + lane; j < j1; j += 32) {
-    if (all || j >= older) {
-      ++above;
-    } else if (p.keep > p.recent) {
-      const uint32_t u = number(j);
-      above += u > low;
-      equal += u == low;
+    const int t = lane < kWarps ? totals[buf][lane] : 0;
+    const int before = incl - kinds + __reduce_add_sync(0xffffffffu, lane < warp ? t : 0);
+    const int chunk = __reduce_add_sync(0xffffffffu, t);
+    int ab = above + (before & 0xFFFF), eq = equal + (before >> 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool in = j + i < mine, is_equal = in && u[i] == low;
+      const bool is_above = in ? u[i] > low : j + i < end;
+      if (is_above || (is_equal && eq < need)) {
+        const int to = ab + min(eq, need);
+        kept[to] = j + i;
+        if (out) out[to] = !in || u[i] == kLowest ? __ldg(w + j + i) : weight_of(u[i]);
+      }
+      ab += is_above;
+      eq += is_equal;
     }
+    above += chunk & 0xFFFF;
+    equal += chunk >> 16;
   }
-  above = __reduce_add_sync(0xffffffffu, above);
-  equal = __reduce_add_sync(0xffffffffu, equal);
-  if (lane == 0) {
-    count[0][warp] = above;
-    count[1][warp] = equal;
-  }
-  __syncthreads();
-  int at = 0, eq = 0;  // kept ones, equal ones before this warp's
-  for (int k = 0; k < warp; ++k) {
-    at += count[0][k];
-    eq += count[1][k];
-  }
-  at += min(eq, need);
-  const uint32_t below = (1u << lane) - 1u;
-  for (int j = j0; j < j1; j += 32) {
-    const int i = j + lane;
-    const bool in = i < j1;
-    bool is_above = in && (all || i >= older), is_equal = false;
-    if (in && !is_above && p.keep > p.recent) {
-      const uint32_t u = number(i);
-      is_above = u > low;
-      is_equal = u == low;
-    }
-    const uint32_t me = __ballot_sync(0xffffffffu, is_equal);
-    const bool take = is_above || (is_equal && eq + __popc(me & below) < need);
-    const uint32_t mt = __ballot_sync(0xffffffffu, take);
-    if (take) {
-      const int to = at + __popc(mt & below);
-      kept[to] = i;
-      if (out) out[to] = __ldg(w + i);
-    }
-    at += __popc(mt);
-    eq += __popc(me);
-  }
+  if (size > 1) cluster_sync();  // the others have read this CTA's sums
 }
 
 template <int D>
@@ -177,7 +306,9 @@ __global__ void __launch_bounds__(256) kv8_copy_kernel(const EvictParams p) {
   const int b = p.heads.div(plane), head = plane - b * p.heads.d;
   const int n = min(max(__ldg(p.lens + b), 0), (int)p.cap), m = min(n, p.keep);
   const int rows = min(m - blk * kKv8Tok, kKv8Tok);
+  wait_for_grid();
   if (rows <= 0) return;
+  const int j = lane < rows ? __ldg(p.kept + (int64_t)plane * p.keep + blk * kKv8Tok + lane) : 0;
   const int dpi = blk / p.bpp, dest_page = __ldg(p.dest + (int64_t)b * p.dest_w + dpi);
   if (dest_page < 0 || dest_page >= p.n_pages) {
     if (lane == 0) atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
@@ -190,7 +321,6 @@ __global__ void __launch_bounds__(256) kv8_copy_kernel(const EvictParams p) {
   int row = 0;
   Kv8Tail tail = {{0.f, 0.f}, 0u, 0u};
   if (lane < rows) {
-    const int j = __ldg(p.kept + (int64_t)plane * p.keep + blk * kKv8Tok + lane);
     const int pi = j / p.page, off = j - pi * p.page;
     const int pg = __ldg(p.table + (int64_t)b * p.table_w + pi);
     row = off % kKv8Tok;
@@ -326,17 +456,38 @@ iha_status kv8_evict(void* cache, const int32_t* block_table, const int32_t* seq
   p.heads.set(Hkv);
   p.items = planes * blocks;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  static SmemLimit limit;
-  const cudaError_t e = limit.ensure(kv8_select_kernel, kCached * 4);
+  static SmemLimit limit[2];
+  const bool vec = aligned16(weights);
+  auto* const select = vec ? kv8_select_kernel<true> : kv8_select_kernel<false>;
+  const cudaError_t e = limit[vec].ensure(select, kSelectSmem + kCached * 4);
   if (e != cudaSuccess)
     return fail(IHA_ERR_CUDA, "%s (smem attribute): %s", name, cudaGetErrorString(e));
-  const int held = (int)(cap < kCached ? cap : kCached) * 4;
-  kv8_select_kernel<<<(unsigned)planes, kThreads, held, s>>>(p);
+  // CTAs of a head: as many as the GPU runs at once (one on an SM), while each has 4096
+  // keys or more
+  unsigned size = 1;
+  while (size < 8 && planes * size * 2 <= (int64_t)sm_count() && cap >= 4096 * 2 * size) size *= 2;
+  int64_t held = ((cap + size - 1) / size + 127) & ~(int64_t)127;
+  if (held > kCached) held = kCached;
+  if (planes * size > INT32_MAX)
+    return fail(IHA_ERR_UNSUPPORTED, "%s: too many heads in one call", name);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = size;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)planes * size);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSelectSmem + held * 4;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t le = cudaLaunchKernelEx(&cfg, select, p);
+  if (le != cudaSuccess) return fail(IHA_ERR_CUDA, "%s: %s", name, cudaGetErrorString(le));
   st = check_launch(name);
   if (st != IHA_OK) return st;
   const unsigned grid = (unsigned)((p.items + 7) / 8);
-  IHA_KV8_D_SWITCH(d, (kv8_copy_kernel<kD><<<grid, 256, 0, s>>>(p)))
-  return check_launch(name);
+  IHA_KV8_D_SWITCH(d, return launch_behind(name, kv8_copy_kernel<kD>, grid, 256, s, p))
+  return IHA_OK;
 }
 
 }  // extern "C"

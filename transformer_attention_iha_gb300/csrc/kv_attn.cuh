@@ -23,10 +23,9 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kKvTok = 16;  // tokens of a block
 static_assert(kKvTok == kKv4Tok, "blocks of the caches");
-// Positions a unit takes besides its blocks: its Q, output and ramp.  Measured on
-// a ragged batch (16 sequences of 1 to 8192 keys, 8 key heads): 2 31 us, 4 23.6,
-// 6 23.1; on 131071 keys x 80 heads they differ by 1 per cent.
-constexpr int kUnitCost = 6;
+// Positions a unit takes besides its blocks: its Q, output and ramp (each cache's kernel
+// says what it measured).
+constexpr int kUnitCost = IHA_KV_UNIT_COST;
 // A warp's stretch is at least this long: shorter ones cost more in joining
 // than they save (777 keys x 80 heads: 3 12.0 us, 4 11.6, 6 12.8).
 constexpr int kMinShare = 4;
