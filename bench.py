@@ -170,6 +170,8 @@ OP_INPUTS = {
     "long_attention_causal": [f"l{a}_{t}" for t in "qkv" for a in "xw"],
     "mu_attention_qpool": [],   # generated on the device (see qpool_case)
     "kv4_store": [], "kv4_load": [], "kv4_decode": [],   # likewise (see kv4_case)
+    "kv8_append": [], "kv8_load": [], "kv8_decode": [], "kv8_evict": [],   # (see kv8_case)
+    "rope_fwd": [], "rope_bwd": [],   # (see rope_case)
 }
 
 
@@ -318,6 +320,68 @@ def kv4_case(T, torch, device, name):
                      device=device)
     return (lambda: T.mha_fwd_kv4(q, cache, pages[None], lens, H, page, out=o, lse=lse,
                                   workspace=ws), n * H * row4 + 4 * H * d, 4 * d * n * H)
+
+
+def kv8_case(T, torch, device, name):
+    """The 8-bit cache at the same shapes as kv4_case's: a prompt of 8192 tokens added or
+    read back, one new token attending over 32768 keys (with the keys' weights), or those
+    keys cut to 8192 (the last 512 and the heaviest)."""
+    pm, page = S.LLAMA_PREMIX, 64
+    prompt = name in ("kv8_append", "kv8_load")
+    H, d, n = pm.HP, pm.d, pm.N if prompt else 32768
+    gen = torch.Generator(device=device)
+    gen.manual_seed(12)
+    e = lambda *s: torch.randn(s, generator=gen, device=device).to(torch.bfloat16)
+    k, v = e(1, n, H, d), e(1, n, H, d)
+    pages = torch.randperm(n // page, generator=gen, device=device).to(torch.int32)
+    if prompt:
+        pages = pages.sort().values
+    table, lens = pages[None].contiguous(), torch.tensor([n], dtype=torch.int32, device=device)
+    cache = torch.empty((n // page + 128, T.kv8_page_bytes(page, H, d)), dtype=torch.uint8,
+                        device=device)
+    append = lambda: T.kv8_append(k, v, table, lens, cache, page)
+    row8 = 2 * d + 1
+    if name == "kv8_append":
+        return append, n * H * (4 * d + row8), 0
+    append()
+    if name == "kv8_load":
+        slots = (pages[:, None] * page + torch.arange(page, device=device)).to(torch.int32)
+        out = (torch.empty_like(k), torch.empty_like(v))
+        return (lambda: T.kv8_load(cache, slots.view(1, n), H, d, page, out=out),
+                n * (H * (4 * d + row8) + 4), 0)
+    w = torch.rand((1, H, n), generator=gen, device=device)
+    if name == "kv8_evict":
+        keep = 8192
+        dest = torch.arange(n // page, n // page + 128, dtype=torch.int32, device=device)[None]
+        new = (torch.empty(1, dtype=torch.int32, device=device),
+               torch.empty((1, H, keep), dtype=torch.int32, device=device),
+               torch.empty((1, H, keep), device=device))
+        return (lambda: T.kv8_evict(cache, table, lens, w, dest, H, d, page, keep, 512, *new),
+                H * (4 * n + 8 * keep + 2 * keep * row8), 0)
+    q = e(1, 1, H, d)
+    o, lse = torch.empty_like(q), torch.empty((1, H, 1), device=device)
+    ws = torch.zeros(T.mha_fwd_kv8_workspace_bytes(1, 1, H, H, d, n), dtype=torch.uint8,
+                     device=device)
+    return (lambda: T.mha_fwd_kv8(q, cache, table, lens, H, page, out=o, lse=lse, weights=w,
+                                  weights_out=w, workspace=ws),
+            n * H * (row8 + 8) + 4 * H * d, 4 * d * n * H)
+
+
+def rope_case(T, torch, device, name):
+    """Q and K (80 heads of 128 each) of 8192 tokens rotated, or rotated back."""
+    pm = S.LLAMA_PREMIX
+    gen = torch.Generator(device=device)
+    gen.manual_seed(13)
+    e = lambda *s: torch.randn(s, generator=gen, device=device).to(torch.bfloat16)
+    q, k = e(1, pm.N, pm.HP, pm.d), e(1, pm.N, pm.HP, pm.d)
+    out, rope = (torch.empty_like(q), torch.empty_like(k)), T.Rope(pm.d)
+    call = T.rope_fwd if name == "rope_fwd" else T.rope_bwd
+    return (lambda: call(q, k, None, rope, out=out), 8 * q.numel(), 6 * q.numel())
+
+
+SERVING_CASES = {**{f"kv4_{o}": kv4_case for o in ("store", "load", "decode")},
+                 **{f"kv8_{o}": kv8_case for o in ("append", "load", "decode", "evict")},
+                 **{f"rope_{o}": rope_case for o in ("fwd", "bwd")}}
 
 
 def extra_ops(T, torch, dev, step, device, iters: int, hbm: float, tc: float):
@@ -831,8 +895,8 @@ def single_op(T, torch, name, dev, device):
                                             mu.mu_h, mu.mu_w)
     if kind == "mu_attention_qpool":
         return qpool_case(T, torch, device)[0]
-    if kind.startswith("kv4_"):
-        return kv4_case(T, torch, device, kind)[0]
+    if kind in SERVING_CASES:
+        return SERVING_CASES[kind](T, torch, device, kind)[0]
     if kind.startswith("mu_"):
         g, ou = e((mu.B, mu.n_keep, mu.unit_tokens, mu.C)), e((mu.B, mu.n_keep, mu.unit_tokens, mu.C))
         dec = torch.zeros((mu.B, mu.grid_h * mu.grid_w, mu.C), dtype=torch.bfloat16, device=device)
@@ -891,8 +955,8 @@ def single_op_arm(args):
     units = hq.B * hq.n_units * hq.heads
     table["mu_attention_qpool"] = (units * (3 * hq.T + hq.Tq) * hq.head_dim * 2,
                                    4 * hq.head_dim * hq.Tq * hq.T * units)
-    if args.only.startswith("kv4_"):
-        table[args.only] = kv4_case(T, torch, device, args.only)[1:]
+    if args.only in SERVING_CASES:
+        table[args.only] = SERVING_CASES[args.only](T, torch, device, args.only)[1:]
     nbytes, flops = table[args.only]
     ms = e0.elapsed_time(e1) / args.steps
     out = {"op": args.only, "ms": round(ms, 5), "GB/s": round(nbytes / ms / 1e6, 1),

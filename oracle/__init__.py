@@ -391,7 +391,7 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None
     return w, 1.0
 
 
-def rope(x: np.ndarray, positions: np.ndarray, w: np.ndarray, gain: float = 1.0,
+def rotate(x: np.ndarray, positions: np.ndarray, w: np.ndarray, gain: float = 1.0,
          interleaved: bool = False, back: bool = False) -> np.ndarray:
     """x [B, N, H, d] (float32 or bf16 bits) rotated at positions [B, N], float64: pair
     i of the first 2 len(w) features by positions * w[i], times gain; back: the

@@ -89,12 +89,12 @@ def test_rope_oracle_is_the_premix_rotation():
     eye = np.eye(2, dtype=np.float32).reshape(2, 1, 2)
     w, _ = O.rope_frequencies(d)
     ref = O.premix_fwd(x, eye, 1, rope=True)
-    np.testing.assert_allclose(O.rope(x, np.arange(5)[None], w), ref, atol=1e-12)
-    y = O.rope(x, np.arange(5)[None], w, 1.5, True)
+    np.testing.assert_allclose(O.rotate(x, np.arange(5)[None], w), ref, atol=1e-12)
+    y = O.rotate(x, np.arange(5)[None], w, 1.5, True)
     z = y.reshape(1, 5, 2, d // 2, 2)
     x2 = S.bf16_bits_to_f32(x).reshape(1, 5, 2, d // 2, 2)
     np.testing.assert_allclose((z ** 2).sum(-1), 2.25 * (x2.astype(np.float64) ** 2).sum(-1))
-    back = O.rope(y.astype(np.float32), np.arange(5)[None], w, 1.0, True, back=True)
+    back = O.rotate(y.astype(np.float32), np.arange(5)[None], w, 1.0, True, back=True)
     np.testing.assert_allclose(back, 1.5 * S.bf16_bits_to_f32(x), atol=1e-6)
 
 

@@ -744,7 +744,7 @@ def test_a_run_of_decode_steps_with_evictions(T, captured):
         at = [a + 1 for a in at]
         qr, kr = (t.cpu().view(torch.int16).numpy().view(np.uint16) for t in (q1, k1))
         for t, a in zip((qr, kr), x):                    # the rotation itself
-            want = O.rope(a, np.array(at)[:, None] - 1, w_, 1.0, True)
+            want = O.rotate(a, np.array(at)[:, None] - 1, w_, 1.0, True)
             f = S.bf16_bits_to_f32(t)
             assert (np.abs(f - want) <= 2.0 ** -8 * np.abs(want) +
                     2.0 ** -20 * np.abs(S.bf16_bits_to_f32(a)).max()).all()

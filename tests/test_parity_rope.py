@@ -33,7 +33,7 @@ def f32(x):
 
 def check(got, x, pos, w, gain, inter, back):
     n = len(w)
-    r = O.rope(x, pos, w, gain, inter, back)
+    r = O.rotate(x, pos, w, gain, inter, back)
     a = np.abs(f32(x).astype(np.float64))
     pair = np.zeros_like(a)
     lo, hi = (slice(0, 2 * n, 2), slice(1, 2 * n, 2)) if inter else (slice(0, n), slice(n, 2 * n))
