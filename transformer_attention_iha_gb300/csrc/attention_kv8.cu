@@ -183,8 +183,10 @@ struct Attend {
 #pragma unroll
         for (int e = 0; e < 4; e += ES) x[nt][b][e] = c4[nt][e] * (sk * cm[nt][e & 1]);
     }
-    const bool any_nan = (nan[0] | nan[1]) != 0;
-    if (any_nan) {
+    uint32_t any_nan = 0;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) any_nan |= nan[b];
+    if (any_nan != 0) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -236,8 +238,11 @@ struct Attend {
     for (int nt = 0; nt < NT; ++nt) {
       float top[2];
 #pragma unroll
-      for (int e = 0; e < 2; e += ES)
-        top[e] = fmaxf(fmaxf(x[nt][0][e], x[nt][0][e + 2]), fmaxf(x[nt][1][e], x[nt][1][e + 2]));
+      for (int e = 0; e < 2; e += ES) {
+        top[e] = fmaxf(x[nt][0][e], x[nt][0][e + 2]);
+#pragma unroll
+        for (int b = 1; b < NB; ++b) top[e] = fmax3f(top[e], x[nt][b][e], x[nt][b][e + 2]);
+      }
       if (__any_sync(0xffffffffu, top[0] > mlim[nt][0] || (!ONE && top[1] > mlim[nt][1]))) {
 #pragma unroll
         for (int e = 0; e < 2; e += ES) {
@@ -290,7 +295,9 @@ struct Attend {
       float wt[2];
 #pragma unroll
       for (int e = 0; e < 2; e += ES) {
-        wt[e] = fmaxf(fmaxf(x[nt][0][e], x[nt][0][e + 2]), fmaxf(x[nt][1][e], x[nt][1][e + 2]));
+        wt[e] = fmaxf(x[nt][0][e], x[nt][0][e + 2]);
+#pragma unroll
+        for (int b = 1; b < NB; ++b) wt[e] = fmax3f(wt[e], x[nt][b][e], x[nt][b][e + 2]);
         grow |= wt[e] * F[nt][e] > 32768.f;
       }
       if (__any_sync(0xffffffffu, grow)) {
@@ -314,7 +321,7 @@ struct Attend {
           }
         }
       }
-      if (any_nan) {  // a visible V row of NaN makes all of O NaN
+      if (any_nan != 0) {  // a visible V row of NaN makes all of O NaN
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
