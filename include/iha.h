@@ -467,7 +467,7 @@ iha_status mha_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
  * V: e is the smallest with every |x| <= 448 * 2^e, at least -100, and c = x / s rounded
  * to nearest even.  A value stands for s * c.  A row (one token and head, of K or
  * of V) that holds a NaN or an infinity stands for NaN throughout, and has no part in s.
- * 2 d + 1 bytes per token and head.
+ * 2 d + 1 bytes per token and head (a page is rounded up to 128 bytes).
  *
  * The cache is n_pages pages of kv8_page_bytes() bytes, dense, 16-byte aligned; a page
  * holds `page` tokens (a multiple of 16) of all Hkv heads, K and V.  Key j of sequence

@@ -173,7 +173,8 @@ def test_rope_refusals(L, fn):
 
 def test_page_bytes(L):
     assert L.kv8_page_bytes(64, 80, 128) == 4 * 80 * (32 * 128 + 16)
-    assert L.kv8_page_bytes(16, 1, 32) == 32 * 32 + 16
+    assert L.kv8_page_bytes(16, 1, 32) == 32 * 32 + 128      # whole lines of 128 bytes
+    assert L.kv8_page_bytes(32, 3, 64) == 6 * 32 * 64 + 128
     for a in ((0, 1, 32), (24, 1, 32), (16, 0, 32), (16, 1, 16), (16, 1, 160), (16, 1, 33)):
         assert L.kv8_page_bytes(*a) == 0
         with pytest.raises(ValueError):

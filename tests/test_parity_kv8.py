@@ -157,9 +157,11 @@ def test_padding_counts_and_bytes_that_stay(T):
         np.testing.assert_array_equal(to_f64(g)[0, 0],
                                       O.Kv8Rows(H, d).append(x[1, -1:]).values[0])
         assert not g[0, 1:].any()
-    per = T.kv8_page_bytes(page, H, d) // (H * 2)      # the other block of each head in page 5
-    blocks = cache[5].view(H, 2, per)
-    assert bool((blocks[:, 1] == 0x5A).all())
+    blocks = cache[5, :2 * H * 32 * d].view(H, 2, -1)  # the other block of each head in page 5
+    assert bool((blocks[:, 1] == 0x5A).all()) and bool((blocks[:, 0] != 0x5A).any())
+    tails = cache[5, 2 * H * 32 * d:].view(-1, 16)[:2 * H].view(H, 2, 16)
+    assert bool((tails[:, 1] == 0x5A).all()) and bool((tails[:, 0] != 0x5A).any())
+    assert bool((cache[5, 2 * H * (32 * d + 16):] == 0x5A).all())
 
 
 def test_bad_lengths_counts_and_pages_are_flagged(T):

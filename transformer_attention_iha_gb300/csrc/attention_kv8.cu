@@ -34,6 +34,7 @@ constexpr float kTopF = 8.5070591730234616e37f;
 constexpr int kTopFExp = 126 + 127;
 
 struct Kv8AttnParams : KvAttnParams {
+  Kv8Pages pages;
   float* scores;  // nullable: [B, Hkv, ncols, table_w * page], log2 domain, -inf where hidden
 };
 
@@ -137,18 +138,18 @@ struct Attend {
     return s + row_at + ((row_chunk ^ (2 * cc)) << 4);
   }
 
-  // Two blocks in shared memory at s, of keys from key0 on.  edge: not all of their keys
+  // Two blocks in shared memory at s, tails at st, of keys from key0 on.  edge: not all of their keys
   // are visible to every column; gone: a bit per block that no page holds or that lies
   // past the unit's end, past: a bit per block past it.  scores: nullable, of column 0.
-  __device__ __forceinline__ void step(const Kv8AttnParams& p, uint32_t s, int key0, bool edge,
-                                       uint32_t gone, uint32_t past, int len, int c_first,
-                                       float* scores, int64_t cap) {
+  __device__ __forceinline__ void step(const Kv8AttnParams& p, uint32_t s, uint32_t st, int key0,
+                                       bool edge, uint32_t gone, uint32_t past, int len,
+                                       int c_first, float* scores, int64_t cap) {
     float x[NT][NB][4];  // (token g, columns 2 t, 2 t + 1), (token g + 8, ...)
     float sv[NB];
     uint32_t nan[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const uint4 tail = lds128(s + b * BYTES + 32 * D);
+      const uint4 tail = lds128(st + b * kKv8TailBytes);
       const float sk = __uint_as_float(tail.x);
       sv[b] = __uint_as_float(tail.y);
       nan[b] = tail.z;
@@ -488,12 +489,12 @@ struct BlockRing {
   int pr, pr_end, stretch, lane;
   bool more;
   Run run, run_next;
-  const uint8_t* src;  // the run's next block; null: no such page
+  const uint8_t *src, *src_tail;  // the run's next block and its tail; null: no such page
   // bit per block of the ring: no such page; bit per stage: copies under way, and the
   // parity of its barrier
-  uint32_t bad, flying, phase, ring, bars;
+  uint32_t bad, flying, phase, ring, tails, bars;
 
-  __device__ __forceinline__ Run next_run(const KvAttnParams& p) {
+  __device__ __forceinline__ Run next_run(const Kv8AttnParams& p) {
     Run r = {0, 0, 0, 0, 0};
     while (more && pr >= pr_end) {
       more = pu.at + pu.n + kUnitCost < stretch && next_unit<COLS>(p, pu);
@@ -510,34 +511,35 @@ struct BlockRing {
     }
     return r;
   }
-  __device__ __forceinline__ void take_run(const KvAttnParams& p) {
+  __device__ __forceinline__ void take_run(const Kv8AttnParams& p) {
     run = run_next;
     if (run.cnt > 0) {
       run_next = next_run(p);
       const bool in = run.id >= 0 && run.id < p.n_pages;
       if (!in && lane == 0) atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
-      src = in ? p.cache + (((int64_t)run.id * p.Hkv + run.head) * p.blocks_per_page +
-                            run.in_page) * (int64_t)BYTES
-               : nullptr;
+      src = in ? p.cache + p.pages.block(run.id, run.head, run.in_page, BYTES / 32) : nullptr;
+      src_tail = in ? p.cache + p.pages.tail(run.id, run.head, run.in_page) : nullptr;
     }
   }
-  __device__ __forceinline__ void start(const KvAttnParams& p, const Unit& u, int stretch_,
-                                        int lane_, uint32_t ring_, uint32_t bars_) {
+  __device__ __forceinline__ void start(const Kv8AttnParams& p, const Unit& u, int stretch_,
+                                        int lane_, uint32_t ring_, uint32_t tails_,
+                                        uint32_t bars_) {
     pu = u;
     stretch = stretch_;
     lane = lane_;
     ring = ring_;
+    tails = tails_;
     bars = bars_;
     more = true;
     bad = flying = phase = 0;
-    src = nullptr;
+    src = src_tail = nullptr;
     my_blocks(pu, stretch, pr, pr_end);
     run_next = next_run(p);
     take_run(p);
 #pragma unroll 1
     for (int i = 0; i < STAGES; ++i) fetch(p, i);
   }
-  __device__ __forceinline__ void fetch(const KvAttnParams& p, int stage) {
+  __device__ __forceinline__ void fetch(const Kv8AttnParams& p, int stage) {
     bad &= ~(((1u << RUN) - 1u) << (stage * RUN));
     flying &= ~(1u << stage);
     if (run.cnt == 0) return;
@@ -547,10 +549,14 @@ struct BlockRing {
     do {
       const int c = min(want - have, run.cnt);
       if (src != nullptr) {
-        if (lane == 0)
+        if (lane == 0) {
           bulk_load(ring + (stage * RUN + have) * BYTES, src, c * BYTES, bars + 8 * stage);
-        bytes += c * BYTES;
+          bulk_load(tails + (stage * RUN + have) * kKv8TailBytes, src_tail, c * kKv8TailBytes,
+                    bars + 8 * stage);
+        }
+        bytes += c * (BYTES + kKv8TailBytes);
         src += c * BYTES;
+        src_tail += c * kKv8TailBytes;
       } else {
         bad |= ((1u << c) - 1u) << (stage * RUN + have);
       }
@@ -562,14 +568,14 @@ struct BlockRing {
     if (lane == 0) mbar_arrive_expect_tx(bars + 8 * stage, bytes);
     flying |= 1u << stage;
   }
-  __device__ __forceinline__ bool wait(const KvAttnParams& p, int stage, volatile int* abort_flag) {
+  __device__ __forceinline__ bool wait(const Kv8AttnParams& p, int stage, volatile int* abort_flag) {
     if (!mbar_wait_warp(bars + 8 * stage, (phase >> stage) & 1u, abort_flag, p.wait_ns))
       return false;
     phase ^= 1u << stage;
     return true;
   }
   // After a wait that gave up: what is in flight lands before the memory goes away.
-  __device__ __forceinline__ void drain(const KvAttnParams& p) {
+  __device__ __forceinline__ void drain(const Kv8AttnParams& p) {
     volatile int no_abort = 0;
     for (int i = 0; i < STAGES; ++i)
       if ((flying >> i) & 1u) mbar_wait(bars + 8 * i, (phase >> i) & 1u, &no_abort, p.wait_ns);
@@ -727,6 +733,7 @@ template <int D, int NT>
 struct Smem {
   // a warp's ring; when it has run out, the part of the unit its stretch ends in
   alignas(128) uint8_t ring[kWarps][kStages][run_of(D)][kv8_block_bytes(D)];
+  alignas(16) uint8_t tails[kWarps][kStages][run_of(D)][kKv8TailBytes];
   uint2 q[NT > 1 ? kWarps : 1][NT > 1 ? NT * (D / 16) * 32 : 1];
   uint64_t full[kWarps][kStages];
   LineSmem line;
@@ -773,7 +780,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
     };
     prefetch_q(u);
     BlockRing<BYTES, RUN, kStages, COLS> ring;
-    ring.start(p, u, stretch, lane, smem_u32(sm.ring[warp]), smem_u32(sm.full[warp]));
+    ring.start(p, u, stretch, lane, smem_u32(sm.ring[warp]), smem_u32(sm.tails[warp]),
+               smem_u32(sm.full[warp]));
     Attend<D, NT, ONE> a;
     a.init(lane, sm.q[NT > 1 ? warp : 0]);
     const int64_t cap = (int64_t)p.table_w * p.page;
@@ -818,7 +826,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
             const uint32_t gk = (gone >> k0) & ((1u << NB) - 1u);
             const bool edge = (unsigned)(rk - rf0) >= rf_n || (unsigned)(rk + NB - 1 - rf0) >= rf_n ||
                               gk != 0;
-            a.step(p, ring.ring + (stage * RUN + k0) * BYTES, (u.b0 + rk) * kKv8Tok, edge, gk,
+            a.step(p, ring.ring + (stage * RUN + k0) * BYTES,
+                   ring.tails + (stage * RUN + k0) * kKv8TailBytes, (u.b0 + rk) * kKv8Tok, edge, gk,
                    past >> k0, u.len, c_first, scores, cap);
           }
           __syncwarp();  // the stage has been read
@@ -975,6 +984,7 @@ iha_status mha_fwd_kv8(const void* q, const void* cache, const int32_t* block_ta
       lse_out, workspace, workspace_bytes, B, Nq, Hq, Hkv, d, n_pages, page, table_width, sq, so,
       scale, mask_mode, window, dt);
   if (st != IHA_OK) return st;
+  p.pages.set(page, Hkv, d);
   p.scores = nullptr;
   if (weights) {
     if (p.ncols > kMaxWeighed)

@@ -8,13 +8,17 @@
 // become subnormal: rows that are moved or whose block grows keep their values.
 //
 // Pages hold `page` tokens (a multiple of 16) of every head, K and V together:
-//   cache[page id][head][token / 16] = one block of 32 d + 16 bytes:
-//   K codes  [16][d], V codes [16][d]: a row's 16-byte chunks c lie at c ^ swap(row),
-//            so that eight rows' chunks of the same c are in different banks
-//            (ldmatrix of either, transposed for V, without conflicts)
-//   tail     scale of K, scale of V (fp32), one bit per row of K (low half) and of V
-//            whose values were not all finite: it stands for NaN throughout, its
-//            codes are 0.  No code is ever NaN, so hidden rows are harmless as operands.
+//   codes    [head][token / 16] blocks of 32 d bytes, K [16][d] and V [16][d]: a row's
+//            16-byte chunks c lie at c ^ swap(row), so that eight rows' chunks of the same
+//            c are in different banks (ldmatrix of either, transposed for V, without
+//            conflicts).  Rows of 128 features are whole lines: with the tails between
+//            the blocks a row alone moved half as much again (rows gathered from
+//            32768 x 80 heads: 288 MB read for 168).
+//   tails    [head][token / 16] 16 bytes: scale of K, scale of V (fp32), one bit per row of
+//            K (low half) and of V whose values were not all finite: it stands for NaN
+//            throughout, its codes are 0.  No code is ever NaN, so hidden rows are
+//            harmless as operands.
+// A page is a multiple of 128 bytes.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -27,7 +31,8 @@ constexpr int kKv8Tok = 16;      // tokens of a block
 constexpr int kKv8LowestE = -100;  // smallest e
 constexpr int kKv8HighestE = 120;  // the largest that finite rows need
 
-__host__ __device__ constexpr int kv8_block_bytes(int d) { return 32 * d + 16; }
+__host__ __device__ constexpr int kv8_block_bytes(int d) { return 32 * d; }  // of codes
+constexpr int kKv8TailBytes = 16;
 // What a row's chunk numbers are XORed with.
 __host__ __device__ constexpr int kv8_swap(int d, int row) {
   return d == 128 ? row & 7 : d == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
@@ -39,14 +44,29 @@ struct alignas(16) Kv8Tail {
   uint32_t unused;
 };
 
+// Where a page's blocks and tails are.
+struct Kv8Pages {
+  int64_t bytes, tails;  // of a page; from its start to its tails
+  int bpp;               // blocks of a head in a page
+  void set(int page, int heads, int d) {
+    bpp = page / kKv8Tok;
+    tails = (int64_t)heads * bpp * kv8_block_bytes(d);
+    bytes = (tails + (int64_t)heads * bpp * kKv8TailBytes + 127) & ~(int64_t)127;
+  }
 #if defined(__CUDACC__)
-__device__ __forceinline__ int64_t kv8_block_of(int page_id, int blk_in_page, int head, int heads,
-                                                int blocks_per_page, int d) {
-  return (((int64_t)page_id * heads + head) * blocks_per_page + blk_in_page) *
-         (int64_t)kv8_block_bytes(d);
-}
-__device__ __forceinline__ Kv8Tail kv8_tail(const uint8_t* blk, int d) {
-  const uint4 u = *reinterpret_cast<const uint4*>(blk + 32 * d);
+  // Byte offsets (64 bits: a cache can be far longer than 4 GB) of a block, and of its tail.
+  __device__ __forceinline__ int64_t block(int page_id, int head, int blk, int d) const {
+    return page_id * bytes + (int64_t)(head * bpp + blk) * kv8_block_bytes(d);
+  }
+  __device__ __forceinline__ int64_t tail(int page_id, int head, int blk) const {
+    return page_id * bytes + tails + (int64_t)(head * bpp + blk) * kKv8TailBytes;
+  }
+#endif
+};
+
+#if defined(__CUDACC__)
+__device__ __forceinline__ Kv8Tail kv8_tail(const uint8_t* at) {
+  const uint4 u = *reinterpret_cast<const uint4*>(at);
   Kv8Tail t;
   t.scale[0] = __uint_as_float(u.x);
   t.scale[1] = __uint_as_float(u.y);

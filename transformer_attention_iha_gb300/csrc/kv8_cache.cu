@@ -30,7 +30,8 @@ struct AppendParams {
   iha_strides sk, sv;
   FastDiv heads, blocks;  // heads; blocks that one call can touch of a sequence
   int64_t items;
-  int N, n_pages, page, bpp, table_w;
+  Kv8Pages pages;
+  int N, n_pages, page, table_w;
 };
 
 // 16 bytes of a row: the largest magnitude as fp32 bits (infinite or above: not finite).
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv8_append_kernel(const AppendPar
   const int first = max(0, len - cnt);  // the first new position
   const int blk = first / kKv8Tok + nth, pos0 = blk * kKv8Tok;
   if (first >= len || pos0 >= len) return;
-  const int pi = blk / p.bpp, page_id = __ldg(p.table + (int64_t)b * p.table_w + pi);
+  const int bpp = p.pages.bpp, pi = blk / bpp, page_id = __ldg(p.table + (int64_t)b * p.table_w + pi);
   const int had = max(0, first - pos0), end = min(len - pos0, kKv8Tok);  // new rows [had, end)
   const int r = lane / LPR, c = lane - r * LPR;  // row of an iteration, vector of the row
 
@@ -105,10 +106,10 @@ __global__ void __launch_bounds__(32 * kWarps) kv8_append_kernel(const AppendPar
     if (lane == 0) atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
     return;
   }
-  uint8_t* const base =
-      p.cache + kv8_block_of(page_id, blk - pi * p.bpp, head, p.heads.d, p.bpp, D);
+  uint8_t* const base = p.cache + p.pages.block(page_id, head, blk - pi * bpp, D);
+  uint8_t* const tail_at = p.cache + p.pages.tail(page_id, head, blk - pi * bpp);
   Kv8Tail tail = {{0.f, 0.f}, 0u, 0u};
-  if (had > 0) tail = kv8_tail(base, D);
+  if (had > 0) tail = kv8_tail(tail_at);
 
   const uint32_t row_lanes =
       LPR == 32 ? ~0u : ((1u << (LPR % 32)) - 1u) << (r * LPR % 32);
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv8_append_kernel(const AppendPar
   if (!BOTH) load(1, xv);
   store(base + kKv8Tok * D, xv, tail.scale[1], 16, sv);
   if (lane == 0)
-    *reinterpret_cast<uint4*>(base + 32 * D) =
+    *reinterpret_cast<uint4*>(tail_at) =
         make_uint4(__float_as_uint(sk), __float_as_uint(sv), tail.nan, 0u);
 }
 
@@ -183,7 +184,8 @@ struct LoadParams {
   iha_strides sk, sv;
   FastDiv heads, N, Bi, page;  // heads; as kv4_load
   int64_t items;
-  int n_slots, bpp;
+  Kv8Pages pages;
+  int n_slots;
 };
 
 // Codes of 16 bytes of values: 8 bf16 (the products are exact), 4 fp32.
@@ -226,8 +228,8 @@ __global__ void __launch_bounds__(256) kv8_load_kernel(const LoadParams p) {
   k[0] = k[1] = v[0] = v[1] = make_uint4(0, 0, 0, 0);
   if (in) {
     const int pg = p.page.div(slot), off = slot - pg * p.page.d, r = off % kKv8Tok;
-    const uint8_t* blk = p.cache + kv8_block_of(pg, off / kKv8Tok, head, p.heads.d, p.bpp, D);
-    const Kv8Tail t = kv8_tail(blk, D);
+    const uint8_t* blk = p.cache + p.pages.block(pg, head, off / kKv8Tok, D);
+    const Kv8Tail t = kv8_tail(p.cache + p.pages.tail(pg, head, off / kKv8Tok));
     Codes<T> ck[2], cv[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -301,7 +303,9 @@ extern "C" {
 
 size_t kv8_page_bytes(int page, int Hkv, int d) {
   if (page <= 0 || page % iha::kKv8Tok || Hkv <= 0 || d <= 0 || d % 32 || d > 128) return 0;
-  return (size_t)(page / iha::kKv8Tok) * Hkv * iha::kv8_block_bytes(d);
+  iha::Kv8Pages pages;
+  pages.set(page, Hkv, d);
+  return (size_t)pages.bytes;
 }
 
 iha_status kv8_append(const void* k, const void* v, const int32_t* block_table,
@@ -344,11 +348,11 @@ iha_status kv8_append(const void* k, const void* v, const int32_t* block_table,
   p.N = N;
   p.n_pages = n_pages;
   p.page = page;
-  p.bpp = page / kKv8Tok;
+  p.pages.set(page, Hkv, d);
   p.table_w = table_width;
   // N neighbours touch at most this many blocks, a table no more than it has
   const int64_t touched = ((int64_t)N + 2 * kKv8Tok - 2) / kKv8Tok;
-  const int64_t most = (int64_t)table_width * p.bpp;
+  const int64_t most = (int64_t)table_width * p.pages.bpp;
   p.blocks.set((int)(touched < most ? touched : most));
   p.heads.set(Hkv);
   p.items = (int64_t)B * p.blocks.d * Hkv;
@@ -412,7 +416,7 @@ iha_status kv8_load(const void* cache, const int32_t* slots, void* k, void* v, i
   p.page.set(page);
   p.items = rows * (d * es / 32);
   p.n_slots = n_pages * page;
-  p.bpp = page / kKv8Tok;
+  p.pages.set(page, Hkv, d);
   const int64_t ctas = (p.items + 255) / 256;
   if (ctas > INT32_MAX)
     return fail(IHA_ERR_UNSUPPORTED, "%s: too many rows in one call", name);

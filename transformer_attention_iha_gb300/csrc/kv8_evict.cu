@@ -26,7 +26,8 @@ struct EvictParams {
   const float* weights;
   int32_t *new_lens, *kept;
   float* weights_out;  // nullable
-  int B, H, n_pages, page, bpp, table_w, dest_w, keep, recent;
+  int B, H, n_pages, page, table_w, dest_w, keep, recent;
+  Kv8Pages pages;
   int64_t cap, dest_cap;
   FastDiv blocks, heads;  // copy: blocks of keep rows; heads
   int64_t items;
@@ -309,13 +310,12 @@ __global__ void __launch_bounds__(256) kv8_copy_kernel(const EvictParams p) {
   wait_for_grid();
   if (rows <= 0) return;
   const int j = lane < rows ? __ldg(p.kept + (int64_t)plane * p.keep + blk * kKv8Tok + lane) : 0;
-  const int dpi = blk / p.bpp, dest_page = __ldg(p.dest + (int64_t)b * p.dest_w + dpi);
+  const int bpp = p.pages.bpp, dpi = blk / bpp, dest_page = __ldg(p.dest + (int64_t)b * p.dest_w + dpi);
   if (dest_page < 0 || dest_page >= p.n_pages) {
     if (lane == 0) atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
     return;
   }
-  uint8_t* const to =
-      p.cache + kv8_block_of(dest_page, blk - dpi * p.bpp, head, p.heads.d, p.bpp, D);
+  uint8_t* const to = p.cache + p.pages.block(dest_page, head, blk - dpi * bpp, D);
   // lane i < 16: where row i comes from
   int64_t from = -1;
   int row = 0;
@@ -325,8 +325,8 @@ __global__ void __launch_bounds__(256) kv8_copy_kernel(const EvictParams p) {
     const int pg = __ldg(p.table + (int64_t)b * p.table_w + pi);
     row = off % kKv8Tok;
     if (pg >= 0 && pg < p.n_pages) {
-      from = kv8_block_of(pg, off / kKv8Tok, head, p.heads.d, p.bpp, D);
-      tail = kv8_tail(p.cache + from, D);
+      from = p.pages.block(pg, head, off / kKv8Tok, D);
+      tail = kv8_tail(p.cache + p.pages.tail(pg, head, off / kKv8Tok));
     } else {
       atomicOr(&g_dev_error, DEV_ERR_CACHE_INDEX);
     }
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(256) kv8_copy_kernel(const EvictParams p) {
     }
   }
   if (lane == 0)
-    *reinterpret_cast<uint4*>(to + 32 * D) =
+    *reinterpret_cast<uint4*>(p.cache + p.pages.tail(dest_page, head, blk - dpi * bpp)) =
         make_uint4(__float_as_uint(kv8_two(tk)), __float_as_uint(kv8_two(tv)),
                    (nan_k & 0xFFFFu) | (nan_v << 16), 0u);
 }
@@ -445,7 +445,7 @@ iha_status kv8_evict(void* cache, const int32_t* block_table, const int32_t* seq
   p.H = Hkv;
   p.n_pages = n_pages;
   p.page = page;
-  p.bpp = page / kKv8Tok;
+  p.pages.set(page, Hkv, d);
   p.table_w = table_width;
   p.dest_w = dest_width;
   p.keep = keep;
