@@ -227,20 +227,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_select_kernel(const EvictPara
       }
       if (pass == 0 && same <= kList) {
         has_list = true;
-        for (int j0 = first + 4 * (warp * 32); j0 < mine; j0 += kChunk) {
-          const int j = j0 + 4 * lane;
-          uint32_t u[4] = {0, 0, 0, 0};
-          if (j < mine) numbers(j, u, false);
+        for (int j = first + 4 * tid; j < mine; j += kChunk) {
+          uint32_t u[4];
+          numbers(j, u, false);
+          uint32_t hit = 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool in = j + i < mine && u[i] >> 21 == low >> 21;
-            const uint32_t who = __ballot_sync(0xffffffffu, in);
-            if (who == 0) continue;
-            int to = 0;
-            if (lane == 0) to = atomicAdd(&sums[2], __popc(who));
-            to = __shfl_sync(0xffffffffu, to, 0) + __popc(who & ((1u << lane) - 1u));
-            if (in) list[to] = u[i];
-          }
+          for (int i = 0; i < 4; ++i) hit |= j + i < mine && u[i] >> 21 == low >> 21 ? 1u << i : 0u;
+          if (hit == 0) continue;
+          int to = atomicAdd(&sums[2], __popc(hit));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((hit >> i) & 1u) list[to++] = u[i];
         }
         __syncthreads();
       }
@@ -262,10 +259,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_select_kernel(const EvictPara
     uint32_t u[4] = {0, 0, 0, 0};
     if (j < mine) numbers(j, u, false);
     int kinds = 0;  // above in the low half, equal in the high
+    uint32_t is_above = 0, is_equal = 0;
+    const bool whole = j0 + kChunk <= mine;  // the same in the CTA
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const bool in = j + i < mine;
-      kinds += (in ? u[i] > low : j + i < end) ? 1 : in && u[i] == low ? 1 << 16 : 0;
+      const bool in = whole || j + i < mine;
+      const bool a = in ? u[i] > low : j + i < end, q = in && u[i] == low;
+      is_above |= a ? 1u << i : 0u;
+      is_equal |= q ? 1u << i : 0u;
+      kinds += (a ? 1 : 0) + (q ? 1 << 16 : 0);
     }
     int incl = kinds;
 #pragma unroll
@@ -278,18 +280,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_select_kernel(const EvictPara
     const int t = lane < kWarps ? totals[buf][lane] : 0;
     const int before = incl - kinds + __reduce_add_sync(0xffffffffu, lane < warp ? t : 0);
     const int chunk = __reduce_add_sync(0xffffffffu, t);
-    int ab = above + (before & 0xFFFF), eq = equal + (before >> 16);
+    int eq = equal + (before >> 16), to = above + (before & 0xFFFF) + min(eq, need);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const bool in = j + i < mine, is_equal = in && u[i] == low;
-      const bool is_above = in ? u[i] > low : j + i < end;
-      if (is_above || (is_equal && eq < need)) {
-        const int to = ab + min(eq, need);
+      const bool q = (is_equal >> i) & 1u;
+      if (((is_above >> i) & 1u) || (q && eq < need)) {
         kept[to] = j + i;
-        if (out) out[to] = !in || u[i] == kLowest ? __ldg(w + j + i) : weight_of(u[i]);
+        if (out)
+          out[to] = (!whole && j + i >= mine) || u[i] == kLowest ? __ldg(w + j + i) : weight_of(u[i]);
+        ++to;
       }
-      ab += is_above;
-      eq += is_equal;
+      eq += q;
     }
     above += chunk & 0xFFFF;
     equal += chunk >> 16;
