@@ -491,6 +491,8 @@ size_t kv8_page_bytes(int page, int Hkv, int d);  /* 0 for sizes it cannot hold 
  * A block that has keys before its first new row keeps them: its scales become the
  * larger of what they were and what the new rows need, and where one grows the
  * codes that are there are rounded again (exact but for codes that become subnormal).
+ * (Such keys are those of earlier calls: in a page that was never written a sequence
+ * starts at a multiple of 16.)
  * A block whose first row is new starts afresh, its rows behind the last key become
  * zeros.  Every other byte of the cache keeps its value.  Blocks that two sequences of
  * a call share race.

@@ -254,6 +254,8 @@ def test_attention_workspace(L):
     assert base > 4096 and f(2, 1, 4, 2, 64, 512) == base + 4 * (8 + 2 * 2 * 2 * 512)
     for a in ((0, 1, 4, 2, 64, 0), (2, 1, 5, 2, 64, 0), (2, 1, 4, 2, 64, -1), (2, 0, 4, 2, 64, 0)):
         assert f(*a) == 0
+    assert f(1 << 20, 1, 1 << 10, 1 << 10, 64, 1 << 30) == 0     # past any memory
+    assert _attn(L, B=1 << 20, w=_p(7), wo=_p(8), width=1 << 26) == 2
     # a workspace without room for the scores is refused
     assert _attn(L, w=_p(7), wo=_p(8), wsb=base) == 1
 
@@ -272,7 +274,7 @@ def test_evict_refusals(L):
                dict(dest=_p(5)), dict(kept=_p(0, 64))):
         assert call(**kw) == 1, kw
     for kw in (dict(d=48), dict(page=8), dict(width=1 << 27), dict(dwidth=1 << 27),
-               dict(B=1 << 18, H=1 << 12)):
+               dict(B=1 << 18, H=1 << 12), dict(B=1 << 27, H=1, keep=1, recent=0)):
         assert call(**kw) == 2, kw
     for kw in (dict(cache=_p(0, 8)), dict(w=_p(3, 2)), dict(kept=_p(6, 1)), dict(wo=_p(7, 3))):
         assert call(**kw) == 3, kw

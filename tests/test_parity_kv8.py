@@ -773,6 +773,87 @@ def test_a_run_of_decode_steps_with_evictions(T, captured):
     assert T.device_error() == 0
 
 
+def test_a_captured_eviction_replays_with_other_lengths_and_weights(T):
+    """Append, attention with weights, eviction and reading back in one graph."""
+    import torch
+    H, d, page, keep, n0 = 2, 64, 16, 30, 100
+    table, n_pages, free = tables([n0], page, 195, spare=3)
+    dest = free[:2][None]
+    cache = cache_of(T, n_pages, page, H, d)
+    rk, rv = O.Kv8Rows(H, d), O.Kv8Rows(H, d)
+    k, v = rows((1, n0, H, d), 196), rows((1, n0, H, d), 197)
+    lens = ints([70])
+    kd, vd = to_dev(k[:, :70]), to_dev(v[:, :70])
+    T.kv8_append(kd, vd, to_dev(table), lens, cache, page)
+    rk.append(k[0, :70]), rv.append(v[0, :70])
+    td, dd = to_dev(table), to_dev(dest)
+    q = to_dev(S.normal((1, 1, H, d), 198, 0))
+    k1, v1 = to_dev(k[:, :1]), to_dev(v[:, :1])
+    w = torch.zeros((1, H, table.shape[1] * page), device="cuda")
+    ws = torch.zeros(T.mha_fwd_kv8_workspace_bytes(1, 1, H, H, d, w.shape[2]), dtype=torch.uint8,
+                     device="cuda")
+    nl, kept = torch.zeros_like(lens), torch.zeros((1, H, keep), dtype=torch.int32, device="cuda")
+    wo, o = torch.zeros((1, H, 32), device="cuda"), torch.zeros_like(q)
+    back = torch.zeros((1, keep, H, d), device="cuda"), torch.zeros((1, keep, H, d), device="cuda")
+    slots = to_dev(slots_of(dest, 0, keep, page))
+
+    def step():
+        T.kv8_append(k1, v1, td, lens, cache, page)
+        T.mha_fwd_kv8(q, cache, td, lens, H, page, out=o, weights=w, weights_out=w, workspace=ws)
+        T.kv8_evict(cache, td, lens, w, dd, H, d, page, keep, 5, nl, kept, wo)
+        T.kv8_load(cache, slots, H, d, page, out=back)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for n in range(70, n0):
+        k1.copy_(to_dev(k[:, n:n + 1]))
+        v1.copy_(to_dev(v[:, n:n + 1]))
+        lens.fill_(n + 1)
+        graph.replay()
+        rk.append(k[0, n:n + 1]), rv.append(v[0, n:n + 1])
+        torch.cuda.synchronize()
+        ids = O.kv8_kept(to_f64(w)[0, :, :n + 1], keep, 5)
+        np.testing.assert_array_equal(kept[0].cpu().numpy(), ids)
+        np.testing.assert_array_equal(to_f64(wo)[0, :, :keep],
+                                      np.take_along_axis(to_f64(w)[0], ids, 1))
+        np.testing.assert_array_equal(to_f64(back[0])[0], rk.evicted(ids).values)
+        np.testing.assert_array_equal(to_f64(back[1])[0], rv.evicted(ids).values)
+        assert nl.tolist() == [keep]
+    assert T.device_error() == 0
+
+
+def test_many_sequences_and_misaligned_weights(T):
+    """More sequences than a CTA has threads, weights off 16 bytes."""
+    import torch
+    lens = [int(x) for x in S.rng(6).integers(0, 50, 300)]
+    H, d, page = 2, 32, 16
+    cache, table, sl, ks, vs, _ = build(T, lens, H, d, page, 210)
+    q = S.normal((300, 1, 4, d), 211, 0)
+    cap = table.shape[1] * page
+    w = torch.rand(300 * H * cap + 3, device="cuda")
+    wi = w[1:-2].view(300, H, cap)
+    wo = torch.zeros(300 * H * cap + 3, device="cuda")[3:].view(300, H, cap)
+    o, wo = T.mha_fwd_kv8(to_dev(q), cache, table, sl, H, page, weights=wi, weights_out=wo)
+    g, g0 = to_f64(wo), to_f64(wi)
+    for b, n in enumerate(lens):
+        check_rows(o[b], None, q[b], ks[b].values, vs[b].values, 1, 0, None, g[b, :, :n],
+                   g0[b, :, :n])
+        np.testing.assert_array_equal(g[b, :, n:], g0[b, :, n:])
+    # one call adds one row to each of them
+    k, v = rows((300, 1, H, d), 212), rows((300, 1, H, d), 213)
+    t2, n_pages, _ = tables([n + 1 for n in lens], page, 214)
+    c2 = cache_of(T, n_pages, page, H, d)
+    for b, n in enumerate(lens):
+        if n:
+            x = [to_dev(rows((1, n, H, d), 210 + b, stream=s)) for s in (0, 3)]
+            T.kv8_append(*x, to_dev(t2[b:b + 1]), ints([n]), c2, page)
+    T.kv8_append(to_dev(k), to_dev(v), to_dev(t2), sl + 1, c2, page)
+    for b in range(0, 300, 7):
+        assert_held(T, c2, t2, b, page, ks[b].append(k[b]), vs[b].append(v[b]), str(b))
+    assert T.device_error() == 0
+
+
 def test_streams(T):
     """Calls on a stream other than the current one, results made in the call."""
     import torch

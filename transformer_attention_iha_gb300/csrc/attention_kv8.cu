@@ -904,8 +904,8 @@ __global__ void __launch_bounds__(kWeighKeys / 4) kv8_weigh_kernel(const WeighPa
     const float4 v = __ldcg(reinterpret_cast<const float4*>(
         p.scores + (plane * (int64_t)p.a.ncols + col) * p.cap + j));
     const float x[4] = {v.x, v.y, v.z, v.w};
-    const float lse =
-        __ldg(p.a.lse + ((int64_t)b * p.a.Hq + qh) * p.a.Nq + qi) * 1.4426950408889634f;
+    const float lse =  // (scores and lse: not through the read-only path)
+        __ldcg(p.a.lse + ((int64_t)b * p.a.Hq + qh) * p.a.Nq + qi) * 1.4426950408889634f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)  // outside [lo, hi) the score may be anything
       if (j + i >= lo && j + i < hi && x[i] != -INFINITY) sum[i] += exp2f(x[i] - lse);
@@ -959,6 +959,7 @@ size_t mha_fwd_kv8_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, int we
   if (B <= 0 || Nq <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv || d <= 0 || weight_keys < 0) return 0;
   const int64_t ncols = (int64_t)Nq * (Hq / Hkv);
   size_t n = iha::kCounterBytes + iha::part_bytes(ncols, d);
+  if (weight_keys > 0 && (double)B * Hkv * ncols * weight_keys > 1e15) return 0;  // no such
   if (weight_keys > 0)  // the rows' lse, their scores
     n += (iha::lse_floats(B, Hq, Nq) + (size_t)B * Hkv * ncols * weight_keys) * sizeof(float);
   return n;
@@ -976,6 +977,8 @@ iha_status mha_fwd_kv8(const void* q, const void* cache, const int32_t* block_ta
   if ((weights == nullptr) != (weights_out == nullptr))
     return fail(IHA_ERR_INVALID_ARG, "%s: weights and weights_out go together", name);
   const int keys = weights && cap > 0 && cap <= (1 << 30) ? (int)cap : 0;
+  if (keys > 0 && Nq > 0 && Hkv > 0 && (double)B * Hq * Nq * keys > 1e15)
+    return fail(IHA_ERR_UNSUPPORTED, "%s: too many scores", name);
   Kv8AttnParams p;
   int nt, grid;
   iha_status st = kv_attn_setup(
@@ -994,9 +997,9 @@ iha_status mha_fwd_kv8(const void* q, const void* cache, const int32_t* block_ta
       return fail(IHA_ERR_ALIGNMENT, "%s: weights must be 4-byte aligned", name);
     bool neg;
     auto span_of = [&](const iha_strides& t) { return view_bytes(t, B, 1, Nq, Hq, d, 2, &neg); };
-    const int64_t nw = (int64_t)B * Hkv * cap * 4, no = span_of(p.so);
     if ((int64_t)B * Hkv * ((cap + kWeighKeys - 1) / kWeighKeys) > INT32_MAX)
       return fail(IHA_ERR_UNSUPPORTED, "%s: too many weights for one launch", name);
+    const int64_t nw = (int64_t)B * Hkv * cap * 4, no = span_of(p.so);
     if ((weights != weights_out && overlaps(weights, nw, weights_out, nw)) ||
         overlaps(weights_out, nw, q, span_of(p.sq)) ||
         overlaps(weights_out, nw, cache, (int64_t)n_pages * (int64_t)kv8_page_bytes(page, Hkv, d)) ||
