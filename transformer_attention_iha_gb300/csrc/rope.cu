@@ -13,7 +13,11 @@
 // through sincospif: off by about 2^-24 in all.
 //
 // A thread takes 32 bytes of a row, 8 pairs of bf16 or 4 of fp32, works out their
-// sines once and applies them to up to `hg` heads of its token.
+// sines once and applies them to up to `hg` heads of its token.  (Where a half of the
+// pairs does not start on 16 bytes: one pair, 2 or 4 bytes at a time.)
+//
+// Bound by HBM: 32768 tokens x 40 heads of 128, bf16, 671 MB: 103 us, 6.5 TB/s (CTAs of
+// 256 threads 110); 8192 x 160 101 us, 6.6; half of each head rotated 5.4; pairs one by one 1.8.
 #include <math.h>
 
 #include "kv4.cuh"
@@ -22,7 +26,7 @@ namespace iha {
 namespace {
 
 constexpr int kMaxPairs = 128;
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kBatch = 4;  // heads whose rows a thread loads at once
 
 struct RopeParams {
@@ -33,6 +37,7 @@ struct RopeParams {
   FastDiv units, groups, N;  // units of a row, groups of heads of a token, tokens of a sequence
   int items;                 // tokens * groups * units
   int turning;               // units that turn; the rest copy
+  int copy_step;             // features between a copying unit's two vectors; 0: it has one
   int Hq, H, hg;             // heads of q, of both, of a group
   int rot;
   float gain, sign;
@@ -89,7 +94,8 @@ __global__ void __launch_bounds__(kRopeThreads)
   // the thread's two vectors (or features) in a row
   int at0, at1;
   if (!turns) {
-    at0 = at1 = p.rot + (u - p.turning) * (VEC ? V : 1);
+    at0 = p.rot + (u - p.turning) * (VEC ? V : 1);
+    at1 = at0 + p.copy_step;
   } else if (INTER) {
     at0 = u * 2 * PAIRS;
     at1 = at0 + PAIRS;
@@ -128,7 +134,7 @@ __global__ void __launch_bounds__(kRopeThreads)
         if (h0 + j < head1) {
           const T* x = row(h0 + j, false);
           v[j][0] = *reinterpret_cast<const uint4*>(x + at0);
-          if (turns) v[j][1] = *reinterpret_cast<const uint4*>(x + at1);
+          v[j][1] = *reinterpret_cast<const uint4*>(x + at1);  // (copying one: the same again)
         }
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
@@ -136,6 +142,7 @@ __global__ void __launch_bounds__(kRopeThreads)
         T* y = row(h0 + j, true);
         if (!turns) {
           *reinterpret_cast<uint4*>(y + at0) = v[j][0];
+          *reinterpret_cast<uint4*>(y + at1) = v[j][1];
           continue;
         }
         float f[2][V], g[2][V];
@@ -280,10 +287,17 @@ iha_status rotate(const char* name, bool back, const void* q, const void* k,
   // vectors where both halves of a turn start on 16 bytes
   const bool vec = rope->rot / 2 % V == 0;
   p.turning = vec ? rope->rot / 2 / V : rope->rot / 2;
-  const int units = p.turning + (vec ? (d - rope->rot) / V : d - rope->rot);
+  int copying = vec ? (d - rope->rot) / V : d - rope->rot;
+  p.copy_step = 0;
+  if (vec && copying % 2 == 0 && copying > 0) {
+    copying /= 2;
+    p.copy_step = copying * V;
+  }
+  const int units = p.turning + copying;
   // heads of a thread: its sines cost about as much as four heads' rows, so as many as
-  // leave half of the GPU's threads (3003 tokens x 40 heads of 96, fp32: 18.1 us, with two
-  // full waves left 26.3; 32768 tokens x 40 heads of 128, bf16: 110 us, one head 222)
+  // leave half of the GPU's threads (32768 tokens x 40 heads of 128: one head a thread 222
+  // us, 8 110, 16 112; 3003 tokens x 40 heads of 96, fp32: two full waves left 26, half
+  // a wave 18)
   p.hg = 1;
   while (p.hg < 8 && toks * p.H * units / (2 * p.hg) >= 1024 * (int64_t)sm_count()) p.hg *= 2;
   const int groups = (p.H + p.hg - 1) / p.hg;
