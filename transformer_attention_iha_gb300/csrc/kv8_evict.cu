@@ -305,11 +305,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_select_kernel(const EvictPara
   if (size > 1) cluster_sync();  // the others have read this CTA's sums
 }
 
+constexpr int kCopyWarps = 4;
+
 template <int D>
-__global__ void __launch_bounds__(256) kv8_copy_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(32 * kCopyWarps) kv8_copy_kernel(const EvictParams p) {
   constexpr int LPR = D / 16, RPI = 32 / LPR, ITER = (kKv8Tok + RPI - 1) / RPI;
   const int lane = threadIdx.x & 31;
-  const int64_t id64 = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int64_t id64 = (int64_t)blockIdx.x * kCopyWarps + (threadIdx.x >> 5);
   if (id64 >= p.items) return;
   const int id = (int)id64, plane = p.blocks.div(id), blk = id - plane * p.blocks.d;
   const int b = p.heads.div(plane), head = plane - b * p.heads.d;
@@ -496,8 +498,8 @@ iha_status kv8_evict(void* cache, const int32_t* block_table, const int32_t* seq
   if (le != cudaSuccess) return fail(IHA_ERR_CUDA, "%s: %s", name, cudaGetErrorString(le));
   st = check_launch(name);
   if (st != IHA_OK) return st;
-  const unsigned grid = (unsigned)((p.items + 7) / 8);
-  IHA_KV8_D_SWITCH(d, return launch_behind(name, kv8_copy_kernel<kD>, grid, 256, s, p))
+  const unsigned grid = (unsigned)((p.items + kCopyWarps - 1) / kCopyWarps);
+  IHA_KV8_D_SWITCH(d, return launch_behind(name, kv8_copy_kernel<kD>, grid, 32 * kCopyWarps, s, p))
   return IHA_OK;
 }
 
