@@ -531,6 +531,24 @@ def test_weights_in_place_and_workspaces(T):
     assert T.device_error() == 0
 
 
+def test_weights_of_a_table_far_wider_than_its_sequences(T):
+    """Weights apart and in place; each CTA of the sum takes several stretches of keys."""
+    import torch
+    lens, H, d, page = [37, 20000], 40, 32, 64
+    cache, table, sl, ks, vs, _ = build(T, lens, H, d, page, 137, width=700)
+    q = S.normal((2, 1, H, d), 138, 0)
+    w = torch.rand((2, H, 700 * page), device="cuda")
+    w0 = to_f64(w)
+    o, w1 = T.mha_fwd_kv8(to_dev(q), cache, table, sl, H, page, weights=w)
+    o, w2 = T.mha_fwd_kv8(to_dev(q), cache, table, sl, H, page, weights=w, weights_out=w)
+    assert w2 is w and torch.equal(w1, w)
+    g = to_f64(w1)
+    for b, n in enumerate(lens):
+        check_rows(o[b], None, q[b], ks[b].values, vs[b].values, 1, 0, None, g[b, :, :n],
+                   w0[b, :, :n])
+        np.testing.assert_array_equal(g[b, :, n:], w0[b, :, n:])
+
+
 def test_two_calls_at_once(T):
     """Two streams, a workspace each, in flight together; then each on its own."""
     import torch

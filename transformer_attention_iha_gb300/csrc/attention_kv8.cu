@@ -17,6 +17,16 @@
 //   Softmax in the log2 domain, fp32; a column's reference moves only when a score
 //     exceeds it, to 8 above that score (a token that weighs alone has p = 2^-8, and
 //     its P s exactly); then O and the sum are rescaled.
+// Work: the line of kv_attn.cuh; each warp keeps a ring of two stages of two blocks (d =
+// 128) that bulk copies fill ahead, codes and tails apart.  Calls with weights keep the scores
+// (4 bytes where K and V have 2 d), and a second kernel adds exp(score - lse) up.
+//
+// What bounds it: long contexts HBM (131071 keys x 80 heads of 128, 2.69 GB: 401 to 411 us,
+// 6.5 to 6.7 TB/s; 137 registers, 12 warps an SM, 34 per cent of the issue slots); there the
+// SMs come to an end between 302 and 400 us, by their place on the chip.  Ragged batches (16
+// sequences of up to 8192 keys, 8 key heads, 103 MB): 32 us with 16 columns, 27 with 4, of
+// which 3 until copies are under way, 15 at HBM's rate, the rest imbalance, parts and joins.
+// 777 keys x 80 heads: latency, 12.3 us.
 #include <cuda_fp16.h>
 
 #include "kv8.cuh"
@@ -873,49 +883,60 @@ struct WeighParams {
   int chunks;  // CTAs of a head
 };
 
-constexpr int kWeighKeys = 1024;  // keys of a CTA
+constexpr int kWeighKeys = 1024;  // keys that a CTA takes at a time
 
 // out[b, h, j] = weights[b, h, j] + the sum over columns of exp(score - lse), four
-// neighbouring keys a thread (VEC: as vectors).
+// neighbouring keys a thread (VEC: as vectors).  Launched behind the attention: the first
+// weights are on their way while that ends.  (1 token over 4 ragged sequences of up to
+// 32768 keys x 20 heads: 5 to 8 us behind the attention's 74.)
 template <bool VEC>
 __global__ void __launch_bounds__(kWeighKeys / 4) kv8_weigh_kernel(const WeighParams p) {
   const int plane = blockIdx.x / p.chunks, b = plane / p.a.Hkv, hk = plane - b * p.a.Hkv;
-  const int j = ((int)blockIdx.x - plane * p.chunks) * kWeighKeys + 4 * (int)threadIdx.x;
+  const int chunk = (int)blockIdx.x - plane * p.chunks;
   const int len = seq_len(p.a, b);
-  const int64_t at = plane * p.cap + j;
-  float w[4] = {0.f, 0.f, 0.f, 0.f}, sum[4] = {0.f, 0.f, 0.f, 0.f};
-  const bool idle = j >= p.cap || (j >= len && p.weights == p.out);
-  if (!idle) {
+  // behind the last key weights are copied; in place there is nothing to do
+  const int64_t end = p.weights == p.out ? len : p.cap;
+  float w[4] = {0.f, 0.f, 0.f, 0.f};
+  auto load = [&](int64_t j) {
+    const float* from = p.weights + plane * p.cap + j;
     if (VEC) {
-      const float4 v = *reinterpret_cast<const float4*>(p.weights + at);
+      const float4 v = *reinterpret_cast<const float4*>(from);
       w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = p.weights[at + i];
+      for (int i = 0; i < 4; ++i) w[i] = from[i];
     }
-  }
+  };
+  const int64_t first = (int64_t)chunk * kWeighKeys + 4 * (int)threadIdx.x;
+  if (first < end) load(first);
   wait_for_grid();
-  if (idle) return;
-  for (int col = 0; j < len && col < p.a.ncols; ++col) {
-    int lo, hi;
-    col_range(p.a, len, col, lo, hi);
-    if (j + 4 <= lo || j >= hi) continue;
-    const int qi = token_of(p.a, col), qh = hk * p.a.G + (col - qi * p.a.G);
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(
-        p.scores + (plane * (int64_t)p.a.ncols + col) * p.cap + j));
-    const float x[4] = {v.x, v.y, v.z, v.w};
-    const float lse =  // (scores and lse: not through the read-only path)
-        __ldcg(p.a.lse + ((int64_t)b * p.a.Hq + qh) * p.a.Nq + qi) * 1.4426950408889634f;
+  for (int64_t j64 = first; j64 < end; j64 += (int64_t)p.chunks * kWeighKeys) {
+    const int j = (int)j64;
+    if (j64 != first) load(j64);
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int col = 0; j < len && col < p.a.ncols; ++col) {
+      int lo, hi;
+      col_range(p.a, len, col, lo, hi);
+      if (j + 4 <= lo || j >= hi) continue;
+      const int qi = token_of(p.a, col), qh = hk * p.a.G + (col - qi * p.a.G);
+      // (scores and lse: not through the read-only path)
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(
+          p.scores + (plane * (int64_t)p.a.ncols + col) * p.cap + j));
+      const float x[4] = {v.x, v.y, v.z, v.w};
+      const float lse =
+          __ldcg(p.a.lse + ((int64_t)b * p.a.Hq + qh) * p.a.Nq + qi) * 1.4426950408889634f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)  // outside [lo, hi) the score may be anything
-      if (j + i >= lo && j + i < hi && x[i] != -INFINITY) sum[i] += exp2f(x[i] - lse);
-  }
-  if (VEC) {
-    *reinterpret_cast<float4*>(p.out + at) =
-        make_float4(w[0] + sum[0], w[1] + sum[1], w[2] + sum[2], w[3] + sum[3]);
-  } else {
+      for (int i = 0; i < 4; ++i)  // outside [lo, hi) the score may be anything
+        if (j + i >= lo && j + i < hi && x[i] != -INFINITY) sum[i] += exp2f(x[i] - lse);
+    }
+    float* to = p.out + plane * p.cap + j;
+    if (VEC) {
+      *reinterpret_cast<float4*>(to) =
+          make_float4(w[0] + sum[0], w[1] + sum[1], w[2] + sum[2], w[3] + sum[3]);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p.out[at + i] = w[i] + sum[i];
+      for (int i = 0; i < 4; ++i) to[i] = w[i] + sum[i];
+    }
   }
 }
 
@@ -997,8 +1018,8 @@ iha_status mha_fwd_kv8(const void* q, const void* cache, const int32_t* block_ta
       return fail(IHA_ERR_ALIGNMENT, "%s: weights must be 4-byte aligned", name);
     bool neg;
     auto span_of = [&](const iha_strides& t) { return view_bytes(t, B, 1, Nq, Hq, d, 2, &neg); };
-    if ((int64_t)B * Hkv * ((cap + kWeighKeys - 1) / kWeighKeys) > INT32_MAX)
-      return fail(IHA_ERR_UNSUPPORTED, "%s: too many weights for one launch", name);
+    if ((int64_t)B * Hkv > (1 << 26))
+      return fail(IHA_ERR_UNSUPPORTED, "%s: weights of more than 2^26 heads", name);
     const int64_t nw = (int64_t)B * Hkv * cap * 4, no = span_of(p.so);
     if ((weights != weights_out && overlaps(weights, nw, weights_out, nw)) ||
         overlaps(weights_out, nw, q, span_of(p.sq)) ||
@@ -1021,8 +1042,11 @@ iha_status mha_fwd_kv8(const void* q, const void* cache, const int32_t* block_ta
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   IHA_KV8_D_SWITCH(d, st = launch<kD>(p, nt, grid, s))
   if (st != IHA_OK || !weights) return st;
-  const WeighParams w = {p, p.scores, weights, weights_out, cap,
-                         (int)((cap + kWeighKeys - 1) / kWeighKeys)};
+  // CTAs of a head: for all of its keys, but no more than fill the GPU (the table may be
+  // far wider than the sequences)
+  const int64_t all = (cap + kWeighKeys - 1) / kWeighKeys;
+  const int64_t fill = (8 * (int64_t)sm_count() + (int64_t)B * Hkv - 1) / ((int64_t)B * Hkv);
+  const WeighParams w = {p, p.scores, weights, weights_out, cap, (int)(all < fill ? all : fill)};
   const unsigned ctas = (unsigned)(B * Hkv * w.chunks);
   return launch_behind(name, aligned16(weights) && aligned16(weights_out) ? kv8_weigh_kernel<true>
                                                                           : kv8_weigh_kernel<false>,
