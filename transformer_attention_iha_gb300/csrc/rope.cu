@@ -9,8 +9,8 @@
 // Angles: a pair's frequency is held as turns per position in 64-bit fixed point,
 // turn = w / 2 pi * 2^64 mod 2^64, so position * turn in 64-bit integers is the angle
 // in turns modulo 1 for any position, without the loss of a 32-bit product (position
-// 2^20 in fp32 is off by 2^-4 radians).  Its upper 32 bits, as a signed number, go
-// through sincospif: off by about 2^-24 in all.
+// 2^20 in fp32 is off by 2^-4 radians).  Of its upper 32 bits the nearest quarter of a turn
+// is taken off, the rest goes through sincospif: off by about 2^-24 in all.
 //
 // A thread takes 32 bytes of a row, 8 pairs of bf16 or 4 of fp32, works out their
 // sines once and applies them to up to `hg` heads of its token.  (Where a half of the
@@ -108,10 +108,13 @@ __global__ void __launch_bounds__(kRopeThreads)
     const int64_t pos = p.pos ? __ldg(p.pos + tok) : n;
 #pragma unroll
     for (int i = 0; i < PAIRS; ++i) {
-      const int32_t part = (int32_t)(((uint64_t)pos * turn[u * PAIRS + i]) >> 32);
-      sincospif((float)part * 4.656612873077393e-10f, &sn[i], &cs[i]);  // 2^-31
-      cs[i] *= p.gain;
-      sn[i] *= p.sign;
+      // q quarters of a turn and a rest of up to an eighth, which fp32 holds to 2^-28 turns
+      const uint32_t part = (uint32_t)(((uint64_t)pos * turn[u * PAIRS + i]) >> 32);
+      const uint32_t q = (part + 0x20000000u) >> 30;
+      float sr, cr;
+      sincospif((float)(int32_t)(part - (q << 30)) * 4.656612873077393e-10f, &sr, &cr);  // 2^-31
+      sn[i] = __uint_as_float(__float_as_uint(q & 1u ? cr : sr) ^ (q & 2u) << 30) * p.sign;
+      cs[i] = __uint_as_float(__float_as_uint(q & 1u ? sr : cr) ^ ((q + 1u) & 2u) << 30) * p.gain;
     }
   }
   const T* q = static_cast<const T*>(p.q) + b * p.sq.b_outer + n * p.sq.seq;
