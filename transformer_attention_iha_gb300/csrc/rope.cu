@@ -13,11 +13,11 @@
 // is taken off, the rest goes through sincospif: off by about 2^-24 in all.
 //
 // A thread takes 32 bytes of a row, 8 pairs of bf16 or 4 of fp32, works out their
-// sines once and applies them to up to `hg` heads of its token.  (Where a half of the
-// pairs does not start on 16 bytes: one pair, 2 or 4 bytes at a time.)
+// sines once and applies them to up to `hg` heads of its token.
 //
 // Bound by HBM: 32768 tokens x 40 heads of 128, bf16, 671 MB: 103 us, 6.5 TB/s (CTAs of
-// 256 threads 110); 8192 x 160 101 us, 6.6; half of each head rotated 5.4; pairs one by one 1.8.
+// 256 threads 110); 8192 x 160 101 us, 6.6; half of each head rotated 5.4.  Halves off 16
+// bytes: 50 of 80 features 2.8, 100 of 128 3.6 (pair by pair from memory 1.8 and 2.3).
 #include <math.h>
 
 #include "kv4.cuh"
@@ -35,8 +35,8 @@ struct RopeParams {
   const int32_t* pos;  // null: the place in the sequence
   iha_strides sq, sk, tq, tk;
   FastDiv units, groups, N;  // units of a row, groups of heads of a token, tokens of a sequence
-  int items;                 // tokens * groups * units
-  int turning;               // units that turn; the rest copy
+  int items;                 // threads (warps) with work
+  int turning;               // units that turn, the rest copy (vectors that hold turned ones)
   int copy_step;             // features between a copying unit's two vectors; 0: it has one
   int Hq, H, hg;             // heads of q, of both, of a group
   int rot;
@@ -70,17 +70,44 @@ __device__ __forceinline__ uint4 repack(const float (&f)[4]) {
   return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
                     __float_as_uint(f[3]));
 }
+// The sine and cosine of a pair at a position, each times its factor.
+__device__ __forceinline__ void turn_of(int64_t pos, uint64_t turn, float gain, float sign,
+                                        float& sn, float& cs) {
+  // q quarters of a turn and a rest of up to an eighth, which fp32 holds to 2^-28 turns
+  const uint32_t part = (uint32_t)(((uint64_t)pos * turn) >> 32);
+  const uint32_t q = (part + 0x20000000u) >> 30;
+  float sr, cr;
+  sincospif((float)(int32_t)(part - (q << 30)) * 4.656612873077393e-10f, &sr, &cr);  // 2^-31
+  sn = __uint_as_float(__float_as_uint(q & 1u ? cr : sr) ^ (q & 2u) << 30) * sign;
+  cs = __uint_as_float(__float_as_uint(q & 1u ? sr : cr) ^ ((q + 1u) & 2u) << 30) * gain;
+}
 __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void narrow(float* p, float x) { *p = x; }
 __device__ __forceinline__ void narrow(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// VEC: 16-byte vectors; else a thread takes one pair, or one feature to copy.
-template <typename T, bool INTER, bool VEC>
+// Rows of q, then of k, of one token.
+template <typename T>
+struct TokenRows {
+  const T *q, *k;
+  T *yq, *yk;
+  __device__ __forceinline__ TokenRows(const RopeParams& p, int b, int n)
+      : q(static_cast<const T*>(p.q) + b * p.sq.b_outer + n * p.sq.seq),
+        k(static_cast<const T*>(p.k) + (p.k ? b * p.sk.b_outer + n * p.sk.seq : 0)),
+        yq(static_cast<T*>(p.yq) + b * p.tq.b_outer + n * p.tq.seq),
+        yk(static_cast<T*>(p.yk) + (p.k ? b * p.tk.b_outer + n * p.tk.seq : 0)) {}
+  __device__ __forceinline__ const T* in(const RopeParams& p, int h) const {
+    return h < p.Hq ? q + h * p.sq.head : k + (h - p.Hq) * p.sk.head;
+  }
+  __device__ __forceinline__ T* out(const RopeParams& p, int h) const {
+    return h < p.Hq ? yq + h * p.tq.head : yk + (h - p.Hq) * p.tk.head;
+  }
+};
+
+template <typename T, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads)
     rope_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int V = 16 / sizeof(T);      // features of a vector
-  constexpr int PAIRS = VEC ? V : 1;     // pairs of a thread
+  constexpr int V = 16 / sizeof(T);  // features of a vector, pairs of a thread
   __shared__ uint64_t turn[kMaxPairs];
   for (int i = threadIdx.x; i < p.rot / 2; i += kRopeThreads) turn[i] = p.turn[i];
   __syncthreads();
@@ -91,109 +118,129 @@ __global__ void __launch_bounds__(kRopeThreads)
   const int b = p.N.div(tok), n = tok - b * p.N.d;
   const int head1 = min(head0 + p.hg, p.H);
   const bool turns = u < p.turning;
-  // the thread's two vectors (or features) in a row
+  // the thread's two vectors in a row
   int at0, at1;
   if (!turns) {
-    at0 = p.rot + (u - p.turning) * (VEC ? V : 1);
+    at0 = p.rot + (u - p.turning) * V;
     at1 = at0 + p.copy_step;
   } else if (INTER) {
-    at0 = u * 2 * PAIRS;
-    at1 = at0 + PAIRS;
+    at0 = u * 2 * V;
+    at1 = at0 + V;
   } else {
-    at0 = u * PAIRS;
+    at0 = u * V;
     at1 = p.rot / 2 + at0;
   }
-  float cs[PAIRS], sn[PAIRS];
+  float cs[V], sn[V];
   if (turns) {
     const int64_t pos = p.pos ? __ldg(p.pos + tok) : n;
 #pragma unroll
-    for (int i = 0; i < PAIRS; ++i) {
-      // q quarters of a turn and a rest of up to an eighth, which fp32 holds to 2^-28 turns
-      const uint32_t part = (uint32_t)(((uint64_t)pos * turn[u * PAIRS + i]) >> 32);
-      const uint32_t q = (part + 0x20000000u) >> 30;
-      float sr, cr;
-      sincospif((float)(int32_t)(part - (q << 30)) * 4.656612873077393e-10f, &sr, &cr);  // 2^-31
-      sn[i] = __uint_as_float(__float_as_uint(q & 1u ? cr : sr) ^ (q & 2u) << 30) * p.sign;
-      cs[i] = __uint_as_float(__float_as_uint(q & 1u ? sr : cr) ^ ((q + 1u) & 2u) << 30) * p.gain;
-    }
+    for (int i = 0; i < V; ++i) turn_of(pos, turn[u * V + i], p.gain, p.sign, sn[i], cs[i]);
   }
-  const T* q = static_cast<const T*>(p.q) + b * p.sq.b_outer + n * p.sq.seq;
-  const T* k = static_cast<const T*>(p.k) + (p.k ? b * p.sk.b_outer + n * p.sk.seq : 0);
-  T* yq = static_cast<T*>(p.yq) + b * p.tq.b_outer + n * p.tq.seq;
-  T* yk = static_cast<T*>(p.yk) + (p.k ? b * p.tk.b_outer + n * p.tk.seq : 0);
-  auto row = [&](int h, bool out) -> T* {
-    const bool isq = h < p.Hq;
-    if (out) return isq ? yq + h * p.tq.head : yk + (h - p.Hq) * p.tk.head;
-    return const_cast<T*>(isq ? q + h * p.sq.head : k + (h - p.Hq) * p.sk.head);
-  };
+  const TokenRows<T> rows(p, b, n);
   // all of a batch's loads before its first store (a row turned in place is read and
   // written by the same thread)
 #pragma unroll 1
   for (int h0 = head0; h0 < head1; h0 += kBatch) {
-    if constexpr (VEC) {
-      uint4 v[kBatch][2];
+    uint4 v[kBatch][2];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        if (h0 + j < head1) {
-          const T* x = row(h0 + j, false);
-          v[j][0] = *reinterpret_cast<const uint4*>(x + at0);
-          v[j][1] = *reinterpret_cast<const uint4*>(x + at1);  // (copying one: the same again)
-        }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        if (h0 + j >= head1) break;
-        T* y = row(h0 + j, true);
-        if (!turns) {
-          *reinterpret_cast<uint4*>(y + at0) = v[j][0];
-          *reinterpret_cast<uint4*>(y + at1) = v[j][1];
-          continue;
-        }
-        float f[2][V], g[2][V];
-        unpack<T>(v[j][0], f[0]);
-        unpack<T>(v[j][1], f[1]);
-#pragma unroll
-        for (int i = 0; i < PAIRS; ++i) {
-          // element i of a pair list: (vector, place) of its two features
-          const int va = INTER ? 2 * i / V : 0, ia = INTER ? 2 * i % V : i;
-          const int vb = INTER ? va : 1, ib = INTER ? ia + 1 : i;
-          const float a = f[va][ia], c = f[vb][ib];
-          g[va][ia] = a * cs[i] - c * sn[i];
-          g[vb][ib] = c * cs[i] + a * sn[i];
-        }
-        *reinterpret_cast<uint4*>(y + at0) = repack(g[0]);
-        *reinterpret_cast<uint4*>(y + at1) = repack(g[1]);
+    for (int j = 0; j < kBatch; ++j)
+      if (h0 + j < head1) {
+        const T* x = rows.in(p, h0 + j);
+        v[j][0] = *reinterpret_cast<const uint4*>(x + at0);
+        v[j][1] = *reinterpret_cast<const uint4*>(x + at1);  // (copying one: the same again)
       }
-    } else {
-      T v[kBatch][2];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        if (h0 + j < head1) {
-          const T* x = row(h0 + j, false);
-          v[j][0] = x[at0];
-          if (turns) v[j][1] = x[at1];
-        }
+    for (int j = 0; j < kBatch; ++j) {
+      if (h0 + j >= head1) break;
+      T* y = rows.out(p, h0 + j);
+      if (!turns) {
+        *reinterpret_cast<uint4*>(y + at0) = v[j][0];
+        *reinterpret_cast<uint4*>(y + at1) = v[j][1];
+        continue;
+      }
+      float f[2][V], g[2][V];
+      unpack<T>(v[j][0], f[0]);
+      unpack<T>(v[j][1], f[1]);
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        if (h0 + j >= head1) break;
-        T* y = row(h0 + j, true);
-        if (!turns) {
-          y[at0] = v[j][0];
-          continue;
-        }
-        const float a = widen(v[j][0]), c = widen(v[j][1]);
-        narrow(y + at0, a * cs[0] - c * sn[0]);
-        narrow(y + at1, c * cs[0] + a * sn[0]);
+      for (int i = 0; i < V; ++i) {
+        // element i of a pair list: (vector, place) of its two features
+        const int va = INTER ? 2 * i / V : 0, ia = INTER ? 2 * i % V : i;
+        const int vb = INTER ? va : 1, ib = INTER ? ia + 1 : i;
+        const float a = f[va][ia], c = f[vb][ib];
+        g[va][ia] = a * cs[i] - c * sn[i];
+        g[vb][ib] = c * cs[i] + a * sn[i];
+      }
+      *reinterpret_cast<uint4*>(y + at0) = repack(g[0]);
+      *reinterpret_cast<uint4*>(y + at1) = repack(g[1]);
+    }
+  }
+}
+
+// Pairs whose halves do not start on 16 bytes: a warp takes a token's rows, puts their
+// vectors that hold turned features into shared memory, turns pair by pair there and writes
+// whole vectors back.
+template <typename T, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads)
+    rope_rows_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int V = 16 / sizeof(T), MOST = 2 * kMaxPairs / V;  // vectors that hold turned ones
+  constexpr int LANE_PAIRS = kMaxPairs / 32;
+  __shared__ uint64_t turn[kMaxPairs];
+  __shared__ uint4 held[kRopeThreads / 32][kBatch][MOST];
+  for (int i = threadIdx.x; i < p.rot / 2; i += kRopeThreads) turn[i] = p.turn[i];
+  __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int id = blockIdx.x * (kRopeThreads / 32) + warp;
+  if (id >= p.items) return;
+  const int tok = p.groups.div(id), head0 = (id - tok * p.groups.d) * p.hg;
+  const int b = p.N.div(tok), n = tok - b * p.N.d;
+  const int head1 = min(head0 + p.hg, p.H);
+  float cs[LANE_PAIRS], sn[LANE_PAIRS];
+  const int64_t pos = p.pos ? __ldg(p.pos + tok) : n;
+#pragma unroll
+  for (int i = 0; i < LANE_PAIRS; ++i)
+    if (32 * i + lane < p.rot / 2)
+      turn_of(pos, turn[32 * i + lane], p.gain, p.sign, sn[i], cs[i]);
+  const TokenRows<T> rows(p, b, n);
+  const int held_n = p.turning, all_n = p.units.d;  // vectors to hold, of a row
+#pragma unroll 1
+  for (int h0 = head0; h0 < head1; h0 += kBatch) {
+    const int nrows = min(kBatch, head1 - h0);
+    for (int i = lane; i < nrows * all_n; i += 32) {
+      const int r = p.units.div(i), c = i - r * all_n;
+      const uint4 v = reinterpret_cast<const uint4*>(rows.in(p, h0 + r))[c];
+      if (c < held_n)
+        held[warp][r][c] = v;
+      else
+        reinterpret_cast<uint4*>(rows.out(p, h0 + r))[c] = v;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < LANE_PAIRS; ++i) {
+      const int pair = 32 * i + lane;
+      if (pair >= p.rot / 2) break;
+      const int at0 = INTER ? 2 * pair : pair, at1 = INTER ? at0 + 1 : pair + p.rot / 2;
+      for (int r = 0; r < nrows; ++r) {
+        T* x = reinterpret_cast<T*>(held[warp][r]);
+        const float a = widen(x[at0]), c = widen(x[at1]);
+        narrow(x + at0, a * cs[i] - c * sn[i]);
+        narrow(x + at1, c * cs[i] + a * sn[i]);
       }
     }
+    __syncwarp();
+    for (int i = lane; i < nrows * held_n; i += 32) {
+      const int r = i / held_n, c = i - r * held_n;
+      reinterpret_cast<uint4*>(rows.out(p, h0 + r))[c] = held[warp][r][c];
+    }
+    __syncwarp();
   }
 }
 
 template <typename T, bool INTER>
 void launch(const RopeParams& p, bool vec, unsigned blocks, cudaStream_t s) {
   if (vec)
-    rope_kernel<T, INTER, true><<<blocks, kRopeThreads, 0, s>>>(p);
+    rope_kernel<T, INTER><<<blocks, kRopeThreads, 0, s>>>(p);
   else
-    rope_kernel<T, INTER, false><<<blocks, kRopeThreads, 0, s>>>(p);
+    rope_rows_kernel<T, INTER><<<blocks, kRopeThreads, 0, s>>>(p);
 }
 
 iha_status rotate(const char* name, bool back, const void* q, const void* k,
@@ -289,28 +336,38 @@ iha_status rotate(const char* name, bool back, const void* q, const void* k,
   for (int i = 0; i < rope->rot / 2; ++i) p.turn[i] = rope->turn[i];
   // vectors where both halves of a turn start on 16 bytes
   const bool vec = rope->rot / 2 % V == 0;
-  p.turning = vec ? rope->rot / 2 / V : rope->rot / 2;
-  int copying = vec ? (d - rope->rot) / V : d - rope->rot;
-  p.copy_step = 0;
-  if (vec && copying % 2 == 0 && copying > 0) {
-    copying /= 2;
-    p.copy_step = copying * V;
-  }
-  const int units = p.turning + copying;
-  // heads of a thread: its sines cost about as much as four heads' rows, so as many as
-  // leave half of the GPU's threads (32768 tokens x 40 heads of 128: one head a thread 222
-  // us, 8 110, 16 112; 3003 tokens x 40 heads of 96, fp32: two full waves left 26, half
-  // a wave 18)
   p.hg = 1;
-  while (p.hg < 8 && toks * p.H * units / (2 * p.hg) >= 1024 * (int64_t)sm_count()) p.hg *= 2;
-  const int groups = (p.H + p.hg - 1) / p.hg;
-  p.units.set(units);
-  p.groups.set(groups);
-  p.N.set(N);
-  if (toks * groups * units > (1 << 30))
+  p.copy_step = 0;
+  const int64_t sms = sm_count();
+  int64_t items;
+  if (vec) {
+    p.turning = rope->rot / 2 / V;
+    int copying = (d - rope->rot) / V;
+    if (copying % 2 == 0 && copying > 0) {
+      copying /= 2;
+      p.copy_step = copying * V;
+    }
+    const int units = p.turning + copying;
+    // heads of a thread: its sines cost about as much as four heads' rows, so as many as
+    // leave half of the GPU's threads (32768 tokens x 40 heads of 128: one head a thread 222
+    // us, 8 110, 16 112; 3003 tokens x 40 heads of 96, fp32: two full waves left 26, half
+    // a wave 18)
+    while (p.hg < 8 && toks * p.H * units / (2 * p.hg) >= 1024 * sms) p.hg *= 2;
+    p.units.set(units);
+    items = toks * ((p.H + p.hg - 1) / p.hg) * units;
+  } else {  // a warp for some heads of a token; likewise
+    p.turning = (rope->rot + V - 1) / V;
+    p.units.set(d / V);
+    while (p.hg < 16 && toks * p.H / (2 * p.hg) >= 32 * sms) p.hg *= 2;
+    items = toks * ((p.H + p.hg - 1) / p.hg);
+  }
+  if (items > (1 << 30) || d / V > (1 << 20))
     return fail(IHA_ERR_UNSUPPORTED, "%s: too many rows in one call", name);
-  p.items = (int)(toks * groups * units);
-  const unsigned blocks = (unsigned)((p.items + kRopeThreads - 1) / kRopeThreads);
+  p.groups.set((p.H + p.hg - 1) / p.hg);
+  p.N.set(N);
+  p.items = (int)items;
+  const int per = vec ? kRopeThreads : kRopeThreads / 32;  // items of a CTA
+  const unsigned blocks = (unsigned)((p.items + per - 1) / per);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dt == IHA_BF16) {
     if (rope->interleaved)
