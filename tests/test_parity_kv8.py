@@ -549,6 +549,43 @@ def test_weights_of_a_table_far_wider_than_its_sequences(T):
         np.testing.assert_array_equal(g[b, :, n:], w0[b, :, n:])
 
 
+def test_a_cache_off_128_bytes_and_a_workspace_of_both_caches(T):
+    """A cache that starts on 16 bytes only gives the same bits; one workspace serves the
+    attentions over both caches, one after the other."""
+    import torch
+    lens, H, d, page = [100, 33], 2, 96, 48
+    cache, table, sl, ks, vs, free = build(T, lens, H, d, page, 145, spare=6)
+    moved = torch.empty(cache.numel() + 16, dtype=torch.uint8, device="cuda")[16:].view(cache.shape)
+    moved.copy_(cache)
+    q = to_dev(S.normal((2, 2, 4, d), 146, 0))
+    w = torch.rand((2, H, table.shape[1] * page), device="cuda")
+    a = T.mha_fwd_kv8(q, cache, table, sl, H, page, weights=w, return_lse=True)
+    b = T.mha_fwd_kv8(q, moved, table, sl, H, page, weights=w, return_lse=True)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    dest = ints([free[:3].tolist(), free[3:6].tolist()])
+    for c in (cache, moved):
+        T.kv8_evict(c, table, sl, w, dest, H, d, page, 40, 5)
+        T.kv8_append(q[:, :, :H].contiguous(), q[:, :, 2:], dest, ints([42, 35]), c, page)
+    assert torch.equal(*(T.kv8_load(c, ints([[i * page + j for j in range(42)] for i in
+                                             (dest[0, 0].item(), dest[1, 0].item())]), H, d,
+                                    page)[0] for c in (cache, moved)))
+    k4 = torch.zeros((8, T.kv4_page_bytes(page, H, d)), dtype=torch.uint8, device="cuda")
+    slots = torch.arange(100, dtype=torch.int32, device="cuda")[None]
+    kv = [to_dev(rows((1, 100, H, d), 147 + i)) for i in range(2)]
+    T.kv4_store(*kv, slots, k4, page)
+    t4, l4 = ints([[0, 1, 2]]), ints([100])
+    ref = T.mha_fwd_kv4(q[:1], k4, t4, l4, H, page)
+    ws = torch.zeros(max(T.mha_fwd_kv8_workspace_bytes(2, 2, 4, H, d, w.shape[2]),
+                         T.mha_fwd_kv4_workspace_bytes(1, 2, 4, H, d)), dtype=torch.uint8,
+                     device="cuda")
+    cache, table, sl, *_ = build(T, lens, H, d, page, 145)
+    for _ in range(3):
+        c = T.mha_fwd_kv8(q, cache, table, sl, H, page, weights=w, return_lse=True, workspace=ws)
+        assert all(torch.equal(x, y) for x, y in zip(a, c))
+        assert torch.equal(T.mha_fwd_kv4(q[:1], k4, t4, l4, H, page, workspace=ws), ref)
+    assert T.device_error() == 0
+
+
 def test_two_calls_at_once(T):
     """Two streams, a workspace each, in flight together; then each on its own."""
     import torch
