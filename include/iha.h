@@ -551,7 +551,7 @@ iha_status mha_fwd_kv8(const void* q, const void* cache, const int32_t* block_ta
  *   kept         int32 [B, Hkv, keep], written: positions of the kept keys, then -1
  *   weights_out  nullable; float32 [B, Hkv, dest_width * page], written: their weights
  *                (-0 as 0), then 0
- * 0 <= recent <= keep, dest_width * page >= min(keep, table_width * page).  Afterwards
+ * 0 <= recent <= keep <= 2^30, dest_width * page >= min(keep, table_width * page).  Afterwards
  * keys sit at other distances than their tokens: attend with IHA_MASK_CAUSAL or
  * IHA_MASK_NONE.  A page id outside the cache leaves its rows zero or unwritten (flagged).
  */

@@ -34,7 +34,7 @@ struct EvictParams {
   int B, H, n_pages, page, table_w, dest_w, keep, recent;
   Kv8Pages pages;
   int64_t cap, dest_cap;
-  FastDiv blocks, heads;  // copy: blocks of keep rows; heads
+  FastDiv blocks, heads;  // copy: blocks that a head can fill; heads
   int64_t items;
 };
 
@@ -413,7 +413,10 @@ iha_status kv8_evict(void* cache, const int32_t* block_table, const int32_t* seq
   const int64_t cap = (int64_t)table_width * page, dest_cap = (int64_t)dest_width * page;
   if (cap > (1 << 30) || dest_cap > (1 << 30))
     return fail(IHA_ERR_UNSUPPORTED, "%s: block table longer than 2^30 tokens", name);
-  if (dest_cap < (keep < cap ? keep : cap))
+  if (keep > (1 << 30))  // (places of the list are counted in 32 bits)
+    return fail(IHA_ERR_UNSUPPORTED, "%s: keep %d is more than 2^30", name, keep);
+  const int64_t most = keep < cap ? keep : cap;  // keys that a head can have afterwards
+  if (dest_cap < most)
     return fail(IHA_ERR_INVALID_ARG, "%s: dest_table holds %lld tokens, keep is %d", name,
                 (long long)dest_cap, keep);
   if ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(seq_lens) |
@@ -422,7 +425,7 @@ iha_status kv8_evict(void* cache, const int32_t* block_table, const int32_t* seq
        reinterpret_cast<uintptr_t>(weights_out)) & 3)
     return fail(IHA_ERR_ALIGNMENT, "%s: tables, lengths, ids and weights must be 4-byte aligned",
                 name);
-  const int64_t planes = (int64_t)B * Hkv, blocks = ((int64_t)keep + kKv8Tok - 1) / kKv8Tok;
+  const int64_t planes = (int64_t)B * Hkv, blocks = (most + kKv8Tok - 1) / kKv8Tok;
   if (planes > (1 << 26) || planes * blocks > INT32_MAX)
     return fail(IHA_ERR_UNSUPPORTED, "%s: more than 2^26 heads or 2^31 - 1 blocks in one call",
                 name);
