@@ -519,6 +519,7 @@ iha_status kv8_load(const void* cache, const int32_t* slots, void* k, void* v, i
  *                              softmax_j(scale <q[b, t, .], k_j>),
  *                where key j is visible, else weights[b, h, j].  They may be the same
  *                array.  Needs Nq * Hq / Hkv <= 64; new keys usually start at 0.
+ *                A call that gave up (device error 2) leaves weights_out unwritten.
  *   workspace    of mha_fwd_kv8_workspace_bytes() bytes, weight_keys = table_width * page
  *                for a call with weights, else 0; zeroed and shared like mha_fwd_kv4's
  *                (one workspace serves calls of both, one after the other)
@@ -616,9 +617,9 @@ iha_status mu_attention_fused(const void* x, const int32_t* keep, void* canvas, 
  * The launch then takes its abort path: the waiting role raises the block's
  * abort flag, the others unwind, copies in flight land, the MMAs drain,
  * tensor memory is released, and the kernel returns with device error 2
- * (iha_device_error); rows that CTA 0 had a part in are left unwritten.  The GPU
- * context stays usable and the next launch runs normally (caches: once its
- * workspace is zeroed again).
+ * (iha_device_error); rows that CTA 0 had a part in are left unwritten, and so is all of
+ * mha_fwd_kv8's weights_out.  The GPU context stays usable and the next launch runs
+ * normally (caches: once its workspace is zeroed again).
  * IHA_ERR_INVALID_ARG for a limit out of range.
  */
 iha_status iha_test_fail_next_wait(int limit_us);

@@ -867,7 +867,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
     }
     if (!ok) {  // a copy never came: report it, let what is in flight land
       *abort_flag = 1;
-      if (lane == 0) atomicOr(&g_dev_error, DEV_ERR_WAIT_TIMEOUT);
+      if (lane == 0) {
+        atomicOr(&g_dev_error, DEV_ERR_WAIT_TIMEOUT);
+        p.counters[kGaveUp] = 1u;  // the weights' kernel then leaves them alone
+      }
       ring.drain(p);
     }
   }
@@ -910,6 +913,8 @@ __global__ void __launch_bounds__(kWeighKeys / 4) kv8_weigh_kernel(const WeighPa
   const int64_t first = (int64_t)chunk * kWeighKeys + 4 * (int)threadIdx.x;
   if (first < end) load(first);
   wait_for_grid();
+  // an attention that gave up left scores and lse unwritten, in all of its units perhaps
+  const bool gave_up = __ldcg(p.a.counters + kGaveUp) != 0u;
   for (int64_t j64 = first; j64 < end; j64 += (int64_t)p.chunks * kWeighKeys) {
     const int j = (int)j64;
     if (j64 != first) load(j64);
@@ -929,6 +934,7 @@ __global__ void __launch_bounds__(kWeighKeys / 4) kv8_weigh_kernel(const WeighPa
       for (int i = 0; i < 4; ++i)  // outside [lo, hi) the score may be anything
         if (j + i >= lo && j + i < hi && x[i] != -INFINITY) sum[i] += exp2f(x[i] - lse);
     }
+    if (gave_up) return;
     float* to = p.out + plane * p.cap + j;
     if (VEC) {
       *reinterpret_cast<float4*>(to) =

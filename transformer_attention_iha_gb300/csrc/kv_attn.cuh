@@ -30,7 +30,11 @@ constexpr int kUnitCost = IHA_KV_UNIT_COST;
 // than they save (777 keys x 80 heads: 3 12.0 us, 4 11.6, 6 12.8).
 constexpr int kMinShare = 4;
 constexpr int kMaxCtas = 480;  // counters for 152 SMs x 3 CTAs and some
-constexpr int kCounterBytes = kMaxCtas * 4;
+// The word behind the counters: not 0 once a wait has given up (written for 8 bits).  With it
+// they end on a line.
+constexpr int kGaveUp = kMaxCtas;
+constexpr int kCounterBytes = 2048;
+static_assert((kGaveUp + 1) * 4 <= kCounterBytes, "the workspace's first words");
 // Parts a CTA may leave in the workspace: of the unit it begins in and the one it
 // ends in; and of the unit each of its warps begins in, for the CTA itself.
 constexpr int kCtaParts = 2 + kWarps;
@@ -42,7 +46,7 @@ struct KvAttnParams {
   const int32_t* lens;
   __nv_bfloat16* o;
   float* lse;
-  unsigned* counters;  // [kMaxCtas], zero between calls
+  unsigned* counters;  // [kMaxCtas] and the word kGaveUp, zero between calls
   float* parts;        // [CTAs][kCtaParts][part_stride]
   int part_cols, part_stride;
   int B, Nq, Hq, Hkv, G, ncols, ncb;  // ncols = Nq * G columns of a key-value head, in ncb blocks
@@ -401,7 +405,7 @@ iha_status kv_attn_setup(const char* name, KvAttnParams& p, int& nt, int& grid,
   p.ncb = (int)ncb;
   p.inv_g = ((1ull << 32) + G - 1) / G;
   p.counters = static_cast<unsigned*>(workspace);
-  p.parts = reinterpret_cast<float*>(p.counters + kMaxCtas);
+  p.parts = reinterpret_cast<float*>(p.counters + kCounterBytes / 4);
   p.part_cols = part_cols(ncols);
   p.part_stride = part_stride(ncols, d);
   p.n_pages = n_pages;
