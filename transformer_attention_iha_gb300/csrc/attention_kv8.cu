@@ -19,7 +19,7 @@
 //     its P s exactly); then O and the sum are rescaled.
 // Work: the line of kv_attn.cuh; each warp keeps a ring of two stages of two blocks (d =
 // 128) that bulk copies fill ahead, codes and tails apart.  Calls with weights keep the scores
-// (4 bytes where K and V have 2 d), and a second kernel adds exp(score - lse) up.
+// (4 bytes where K and V have 2 d), and a second kernel adds 2^(score - reference) / l up.
 //
 // What bounds it: long contexts HBM (131071 keys x 80 heads of 128, 2.69 GB: 401 to 411 us,
 // 6.5 to 6.7 TB/s; 137 registers, 12 warps an SM, 34 per cent of the issue slots); there the
@@ -43,9 +43,24 @@ constexpr int NB = 2;  // blocks computed together
 constexpr float kTopF = 8.5070591730234616e37f;
 constexpr int kTopFExp = 126 + 127;
 
+// What is written of a row besides O.  A function that is called: in the body of the joins,
+// four rows unrolled, it cost 16-column calls 1.2 of 32 us.
+__device__ __noinline__ void write_row_stats(float* lse, float2* rows, int64_t row, float ref,
+                                             float l, float inv) {
+  if (lse != nullptr) lse[row] = lse_of(ref, l);
+  if (rows != nullptr) rows[row] = make_float2(ref, inv);
+}
+
 struct Kv8AttnParams : KvAttnParams {
   Kv8Pages pages;
   float* scores;  // nullable: [B, Hkv, ncols, table_w * page], log2 domain, -inf where hidden
+  // with scores: each row's reference (log2 domain) and 1 / l.  (Not its lse: a sum of both
+  // in fp32, let alone turned to natural logarithms and back, is off by 2^-24 of its size, and
+  // so are all weights of the row: 1e-4 of themselves for scores about 1000.)
+  float2* rows;
+  __device__ __forceinline__ void write_row(int64_t row, float ref, float l, float inv) const {
+    write_row_stats(lse, rows, row, ref, l, inv);
+  }
 };
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
@@ -617,7 +632,7 @@ __device__ __forceinline__ void note_span(LineSmem& sm, const Unit& u, int warp,
 // join_ctas for units of many columns: I items of a thread, U parts of each, on their way
 // together (a join waits for memory: 16 columns of 128 features, 7 parts, ...).
 template <int D, int COLS>
-__device__ __forceinline__ void join_wide(const KvAttnParams& p, const int* span, const int* of,
+__device__ __forceinline__ void join_wide(const Kv8AttnParams& p, const int* span, const int* of,
                                           float* scratch) {
   const int c_first = span[2] * COLS, first = of[0], last = of[1];
   const int items = min(COLS, p.ncols - c_first) * (D / 4);
@@ -660,7 +675,7 @@ __device__ __forceinline__ void join_wide(const KvAttnParams& p, const int* span
 // them in the CTA that arrives last (all threads call).  head_of, tail_of: a warp's part
 // of a unit that ends in its stretch after beginning before it, and of one that goes on.
 template <int D, int COLS, typename Head, typename Tail>
-__device__ __forceinline__ void join_units(const KvAttnParams& p, LineSmem& sm, Head head_of,
+__device__ __forceinline__ void join_units(const Kv8AttnParams& p, LineSmem& sm, Head head_of,
                                            Tail tail_of, float* cta_parts, float* scratch) {
   const int tid = threadIdx.x;
   __syncthreads();
@@ -881,6 +896,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
 struct WeighParams {
   KvAttnParams a;
   const float *scores, *weights;
+  const float2* rows;
   float* out;
   int64_t cap;
   int chunks;  // CTAs of a head
@@ -888,7 +904,7 @@ struct WeighParams {
 
 constexpr int kWeighKeys = 1024;  // keys that a CTA takes at a time
 
-// out[b, h, j] = weights[b, h, j] + the sum over columns of exp(score - lse), four
+// out[b, h, j] = weights[b, h, j] + the sum over columns of 2^(score - reference) / l, four
 // neighbouring keys a thread (VEC: as vectors).  Launched behind the attention: the first
 // weights are on their way while that ends.  (1 token over 4 ragged sequences of up to
 // 32768 keys x 20 heads: 5 to 8 us behind the attention's 74.)
@@ -913,7 +929,7 @@ __global__ void __launch_bounds__(kWeighKeys / 4) kv8_weigh_kernel(const WeighPa
   const int64_t first = (int64_t)chunk * kWeighKeys + 4 * (int)threadIdx.x;
   if (first < end) load(first);
   wait_for_grid();
-  // an attention that gave up left scores and lse unwritten, in all of its units perhaps
+  // an attention that gave up left scores and rows unwritten, in all of its units perhaps
   const bool gave_up = __ldcg(p.a.counters + kGaveUp) != 0u;
   for (int64_t j64 = first; j64 < end; j64 += (int64_t)p.chunks * kWeighKeys) {
     const int j = (int)j64;
@@ -924,15 +940,16 @@ __global__ void __launch_bounds__(kWeighKeys / 4) kv8_weigh_kernel(const WeighPa
       col_range(p.a, len, col, lo, hi);
       if (j + 4 <= lo || j >= hi) continue;
       const int qi = token_of(p.a, col), qh = hk * p.a.G + (col - qi * p.a.G);
-      // (scores and lse: not through the read-only path)
+      // (scores, references and 1 / l: not through the read-only path)
       const float4 v = __ldcg(reinterpret_cast<const float4*>(
           p.scores + (plane * (int64_t)p.a.ncols + col) * p.cap + j));
       const float x[4] = {v.x, v.y, v.z, v.w};
-      const float lse =
-          __ldcg(p.a.lse + ((int64_t)b * p.a.Hq + qh) * p.a.Nq + qi) * 1.4426950408889634f;
+      const int64_t row = ((int64_t)b * p.a.Hq + qh) * p.a.Nq + qi;
+      const float2 r = __ldcg(p.rows + row);
 #pragma unroll
       for (int i = 0; i < 4; ++i)  // outside [lo, hi) the score may be anything
-        if (j + i >= lo && j + i < hi && x[i] != -INFINITY) sum[i] += exp2f(x[i] - lse);
+        if (j + i >= lo && j + i < hi && x[i] != -INFINITY)
+          sum[i] += exp2f(x[i] - r.x) * r.y;
     }
     if (gave_up) return;
     float* to = p.out + plane * p.cap + j;
@@ -971,7 +988,7 @@ size_t part_bytes(int64_t ncols, int d) {
   return (size_t)ctas * kCtaParts * part_stride(ncols, d) * sizeof(float);
 }
 
-size_t lse_floats(int B, int Hq, int Nq) {  // what follows starts on 16 bytes
+size_t row_floats(int B, int Hq, int Nq) {  // one a row; what follows starts on 16 bytes
   return ((size_t)B * Hq * Nq + 3) & ~(size_t)3;
 }
 
@@ -985,10 +1002,13 @@ extern "C" {
 size_t mha_fwd_kv8_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, int weight_keys) {
   if (B <= 0 || Nq <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv || d <= 0 || weight_keys < 0) return 0;
   const int64_t ncols = (int64_t)Nq * (Hq / Hkv);
-  size_t n = iha::kCounterBytes + iha::part_bytes(ncols, d);
+  // counters, parts; with weights two floats a row (one of them counts without weights
+  // too), the rows' scores
+  size_t n = iha::kCounterBytes + iha::part_bytes(ncols, d) +
+             iha::row_floats(B, Hq, Nq) * sizeof(float);
   if (weight_keys > 0 && (double)B * Hkv * ncols * weight_keys > 1e15) return 0;  // no such
-  if (weight_keys > 0)  // the rows' lse, their scores
-    n += (iha::lse_floats(B, Hq, Nq) + (size_t)B * Hkv * ncols * weight_keys) * sizeof(float);
+  if (weight_keys > 0)
+    n += (iha::row_floats(B, Hq, Nq) + (size_t)B * Hkv * ncols * weight_keys) * sizeof(float);
   return n;
 }
 
@@ -1016,6 +1036,7 @@ iha_status mha_fwd_kv8(const void* q, const void* cache, const int32_t* block_ta
   if (st != IHA_OK) return st;
   p.pages.set(page, Hkv, d);
   p.scores = nullptr;
+  p.rows = nullptr;
   if (weights) {
     if (p.ncols > kMaxWeighed)
       return fail(IHA_ERR_UNSUPPORTED, "%s: weights of more than %d rows of a key head", name,
@@ -1040,8 +1061,8 @@ iha_status mha_fwd_kv8(const void* q, const void* cache, const int32_t* block_ta
       return fail(IHA_ERR_INVALID_ARG, "%s: weights overlap another tensor", name);
     float* own = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterBytes +
                                           part_bytes(p.ncols, d));
-    if (!p.lse) p.lse = own;
-    p.scores = own + lse_floats(B, Hq, Nq);
+    p.rows = reinterpret_cast<float2*>(own);
+    p.scores = own + 2 * row_floats(B, Hq, Nq);
   }
   p.wait_ns = wait_limit_for_next_launch();
   p.withhold = withhold_for_this_launch() ? 1 : 0;
@@ -1052,7 +1073,8 @@ iha_status mha_fwd_kv8(const void* q, const void* cache, const int32_t* block_ta
   // far wider than the sequences)
   const int64_t all = (cap + kWeighKeys - 1) / kWeighKeys;
   const int64_t fill = (8 * (int64_t)sm_count() + (int64_t)B * Hkv - 1) / ((int64_t)B * Hkv);
-  const WeighParams w = {p, p.scores, weights, weights_out, cap, (int)(all < fill ? all : fill)};
+  const WeighParams w = {p,           p.scores, weights, p.rows,
+                         weights_out, cap,      (int)(all < fill ? all : fill)};
   const unsigned ctas = (unsigned)(B * Hkv * w.chunks);
   return launch_behind(name, aligned16(weights) && aligned16(weights_out) ? kv8_weigh_kernel<true>
                                                                           : kv8_weigh_kernel<false>,

@@ -57,6 +57,7 @@ struct KvAttnParams {
   iha_strides sq, so;
   uint64_t wait_ns;
   int withhold;  // failure-path test: the first stage of CTA 0's warps never completes
+  __device__ __forceinline__ void write_row(int64_t row, float ref, float l, float inv) const;
 };
 
 // d = a b + c on fp16 or bf16 operands, fp32 accumulators.
@@ -100,30 +101,34 @@ __device__ __forceinline__ int token_of(const KvAttnParams& p, int col) {
   return (int)((unsigned long long)(unsigned)col * p.inv_g >> 32);
 }
 
-// Four features of one output row: O / l, and with the first four the row's lse.
-__device__ __forceinline__ void write_out(const KvAttnParams& p, int b, int hk, int col, int f,
-                                          float4 o, float ref, float l) {
+// A row's lse (natural logarithm) from its reference and sum.
+__device__ __forceinline__ float lse_of(float ref, float l) {
+  return l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+}
+__device__ __forceinline__ void KvAttnParams::write_row(int64_t row, float ref, float l,
+                                                        float) const {
+  if (lse) lse[row] = lse_of(ref, l);
+}
+// Features of one output row, O / l; with the first ones what is written of the row besides.
+template <typename P>
+__device__ __forceinline__ void write_out(const P& p, int b, int hk, int col, int f, float4 o,
+                                          float ref, float l) {
   const int qi = token_of(p, col), qh = hk * p.G + (col - qi * p.G);
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint2 u;
   u.x = pack_bf16x2(o.x * inv, o.y * inv);
   u.y = pack_bf16x2(o.z * inv, o.w * inv);
   *reinterpret_cast<uint2*>(p.o + b * p.so.b_outer + qi * p.so.seq + qh * p.so.head + f) = u;
-  if (p.lse && f == 0)
-    p.lse[((int64_t)b * p.Hq + qh) * p.Nq + qi] =
-        l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+  if (f == 0) p.write_row(((int64_t)b * p.Hq + qh) * p.Nq + qi, ref, l, inv);
 }
-
-// Two features of it.
-__device__ __forceinline__ void write_out(const KvAttnParams& p, int b, int hk, int col, int f,
-                                          float2 o, float ref, float l) {
+template <typename P>
+__device__ __forceinline__ void write_out(const P& p, int b, int hk, int col, int f, float2 o,
+                                          float ref, float l) {
   const int qi = token_of(p, col), qh = hk * p.G + (col - qi * p.G);
   const float inv = l == 0.f ? 0.f : 1.f / l;
   *reinterpret_cast<uint32_t*>(p.o + b * p.so.b_outer + qi * p.so.seq + qh * p.so.head + f) =
       pack_bf16x2(o.x * inv, o.y * inv);
-  if (p.lse && f == 0)
-    p.lse[((int64_t)b * p.Hq + qh) * p.Nq + qi] =
-        l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+  if (f == 0) p.write_row(((int64_t)b * p.Hq + qh) * p.Nq + qi, ref, l, inv);
 }
 
 // Visible keys [lo, hi) of column col of a sequence of len keys.
@@ -227,16 +232,16 @@ struct Joined {
       o.w = fmaf(po[k].w, c, o.w);
     }
   }
-  __device__ __forceinline__ void write(const KvAttnParams& p, const int* span, int col,
-                                        int f) const {
+  template <typename P>
+  __device__ __forceinline__ void write(const P& p, const int* span, int col, int f) const {
     write_out(p, span[0], span[1], col, f, o, m == -INFINITY ? 0.f : m, l);
   }
 };
 
 // Joins the parts that CTAs of[0] .. of[1] left of a unit (all threads of the CTA).
-template <int D, int COLS>
-__device__ __forceinline__ void join_ctas(const KvAttnParams& p, const int* span,
-                                          const int* of, float* scratch) {
+template <int D, int COLS, typename P>
+__device__ __forceinline__ void join_ctas(const P& p, const int* span, const int* of,
+                                          float* scratch) {
   const int c_first = span[2] * COLS, first = of[0], last = of[1];
   const int ncolv = min(COLS, p.ncols - c_first), items = ncolv * (D / 4);
   // few items: several threads share one, each taking every groups-th part
