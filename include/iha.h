@@ -181,7 +181,7 @@ typedef struct {
   double fast, slow;   /* PARTS: 0 <= slow < fast, usually 32 and 1 */
   double gain;         /* 0: 1, with PARTS 0.1 ln f + 1 */
   /* set by iha_rope_init */
-  uint64_t turn[128];  /* 2^-64 turns of pair i per position */
+  uint64_t turn[128];  /* 2^-64 turns of pair i per position, rounded */
   float mul;           /* the gain */
   int32_t unused;
 } iha_rope;
@@ -199,8 +199,8 @@ iha_status iha_rope_init(iha_rope* rope);
  *   rope       host memory, from iha_rope_init; copied before the call returns
  * yq may be q itself (same pointer and strides: in place), yk may be k; else no row of
  * an output may lie on a row of an input or of another output.
- * d a multiple of 16 bytes, rot <= d.  Angles are exact modulo a turn to 2^-32 turns
- * wherever the position, sines and cosines good to about 2^-23, products in fp32.
+ * d a multiple of 16 bytes, rot <= d.  Angles modulo a turn are within 2^-31 turns at any
+ * position, sines and cosines good to about 2^-23, products in fp32.
  */
 iha_status iha_rope_fwd(const void* q, const void* k, const int32_t* positions, void* yq,
                         void* yk, const iha_rope* rope, int B, int N, int Hq, int Hk, int d,

@@ -9,7 +9,7 @@
 // Angles: a pair's frequency is held as turns per position in 64-bit fixed point,
 // turn = w / 2 pi * 2^64 mod 2^64, so position * turn in 64-bit integers is the angle
 // in turns modulo 1 for any position, without the loss of a 32-bit product (position
-// 2^20 in fp32 is off by 2^-4 radians).  Of its upper 32 bits the nearest quarter of a turn
+// 2^20 in fp32 is off by 2^-4 radians).  The table is right to its last bit.  Of its upper 32 bits the nearest quarter of a turn
 // is taken off, the rest goes through sincospif: off by about 2^-24 in all.
 //
 // A thread takes 32 bytes of a row, 8 pairs of bf16 or 4 of fp32, works out their
@@ -383,6 +383,46 @@ iha_status rotate(const char* name, bool back, const void* q, const void* k,
   return check_launch(name);
 }
 
+// ---- the table.  A turn is fixed to 2^-64, and far positions take up all of its bits (53 of
+// them, a double's, leave 2^-25 turns at position 2^31), so it is worked out on sums of two
+// doubles, some 104 bits: Knuth's and Dekker's sums and products without error, a product's
+// rest by fma.  (Where a compiler joins a product and a sum, bits only move between hi and lo.)
+struct Pair {
+  double hi, lo;
+};
+Pair two_sum(double a, double b) {
+  const double s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+Pair operator+(Pair a, Pair b) {
+  const Pair s = two_sum(a.hi, b.hi), t = two_sum(a.lo, b.lo);
+  const Pair u = two_sum(s.hi, s.lo + t.hi);
+  return two_sum(u.hi, u.lo + t.lo);
+}
+Pair operator-(Pair a, Pair b) { return a + Pair{-b.hi, -b.lo}; }
+Pair operator*(Pair a, Pair b) {
+  const double p = a.hi * b.hi;
+  return two_sum(p, fma(a.hi, b.lo, fma(a.lo, b.hi, fma(a.hi, b.hi, -p))));
+}
+Pair operator/(Pair a, Pair b) {
+  const double q = a.hi / b.hi;
+  const Pair r = a - Pair{q, 0.0} * b;
+  const double q2 = r.hi / b.hi;
+  const Pair r2 = r - Pair{q2, 0.0} * b;
+  return two_sum(q, q2) + Pair{r2.hi / b.hi, 0.0};
+}
+// x^(-1 / n), 1 <= n < 2^7: a double's root and a step of Newton's method; x is brought to
+// below 2^n, so that no power leaves its range.
+Pair inverse_root(double x, int n) {
+  const int k = ilogb(x) / n;
+  const double m = ldexp(x, -n * k), y = pow(m, 1.0 / n);
+  Pair p = {y, 0.0};  // y^n
+  for (int i = 1; i < n; ++i) p = p * Pair{y, 0.0};
+  const Pair rest = Pair{m, 0.0} - p;
+  const Pair root = two_sum(y, y * (rest.hi / p.hi / n));
+  return Pair{ldexp(1.0, -k), 0.0} / root;
+}
+
 }  // namespace
 }  // namespace iha
 
@@ -412,17 +452,24 @@ iha_status iha_rope_init(iha_rope* r) {
   if (r->scaling == IHA_ROPE_PARTS &&
       (r->trained < 1 || !(r->slow >= 0.0) || !(r->fast > r->slow) || !isfinite(r->fast)))
     return fail(IHA_ERR_INVALID_ARG, "%s: parts needs trained >= 1 and 0 <= slow < fast", name);
-  const double two_pi = 6.283185307179586476925;
-  double base = r->base;
-  if (r->scaling == IHA_ROPE_BASE) base *= pow(f, r->rot / (r->rot - 2.0));
-  for (int i = 0; i < r->rot / 2; ++i) {
-    double turns = pow(base, -2.0 * i / r->rot) / two_pi;  // per position, below 1 / 6
-    if (r->scaling == IHA_ROPE_LINEAR) turns /= f;
+  const Pair per_turn = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};  // 1 / 2 pi
+  const Pair one = {1.0, 0.0}, zero = {0.0, 0.0}, by = {f, 0.0};
+  // base^(-2 i / rot), with a scaled base times f^(-2 i / (rot - 2))
+  Pair ratio = inverse_root(r->base, r->rot / 2), turns = per_turn;
+  if (r->scaling == IHA_ROPE_BASE) ratio = ratio * inverse_root(f, r->rot / 2 - 1);
+  for (int i = 0; i < r->rot / 2; ++i, turns = turns * ratio) {
+    Pair t = turns;  // per position, below 1 / 6
+    if (r->scaling == IHA_ROPE_LINEAR) t = t / by;
     if (r->scaling == IHA_ROPE_PARTS) {
-      const double g = fmin(1.0, fmax(0.0, (r->trained * turns - r->slow) / (r->fast - r->slow)));
-      turns *= g + (1.0 - g) / f;
+      Pair g = (Pair{(double)r->trained, 0.0} * t - Pair{r->slow, 0.0}) /
+               two_sum(r->fast, -r->slow);
+      if (g.hi < 0.0) g = zero;
+      if (g.hi >= 1.0) g = one;
+      t = t * (g + (one - g) / by);
     }
-    r->turn[i] = (uint64_t)(turns * 18446744073709551616.0);
+    const double hi = ldexp(t.hi, 64), whole = floor(hi);
+    const double rest = floor((hi - whole) + ldexp(t.lo, 64) + 0.5);
+    r->turn[i] = (uint64_t)((int64_t)whole + (int64_t)rest);
   }
   r->mul = (float)(r->gain > 0.0 ? r->gain
                                  : r->scaling == IHA_ROPE_PARTS ? 0.1 * log(f) + 1.0 : 1.0);
