@@ -491,6 +491,9 @@ size_t kv8_page_bytes(int page, int Hkv, int d);  /* 0 for sizes it cannot hold 
  * A block that has keys before its first new row keeps them: its scales become the
  * larger of what they were and what the new rows need, and where one grows the
  * codes that are there are rounded again (exact but for codes that become subnormal).
+ * A scale never falls while its block goes on: where a length goes back (drafted tokens that
+ * were rejected) and rows are added again, the block keeps the scale that the rejected rows
+ * made necessary, and small values of its other rows stay as coarse as that made them.
  * (Such keys are those of earlier calls: in a page that was never written a sequence
  * starts at a multiple of 16.)
  * A block whose first row is new starts afresh, its rows behind the last key become
@@ -503,8 +506,9 @@ iha_status kv8_append(const void* k, const void* v, const int32_t* block_table,
                       iha_strides sv, iha_dtype dt, void* stream);
 
 /*
- * Read rows back by their slots, s * c exactly in f32 or rounded to bf16 (exact too,
- * unless it overflows); arguments, padding and checks as kv4_load.
+ * Read rows back by their slots, s * c exactly in f32 or bf16 (infinite where it is 2^128:
+ * values from 1.9375 * 2^127 on are rounded to that); arguments, padding and checks as
+ * kv4_load.
  */
 iha_status kv8_load(const void* cache, const int32_t* slots, void* k, void* v, int B_outer,
                     int B_inner, int N, int n_pages, int page, int Hkv, int d, iha_strides sk,
@@ -518,15 +522,16 @@ iha_status kv8_load(const void* cache, const int32_t* slots, void* k, void* v, i
  *       weights_out[b, h, j] = weights[b, h, j] + sum over t and the query heads of h of
  *                              softmax_j(scale <q[b, t, .], k_j>),
  *                where key j is visible, else weights[b, h, j].  They may be the same
- *                array.  Needs Nq * Hq / Hkv <= 64; new keys usually start at 0.
+ *                array.  Needs Nq * Hq / Hkv <= 64; new keys usually start at 0
+ *                (also where they take the places of rejected ones, whose weight stays).
  *                A call that gave up (device error 2) leaves weights_out unwritten.
  *   workspace    of mha_fwd_kv8_workspace_bytes() bytes, weight_keys = table_width * page
  *                for a call with weights, else 0; zeroed and shared like mha_fwd_kv4's
  *                (one workspace serves calls of both, one after the other)
  * Accuracy: scores, sums, weights and O are held in fp32, codes enter exactly, q with its
  * 8-bit mantissas (features below 2^-28 of a row's largest lose bits); p times V's scale
- * is rounded to fp16, 2^-11 of a term.  o is rounded to bf16.  |q| * |k| * scale has to
- * stay within fp32.  The result does not depend on timing.
+ * is rounded to fp16, 2^-11 of a term.  o is rounded to bf16.  The weights of a row add up
+ * to 1 within about 2^-17, whatever the scores.  |q| * |k| * scale has to stay within fp32.  The result does not depend on timing.
  */
 size_t mha_fwd_kv8_workspace_bytes(int B, int Nq, int Hq, int Hkv, int d, int weight_keys);
 iha_status mha_fwd_kv8(const void* q, const void* cache, const int32_t* block_table,
@@ -551,7 +556,7 @@ iha_status mha_fwd_kv8(const void* q, const void* cache, const int32_t* block_ta
  *   new_lens     int32 [B], written: min(n, keep)
  *   kept         int32 [B, Hkv, keep], written: positions of the kept keys, then -1
  *   weights_out  nullable; float32 [B, Hkv, dest_width * page], written: their weights
- *                (-0 as 0), then 0
+ *                (-0 perhaps as 0), then 0
  * 0 <= recent <= keep <= 2^30, dest_width * page >= min(keep, table_width * page).  Afterwards
  * keys sit at other distances than their tokens: attend with IHA_MASK_CAUSAL or
  * IHA_MASK_NONE.  A page id outside the cache leaves its rows zero or unwritten (flagged).

@@ -11,8 +11,11 @@
 // Load: a thread writes two vectors of 16 bytes of a K row and of a V row.
 //
 // Both move bytes, and are bound by HBM: a token and head of d features is 4 d bytes of
-// bf16 and 2 d + 1 of cache.  8192 tokens x 80 heads of 128, 504 MB: append 74.5 us, 6.8
-// TB/s, load 74.5 us, in random order 77; one row of 32 sequences: latency, 3.5 us and 2.3.
+// bf16 and 2 d + 1 of cache.  8192 tokens x 80 heads of 128, 504 MB, replayed from a graph:
+// append 73 us, load 74, in random order 77 (6.5 to 6.9 TB/s; the last writes are still in
+// L2 then), launched one by one 77; as many bytes of d = 64: 74, 75 and 97, of d = 96 (a lane in
+// four idle, rows of two lines) 87, 75 and 93, of d = 32 90, 76 and 128.  One row of 32
+// sequences: latency, 3.5 us and 2.3.
 #include <type_traits>
 
 #include "kv8.cuh"
@@ -22,7 +25,7 @@ namespace {
 
 IHA_DEVICE_ERROR_WORD(kv8_cache)
 
-constexpr int kWarps = 4;  // (8192 tokens x 80 heads: 74.5 us, 8 warps 80)
+constexpr int kWarps = 4;  // (8192 tokens x 80 heads: 73 us, 8 warps 80)
 
 struct AppendParams {
   const void *k, *v;

@@ -11,8 +11,8 @@
 // rows are gathered whole, 16 bytes a lane, and rounded again where their block's scale
 // is not the largest of its sixteen.
 //
-// What bounds it: 32768 keys x 80 heads of 128 to 8192, 353 MB: 79 us (floor 53), select
-// 25, copy 52 behind it.  Select: issue (0.64 a cycle, one CTA a head: 72 of 152 SMs idle),
+// What bounds it: 32768 keys x 80 heads of 128 to 8192, 353 MB, replayed from a graph: 79 us
+// (floor 53; launched one by one 83), select 25, copy 52 behind it.  Select: issue (0.64 a cycle, one CTA a head: 72 of 152 SMs idle),
 // and three phases in lockstep (counts 6 us, list and its digits 6, order 8).  Copy: HBM, by
 // rows of one line each.  Few rows: latency, 4 x 8 heads of 1100 keys 11 us.
 #include "kv8.cuh"

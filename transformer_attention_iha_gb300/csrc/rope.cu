@@ -9,15 +9,17 @@
 // Angles: a pair's frequency is held as turns per position in 64-bit fixed point,
 // turn = w / 2 pi * 2^64 mod 2^64, so position * turn in 64-bit integers is the angle
 // in turns modulo 1 for any position, without the loss of a 32-bit product (position
-// 2^20 in fp32 is off by 2^-4 radians).  The table is right to its last bit.  Of its upper 32 bits the nearest quarter of a turn
-// is taken off, the rest goes through sincospif: off by about 2^-24 in all.
+// 2^20 in fp32 is off by 2^-4 radians).  The table is right to its last bit.  Of the product's
+// upper 32 bits the nearest quarter of a turn is taken off, the rest goes through sincospif:
+// off by about 2^-24 in all.
 //
 // A thread takes 32 bytes of a row, 8 pairs of bf16 or 4 of fp32, works out their
 // sines once and applies them to up to `hg` heads of its token.
 //
 // Bound by HBM: 32768 tokens x 40 heads of 128, bf16, 671 MB: 103 us, 6.5 TB/s (CTAs of
-// 256 threads 110); 8192 x 160 101 us, 6.6; half of each head rotated 5.4.  Halves off 16
-// bytes: 50 of 80 features 2.8, 100 of 128 3.6 (pair by pair from memory 1.8 and 2.3).
+// 256 threads 110), into the same buffers again 99; half of each head rotated 98, 8192 x 160
+// heads 101, 6.6.  Halves off 16 bytes: 50 of 80 features 2.8 to 3.2, 100 of 128 3.9 (pair by
+// pair from memory 1.8 and 2.3).
 #include <math.h>
 
 #include "kv4.cuh"
